@@ -17,8 +17,8 @@ The operators (x, y, o, h in bf16 or half; K = input features):
   block     norm with its h quantized at once, then the gemm of the next layer.
 
 Layout of a quantized [rows, K] tensor: codes uint8 [rows, K/2], the even
-element in the low nibble; scales uint8 [ceil(K/256), rows, 8], the biased
-exponent e + 127 of block 8 t + j of a row at [t, row, j] (0 behind the last).
+element in the low nibble; scales uint8 [ceil(K/256), rows rounded up to 16, 8],
+the biased exponent e + 127 of block 8 t + j of a row at [t, row, j].
 """
 
 import math
@@ -215,9 +215,10 @@ def _plain_quantize(x, rot):
     code = code.reshape(rows, k // 2, 2)
     codes = code[..., 0] | (code[..., 1] << 4)
     tiles = -(-k // 256)
-    scales = torch.zeros(rows, tiles * 8, dtype=torch.uint8, device=x.device)
-    scales[:, : k // 32] = (e + 127).to(torch.uint8)
-    return codes, scales.reshape(rows, tiles, 8).transpose(0, 1).contiguous()
+    padded = -(-rows // 16) * 16
+    scales = torch.zeros(padded, tiles * 8, dtype=torch.uint8, device=x.device)
+    scales[:rows, : k // 32] = (e + 127).to(torch.uint8)
+    return codes, scales.reshape(padded, tiles, 8).transpose(0, 1).contiguous()
 
 
 def _plain_values(codes, scales):
@@ -226,7 +227,7 @@ def _plain_values(codes, scales):
     k = 2 * half
     table = torch.tensor(_MAGS + tuple(-a for a in _MAGS), device=codes.device)
     pair = torch.stack((codes & 15, codes >> 4), -1).reshape(rows, k // 32, 32)
-    e = scales.transpose(0, 1).reshape(rows, -1)[:, : k // 32].int() - 127
+    e = scales[:, :rows].transpose(0, 1).reshape(rows, -1)[:, : k // 32].int() - 127
     return torch.ldexp(table[pair.int()], e[..., None]).reshape(rows, k)
 
 
@@ -379,7 +380,7 @@ def _exact_read(codes, scales):
     s, x, f = c // 8, (c // 2) % 4, (c % 2).double()
     v = torch.where(x == 0, f / 2, torch.exp2(x.double() - 1) * (1 + f / 2))
     t = torch.arange(c.shape[1], device=codes.device) // 32
-    e = scales[t // 8, :, t % 8].t().double() - 127
+    e = scales[t // 8, :rows, t % 8].t().double() - 127
     return (1 - 2 * s) * v * torch.pow(torch.full_like(e, 2.0), e)
 
 
