@@ -397,6 +397,132 @@ size_t convrot_linear_int8_workspace_for_rows(int64_t rows, int64_t k);
  * "Memory"). Returns 0 for invalid dimensions. */
 size_t convrot_linear_int8_workspace_size(int64_t m, int64_t n, int64_t k);
 
+/* ---- Microscaled 4-bit (MXFP4) layers ---------------------------------------
+ *
+ * The same chain as the int8 layer, with both operands of the product in the
+ * OCP microscaling format MXFP4 (E2M1 elements, one E8M0 scale per block of 32
+ * consecutive elements of a row): half the weight bytes and twice the matrix
+ * rate of int8. The rotation R is the int8 layer's (the rotation spreads
+ * outlier channels over their group before quantizing), g = 1 turns it off, so
+ * that an unrotated MXFP4 weight can be used as it is.
+ *
+ * A quantized [rows, k] tensor:
+ *   codes   [rows, k/2] uint8: element 2i in the low, 2i + 1 in the high nibble;
+ *           bit 3 is the sign, bits 0..2 one of 0, 0.5, 1, 1.5, 2, 3, 4, 6;
+ *   scales  [ceil(k/256)][rows rounded up to 16][8] uint8: the byte at
+ *           [t][r][j] is the biased exponent (2^(byte - 127)) of elements
+ *           32 (8t + j) .. + 31 of row r; 255 makes the block NaN. Bytes of
+ *           padding rows are not written and bytes behind the last block of a
+ *           row are written 0; neither is ever used. A row-major [rows, k/32]
+ *           scale tensor (k % 256 == 0) is brought into this order by
+ *           reshaping to [rows, k/256, 8] and swapping the first two axes.
+ *
+ * Numerics:
+ *   quantize: x_r = each rotated element's sum in float64 rounded once to fp32
+ *             (exact sum wherever a group's nonzero magnitudes span at most
+ *             37 binades, and for half inputs always; g = 1: the element);
+ *             e = floor(log2(max|x_r|)) - 2 over the block, at least -127;
+ *             code = x_r / 2^e rounded to nearest, ties to even, at most 6 in
+ *             magnitude; a block of zeros has byte 0. The sign of a zero code
+ *             carries no meaning. A block holding an infinity or a NaN (after
+ *             the rotation, which spreads it over its group) gets byte 255.
+ *   dequant:  W_hat = RN16((v 2^e) . blockdiag(R)^T), sums in fp32.
+ *   gemm:     y = RN16(sum over k in fp32 [+ bias[n] in fp32]); a NaN block makes
+ *             its row (column) of y NaN. Results are bit-identical from run to
+ *             run. The order of the sum depends on whether m <= 64, so a row's
+ *             last bit can differ between calls on either side of that.
+ *   linear:   gemm(quantize(x), w), whatever the slices.
+ *
+ * Shapes: k % 32 == 0, k % g == 0, k <= 131072; n % 16 == 0 for the product;
+ * rows < 2^31. Alignment: 16 bytes (bias 8, workspace 256). The conventions at
+ * the top of this file hold, m == 0 included; dtype is the 16-bit format of x,
+ * bias, y and out. */
+
+/* Bytes of the scales tensor (0 for invalid dimensions). */
+size_t convrot_mx4_scales_size(int64_t rows, int64_t k);
+
+/* Rotate and quantize: a weight [n, k] or activations [m, k].
+ *   x [rows, k] in dtype (in); codes, scales (out) */
+convrot_status convrot_quantize_mx4(const void* x, convrot_dtype dtype, int64_t rows, int64_t k,
+                                    int g, uint64_t rot_seed, uint8_t* codes, uint8_t* scales,
+                                    void* stream);
+
+/* The tensor that codes and scales stand for, rotated back (g = 1: as it is).
+ *   out [rows, k] in out_dtype (out) */
+convrot_status convrot_dequant_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                   int64_t k, int g, uint64_t rot_seed, void* out,
+                                   convrot_dtype out_dtype, void* stream);
+
+/* y [m, n] = x . w^T (+ bias [n], nullable), x [m, k] and w [n, k] quantized.
+ * tile: 0 = automatic; 16, 32 or 64 = the kernel for few rows (m <= tile);
+ * 128, 192, 256 (tile x tile outputs), 384 (384 x 192): a test / tuning hook.
+ * Any other value, or more rows than a few-rows tile holds, is
+ * CONVROT_E_INVALID_ARG. */
+convrot_status convrot_gemm_mx4(const uint8_t* x_codes, const uint8_t* x_scales,
+                                const uint8_t* w_codes, const uint8_t* w_scales,
+                                const void* bias, int64_t m, int64_t n, int64_t k, void* y,
+                                convrot_dtype dtype, int tile, void* stream);
+
+/* The forward of a layer with a quantized weight: per slice of token rows,
+ * quantize into the workspace, then the product. The workspace holds the
+ * slice's codes (rounded up to 256 bytes) followed by its scales; slices are
+ * as large as it allows. */
+convrot_status convrot_linear_mx4(const void* x, const uint8_t* w_codes, const uint8_t* w_scales,
+                                  const void* bias, int64_t m, int64_t n, int64_t k, int g,
+                                  uint64_t rot_seed, void* y, convrot_dtype dtype,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes for slices of `rows` rows, and the default: min(m, 3n) rows,
+ * less than the 16-bit weight that the default path would unpack. 0 for
+ * invalid dimensions. */
+size_t convrot_linear_mx4_workspace_for_rows(int64_t rows, int64_t k);
+size_t convrot_linear_mx4_workspace_size(int64_t m, int64_t n, int64_t k);
+
+/* ---- Gated residual and norm ------------------------------------------------
+ *
+ * The step between two layers of a transformer block, in one pass:
+ *   x' = RN16(x + gate * post(o))                    (o null: x' = x, not written)
+ *   h  = RN16(norm(x') * (1 + scale) + shift)
+ * with post and norm one of
+ *   CONVROT_NORM_RMS    v / sqrt(mean(v^2) + eps) [* weight]
+ *   CONVROT_NORM_LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) [* weight]
+ * (post_norm may be CONVROT_NORM_NONE). norm() reads x' as it was rounded; all
+ * else is fp32. h goes out in 16 bits (h), rotated and quantized for
+ * convrot_gemm_mx4 (h_codes, h_scales, g, rot_seed: bit for bit what
+ * convrot_quantize_mx4 gives for the 16-bit h), or both.
+ *   x, o, x_out, h [m, k]; post_weight, weight [k]; all in dtype. Null: absent.
+ *   x_out may be x itself (in place); otherwise no output may overlap an input.
+ *   gate, scale, shift: one [k] row per sample; row r of x takes modulation
+ *     row r / rows_per_mod, `*_stride` elements apart (a multiple of 8; 0 = one
+ *     row for all), so they can be column ranges of one wider tensor.
+ * k % 8 == 0, k <= 16384; quantized also k % 32 == 0 and k % g == 0. */
+typedef enum convrot_norm_kind {
+  CONVROT_NORM_NONE = 0,
+  CONVROT_NORM_RMS = 1,
+  CONVROT_NORM_LAYER = 2
+} convrot_norm_kind;
+typedef struct convrot_norm_args {
+  const void* x;
+  const void* o;
+  void* x_out;
+  const void* post_weight;
+  const void* weight;
+  const void* gate;
+  const void* scale;
+  const void* shift;
+  int64_t gate_stride, scale_stride, shift_stride;
+  void* h;
+  uint8_t* h_codes;
+  uint8_t* h_scales;
+  int64_t m, k, rows_per_mod;
+  uint64_t rot_seed;
+  convrot_norm_kind post_norm, norm;
+  convrot_dtype dtype;
+  int32_t g;
+  float eps;
+} convrot_norm_args;
+convrot_status convrot_norm_residual(const convrot_norm_args* args, void* stream);
+
 /* Host-only: the rotation signs d[0..g) for (g, rot_seed) as +1/-1 bytes into
  * host memory `d` (g bytes). Touches no GPU. */
 convrot_status convrot_rotation_signs(uint64_t rot_seed, int g, int8_t* d);
@@ -422,7 +548,8 @@ typedef enum convrot_kernel {
   CONVROT_KERNEL_ACT_QUANT_DEFERRED = 1, /* its blocks' pass over the rows they defer   */
   CONVROT_KERNEL_EXACT = 2,              /* exact kernel (weights, the _exact hook)     */
   CONVROT_KERNEL_DEQUANT = 3,            /* dequant + derotate                          */
-  CONVROT_KERNEL_GEMM = 4                /* int8 GEMM, automatic tile                   */
+  CONVROT_KERNEL_GEMM = 4,               /* int8 GEMM, automatic tile                   */
+  CONVROT_KERNEL_GEMM_MX4 = 5            /* MXFP4 GEMM, automatic tile                  */
 } convrot_kernel;
 typedef struct convrot_launch_plan {
   int64_t grid;           /* workgroups                                                  */

@@ -31,6 +31,9 @@ __all__ = [
     "Session", "EXPORTED_SYMBOLS", "convrot_compute_units", "convrot_set_compute_units",
     "convrot_plan_launch", "KERNELS", "convrot_linear_int8_noalloc", "NOALLOC_SCRATCH_BYTES",
     "convrot_dequant_derotate_batched",
+    "convrot_quantize_mx4", "convrot_dequant_mx4", "convrot_gemm_mx4", "convrot_linear_mx4",
+    "convrot_linear_mx4_workspace_size", "convrot_linear_mx4_workspace_for_rows",
+    "convrot_mx4_scales_size", "convrot_norm_residual", "convrot_norm_residual_mx4",
 ]
 
 ROT_SEED = 0xC0FFEE
@@ -56,13 +59,17 @@ EXPORTED_SYMBOLS = (
     "convrot_session_import", "convrot_compute_units",
     "convrot_set_compute_units", "convrot_plan_launch", "convrot_linear_int8_noalloc",
     "convrot_dequant_derotate_batched",
+    "convrot_mx4_scales_size", "convrot_quantize_mx4", "convrot_dequant_mx4", "convrot_gemm_mx4",
+    "convrot_linear_mx4", "convrot_linear_mx4_workspace_for_rows",
+    "convrot_linear_mx4_workspace_size", "convrot_norm_residual",
 )
 
 # bytes of the per-device scratch array behind convrot_linear_int8_noalloc
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 # convrot_kernel values (convrot_plan_launch)
-KERNELS = {"act_quant": 0, "act_quant_deferred": 1, "exact": 2, "dequant": 3, "gemm": 4}
+KERNELS = {"act_quant": 0, "act_quant_deferred": 1, "exact": 2, "dequant": 3, "gemm": 4,
+           "gemm_mx4": 5}
 
 
 class _DequantJob(ctypes.Structure):
@@ -144,6 +151,11 @@ def load_library():
             "convrot_linear_int8_noalloc": [P, P, P, I, P, I64, I64, I64, I, U64, P, I, P],
             "convrot_dequant_derotate_batched": [ctypes.POINTER(_DequantJob), I, I, I, U64, I, P],
             "convrot_plan_launch": [I, I64, I64, I64, I, I, ctypes.POINTER(_LaunchPlan)],
+            "convrot_quantize_mx4": [P, I, I64, I64, I, U64, P, P, P],
+            "convrot_dequant_mx4": [P, P, I64, I64, I, U64, P, I, P],
+            "convrot_gemm_mx4": [P, P, P, P, P, I64, I64, I64, P, I, I, P],
+            "convrot_linear_mx4": [P, P, P, P, I64, I64, I64, I, U64, P, I, P, SZ, P],
+            "convrot_norm_residual": [P, P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -153,6 +165,12 @@ def load_library():
         lib.convrot_linear_int8_workspace_for_rows.restype = SZ
         lib.convrot_linear_int8_workspace_size.argtypes = [I64, I64, I64]
         lib.convrot_linear_int8_workspace_size.restype = SZ
+        lib.convrot_mx4_scales_size.argtypes = [I64, I64]
+        lib.convrot_mx4_scales_size.restype = SZ
+        lib.convrot_linear_mx4_workspace_for_rows.argtypes = [I64, I64]
+        lib.convrot_linear_mx4_workspace_for_rows.restype = SZ
+        lib.convrot_linear_mx4_workspace_size.argtypes = [I64, I64, I64]
+        lib.convrot_linear_mx4_workspace_size.restype = SZ
         lib.convrot_status_string.argtypes = [I]
         lib.convrot_status_string.restype = ctypes.c_char_p
         lib.convrot_last_error_string.argtypes = []
@@ -756,3 +774,9 @@ def convrot_dequant_derotate_batched(wqs, s_ws, g: int, rot_seed: int = ROT_SEED
     _check(load_library().convrot_dequant_derotate_batched(jobs, len(wqs), mode, g, rot_seed, dt,
                                                            _stream(wqs[0])))
     return outs
+
+
+from .mx4 import (convrot_dequant_mx4, convrot_gemm_mx4, convrot_linear_mx4,  # noqa: E402
+                  convrot_linear_mx4_workspace_for_rows, convrot_linear_mx4_workspace_size,
+                  convrot_mx4_scales_size, convrot_norm_residual, convrot_norm_residual_mx4,
+                  convrot_quantize_mx4)

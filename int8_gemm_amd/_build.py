@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libconvrot.so")
-SOURCES = ("api.hip", "rotate.hip", "dequant.hip", "gemm.hip", "check.hip")
+SOURCES = ("api.hip", "rotate.hip", "dequant.hip", "gemm.hip", "check.hip",
+           "api_mx4.hip", "mx4.hip", "gemm_mx4.hip", "norm.hip")
 
 # -ffp-contract=off: the numerics contract spells out every fp32 rounding; a
 # fused multiply-add would skip one. The packed-fp32 feature is turned off for
@@ -31,10 +32,11 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build the convrot library)")
 
 
-# the GEMM keeps its MFMA accumulators in VGPRs (its waves are sized so that
-# they fit); otherwise the allocator shuffles accumulator blocks between
+# the GEMMs keep their MFMA accumulators in VGPRs (their waves are sized so
+# that they fit); otherwise the allocator shuffles accumulator blocks between
 # AGPR ranges every K-step
-EXTRA_FLAGS = {"gemm.hip": ["-mllvm", "--amdgpu-mfma-vgpr-form"]}
+_VGPR_FORM = ["-mllvm", "--amdgpu-mfma-vgpr-form"]
+EXTRA_FLAGS = {"gemm.hip": _VGPR_FORM, "gemm_mx4.hip": _VGPR_FORM}
 
 
 def _compile(src: str) -> str:

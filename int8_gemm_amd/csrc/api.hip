@@ -14,17 +14,15 @@
 #include <tuple>
 #include <vector>
 
-#include "../../include/convrot.h"
-#include "common.h"
-#include "internal.h"
+#include "api_common.h"
 
 using namespace convrot;
 
-namespace {
+static thread_local char g_last_error[512] = "";
 
-thread_local char g_last_error[512] = "";
+// helpers of every entry point (api_common.h)
+namespace convrot {
 
-convrot_status fail(convrot_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 convrot_status fail(convrot_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -45,7 +43,7 @@ convrot_status hip_status(hipError_t e, const char* what) {
 
 // SplitMix64 (Steele, Lea, Flood, OOPSLA 2014), counter form:
 // output i = mix(seed + (i + 1) * golden gamma).
-uint64_t splitmix64_mix(uint64_t z) {
+static uint64_t splitmix64_mix(uint64_t z) {
   z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
   z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
   return z ^ (z >> 31);
@@ -61,17 +59,10 @@ SignMask make_signs(uint64_t seed, int g) {
   return sm;
 }
 
-bool valid_group(int g) { return g == 4 || g == 16 || g == 64 || g == 256; }
+}  // namespace convrot
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+namespace {
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t x0 = (uintptr_t)a, x1 = x0 + na, y0 = (uintptr_t)b, y1 = y0 + nb;
-  return x0 < y1 && y0 < x1;
-}
-
-constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxRotK = 16384;
 constexpr int64_t kMaxGemmK = 133144;  // 127^2 * K < 2^31
 
@@ -105,14 +96,6 @@ convrot_status check_gemm(const char* fn, int64_t m, int64_t n, int64_t k) {
   return CONVROT_OK;
 }
 
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-// enum arguments of the *_ex entry points
-bool dtype_of(int v, DType* dt) {
-  if (v != CONVROT_DTYPE_BF16 && v != CONVROT_DTYPE_F16) return false;
-  *dt = v == CONVROT_DTYPE_F16 ? DType::kF16 : DType::kBF16;
-  return true;
-}
 bool scale_mode_of(int v, bool* pc) {
   if (v != CONVROT_SCALE_PER_TENSOR && v != CONVROT_SCALE_PER_CHANNEL) return false;
   *pc = v == CONVROT_SCALE_PER_CHANNEL;
@@ -189,6 +172,11 @@ convrot_status convrot_plan_launch(convrot_kernel kernel, int64_t m, int64_t n, 
       if (convrot_status s = check_gemm(fn, m, n, k)) return s;
       if (m == 0) return ok();
       p = plan_gemm(m, n, k, 0, cus);
+      break;
+    case CONVROT_KERNEL_GEMM_MX4:
+      if (convrot_status s = check_mx4_gemm(fn, m, n, k)) return s;
+      if (m == 0) return ok();
+      p = plan_mx4_gemm(m, n, k, 0, cus);
       break;
     default:
       return fail(CONVROT_E_INVALID_ARG, "%s: kernel=%d", fn, (int)kernel);

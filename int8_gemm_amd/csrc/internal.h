@@ -98,4 +98,43 @@ hipError_t launch_check_rows(const uint16_t* x, const uint16_t* w_hat, const uin
                              const uint16_t* y, int64_t ldy, int rows, int n, int k, DType dt,
                              bool accumulate, float* y_ref, double* partial, hipStream_t st);
 
+
+// ---- microscaled 4-bit (MXFP4) tensors; layout in mx4.h ----
+// The signs of one group, repeated over a 256-element tile.
+SignMask mx4_tile_signs(const SignMask& sm, int g);
+// Whether [rows, k] fits the grids of the two kernels below.
+bool mx4_grid_fits(int64_t rows, int64_t k);
+// Rotate (g = 1: not) and quantize rows; g divides K, K % 32 == 0.
+hipError_t launch_mx4_quantize(const uint16_t* x, int64_t rows, int K, int g, const SignMask& sm,
+                               DType dt, uint8_t* codes, uint8_t* scales, hipStream_t st);
+// The tensor a quantized form stands for, derotated, in dt.
+hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K,
+                              int g, const SignMask& sm, uint16_t* out, DType dt, hipStream_t st);
+// y = RN16(a . b^T [+ bias]) over two quantized tensors, sums in fp32; tile as
+// in convrot_gemm_mx4 (0 = automatic).
+hipError_t launch_mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc,
+                           const uint8_t* ws, const uint16_t* bias, int64_t m, int64_t n,
+                           int64_t k, uint16_t* y, int tile, DType dt, hipStream_t st);
+// Gated residual and norms (norm.hip). Strides are elements between the
+// modulation rows of consecutive samples; row r takes row r / rows_per_mod.
+enum class NormKind { kNone = 0, kRms = 1, kLayer = 2 };
+struct NormArgs {
+  const uint16_t *x, *o, *post_weight, *weight, *gate, *scale, *shift;
+  int64_t gate_stride, scale_stride, shift_stride;
+  uint16_t *x_out, *h;
+  uint8_t *h_codes, *h_scales;
+  int64_t m, rows_per_mod;
+  int k;
+  NormKind post_norm, norm;
+  float eps;
+};
+// g = 0: h in 16 bits; otherwise h is also rotated in groups of g (1: not) and quantized.
+hipError_t launch_norm_residual(const NormArgs& a, int g, const SignMask& sm, DType dt,
+                                hipStream_t st);
+// The tile for `m` rows of a call that has `call_rows` rows in all: the two
+// kernels sum in different orders, so one call keeps to one of them whatever
+// its slices are.
+int mx4_gemm_tile(int64_t m, int64_t n, int64_t call_rows, int cus);
+LaunchPlan plan_mx4_gemm(int64_t m, int64_t n, int64_t k, int tile, int cus);
+
 }  // namespace convrot

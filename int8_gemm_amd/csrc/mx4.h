@@ -1,0 +1,228 @@
+// Device side of the microscaled 4-bit (MXFP4) form, shared by the kernels
+// that write it (mx4.hip, norm.hip) and read it back.
+//
+// A [rows, K] tensor is held as
+//   codes  [rows, K / 2]: one byte per two elements, the even one in the low
+//          nibble; a code is a sign bit and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6;
+//   scales [ceil(K / 256)][R16][8], R16 = rows rounded up to 16: the biased
+//          exponent of the 2^e that 32 consecutive elements of a row share
+//          (255: the block is NaN). Eight blocks of a row are one K-step of
+//          the GEMM; with the rows innermost a tile's scales of a K-step are
+//          one contiguous run, and the padding aligns every K-step's run.
+//
+// Rotation. A tile is 256 elements of one row, held by 8 lanes (a wave holds
+// 8 tiles). Lane j of the 8 keeps label c = j ^ (j & 4 ? 3 : 0) and the
+// elements 64 i + 8 c + e, i < 4, e < 8: one 16-byte load per i, and 8 lanes
+// read 128 consecutive bytes. The Walsh-Hadamard levels over e (and i, for
+// g = 256) are in-lane; those over c are exchanges with lane j ^ 1, j ^ 2
+// and 7 - j (the half-row mirror, a single DPP step that flips bit 2 of the
+// label alone). An exchange level computes
+//   own + s * partner, s = +1 / -1 where the label's bit is 0 / 1,
+// one fused DPP multiply-add, which leaves a lane with the bit set negated.
+// The product of these signs over the levels is (-1)^popcount(c & J), J = the
+// label bits transformed; H with its outputs so signed equals H of the input
+// shifted by J (H[i][j] (-1)^popcount(i & J) = H[i][j ^ J]), so the lane loads
+// the elements of label c ^ J and no sign is left to undo.
+#pragma once
+
+#include "common.h"
+
+namespace convrot {
+
+constexpr int kMx4Block = 32;   // elements per scale
+constexpr int kMx4Tile = 256;   // elements per K-step of the scale layout
+
+__host__ __device__ constexpr int64_t mx4_pad_rows(int64_t rows) { return (rows + 15) / 16 * 16; }
+
+__device__ __forceinline__ int mx4_label(int lane) {
+  const int j = lane & 7;
+  return j ^ ((j & 4) ? 3 : 0);
+}
+// label bits that the rotation transforms across lanes
+template <int G>
+constexpr int kMx4LaneBits = G >= 64 ? 7 : (G == 16 ? 1 : 0);
+
+template <int CTRL>
+__device__ __forceinline__ float mx4_dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double mx4_dpp(double v) {
+  const uint64_t b = __double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+  return __longlong_as_double(((uint64_t)hi << 32) | lo);
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t mx4_dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ float mx4_fma(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
+__device__ __forceinline__ double mx4_fma(double a, double b, double c) { return __builtin_fma(a, b, c); }
+constexpr int kDppXor1 = 0xB1;     // quad_perm [1,0,3,2]
+constexpr int kDppXor2 = 0x4E;     // quad_perm [2,3,0,1]
+constexpr int kDppMirror8 = 0x141; // row_half_mirror: lane j of 8 <- lane 7 - j
+
+// x . blockdiag(H_G) of the tile, unnormalised, in place; `label` is the
+// lane's own (output) label. T = float or double; sums in T.
+template <int G, typename T>
+__device__ __forceinline__ void mx4_hadamard(T (&v)[4][8], int label) {
+  constexpr int LE = G < 8 ? G : 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int h = 1; h < LE; h <<= 1) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (e & h) continue;
+        const T a = v[i][e], b = v[i][e + h];
+        v[i][e] = a + b;
+        v[i][e + h] = a - b;
+      }
+    }
+  }
+  if constexpr (G == 256) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const T a = v[0][e] + v[1][e], b = v[0][e] - v[1][e];
+      const T c = v[2][e] + v[3][e], d = v[2][e] - v[3][e];
+      v[0][e] = a + c;
+      v[1][e] = b + d;
+      v[2][e] = a - c;
+      v[3][e] = b - d;
+    }
+  }
+  if constexpr (G >= 16) {
+    const T s = (label & 1) ? T(-1) : T(1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = mx4_fma(mx4_dpp<kDppXor1>(v[i][e]), s, v[i][e]);
+  }
+  if constexpr (G >= 64) {
+    const T s = (label & 2) ? T(-1) : T(1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = mx4_fma(mx4_dpp<kDppXor2>(v[i][e]), s, v[i][e]);
+    const T t = (label & 4) ? T(-1) : T(1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[i][e] = mx4_fma(mx4_dpp<kDppMirror8>(v[i][e]), t, v[i][e]);
+  }
+}
+
+// The rotation's signs as masks for packed codes: bit 3 of nibble e of word
+// i is set where d = -1 for element 64 i + 8 label + e. `sm` holds the signs
+// of a whole 256-element tile.
+__device__ __forceinline__ void mx4_sign_masks(const SignMask& sm, int label,
+                                               uint32_t (&mask)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = (label & 4) ? sm.w[2 * i + 1] : sm.w[2 * i];
+    uint32_t b = (w >> (8 * (label & 3))) & 0xFFu;
+    b = (b | (b << 12)) & 0x000F000Fu;
+    b = (b | (b << 6)) & 0x03030303u;
+    b = (b | (b << 3)) & 0x11111111u;
+    mask[i] = b << 3;
+  }
+}
+
+// max over the lane's elements of each i and the 4 lanes that share its block
+// (element 64 i + 8 c + e lies in block 2 i + c / 4)
+__device__ __forceinline__ uint32_t mx4_block_max(uint32_t m) {
+  m = max(m, mx4_dpp<kDppXor1>(m));
+  return max(m, mx4_dpp<kDppXor2>(m));
+}
+
+// 2^e as a float from the biased exponent b (e = b - 127; b = 0 gives 2^-127,
+// a subnormal)
+__device__ __forceinline__ float mx4_pow2(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b << 23);
+}
+
+// Quantize the rotated fp32 values of the lane: biased exponents per i and
+// codes without the rotation's signs. A block that holds a value that is not
+// finite gets exponent 255 and codes 0.
+__device__ __forceinline__ void mx4_encode(const float (&v)[4][8], uint32_t (&eb)[4],
+                                           uint32_t (&code)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // largest magnitude as an integer: orders finite < inf < NaN
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+    m = mx4_block_max(m);
+    const uint32_t field = m >> 23;
+    const bool bad = field == 255;
+    // floor(log2 max) - 2 from the exponent field; below 2^-125 (subnormals
+    // among them) it is clamped to -127
+    const uint32_t b = field > 2 ? field - 2 : 0;
+    eb[i] = bad ? 255 : b;
+    // at 2^-127 the conversion's divisor would be subnormal: both sides are
+    // doubled, exactly
+    const float up = b == 0 ? 2.0f : 1.0f;
+    const float unit = __uint_as_float((b == 0 ? 1u : b) << 23);
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][0] * up, v[i][1] * up, unit, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][2] * up, v[i][3] * up, unit, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][4] * up, v[i][5] * up, unit, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][6] * up, v[i][7] * up, unit, 3);
+    code[i] = bad ? 0 : w;
+  }
+}
+
+// Rotate and quantize a tile from its packed 16-bit elements (raw[i] = the 8
+// elements of label c ^ kMx4LaneBits<G>, i as above). Every sum is taken in
+// float64 and rounded once to fp32.
+template <int G, bool F16>
+__device__ __forceinline__ void mx4_quantize_tile(const u4 (&raw)[4], int label,
+                                                  const uint32_t (&signs)[4], uint32_t (&eb)[4],
+                                                  uint32_t (&code)[4]) {
+  float f[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      f[i][2 * p] = lo16<F16>(raw[i][p]);
+      f[i][2 * p + 1] = hi16<F16>(raw[i][p]);
+    }
+  if constexpr (G > 1) {
+    double d[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[i][e] = f[i][e];
+    mx4_hadamard<G>(d, label);
+    constexpr double norm = 1.0 / (1 << (ilog2(G) / 2));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] = (float)(d[i][e] * norm);
+  }
+  mx4_encode(f, eb, code);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) code[i] ^= G > 1 ? signs[i] : 0u;
+}
+
+// Write a quantized tile: word i of the lane covers elements 64 i + 8 c .. + 7
+// (`codes` = the row's tile), lane (c & 3) = i writes the exponent of block
+// 2 i + c / 4 (`scales` = the row's 8 bytes of the tile). Blocks at and behind
+// `blocks` (the row's end) are not part of the tensor: no codes, exponent 0.
+__device__ __forceinline__ void mx4_store_tile(uint8_t* __restrict__ codes,
+                                               uint8_t* __restrict__ scales, int label,
+                                               int blocks, const uint32_t (&eb)[4],
+                                               const uint32_t (&code)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (2 * i + (label >> 2) < blocks)
+      *reinterpret_cast<uint32_t*>(codes + 32 * i + 4 * label) = code[i];
+  const int q = label & 3;
+  const uint32_t lo = q & 1 ? eb[1] : eb[0], hi = q & 1 ? eb[3] : eb[2];
+  const int blk = 2 * q + (label >> 2);
+  scales[blk] = (uint8_t)(blk < blocks ? (q & 2 ? hi : lo) : 0u);
+}
+
+}  // namespace convrot

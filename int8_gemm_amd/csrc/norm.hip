@@ -1,0 +1,226 @@
+// Gated residual and norm of a transformer block (gfx950), the step between
+// two quantized layers:
+//
+//   x' = RN16(x + gate * post(o))         (o absent: x' = x, not written)
+//   h  = RN16(pre(x') * (1 + scale) + shift)
+//   post, pre: RMS   v / sqrt(mean(v^2) + eps) [* weight]
+//              layer (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) [* weight]
+//
+// and h goes out in 16 bits, as rotated MXFP4 (the input of the next layer's
+// product, the same bits that quantizing the 16-bit h would give), or both.
+// pre() reads x' as it was rounded, so that h is a function of the x' that the
+// caller gets. Everything else is fp32.
+//
+// Bound by memory: x and o are read once, x' and h written once; the row stays
+// in registers between the norms (32 elements a lane, in the tile layout of
+// mx4.h). A row takes ceil(K / 2048) waves; rows of one wave share a block of
+// four. Variances are taken in two passes over the registers, around the mean.
+
+#include "internal.h"
+#include "mx4.h"
+
+namespace convrot {
+
+namespace {
+
+constexpr int kLaneElems = 32;                  // elements of a row per lane
+constexpr int kWaveElems = 64 * kLaneElems;     // ... and per wave
+constexpr int kRowsPerBlock = 4;                // when a row is one wave
+constexpr int kMaxWaves = 8;                    // K <= 16384
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) v += __shfl_xor(v, s);
+  return v;
+}
+
+// Sum over the row's waves; `part` holds one slot per wave. Two calls in a row
+// use different slots, so one barrier each is enough.
+__device__ __forceinline__ float row_sum(float v, int waves, float* part) {
+  v = wave_sum(v);
+  if (waves == 1) return v;
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) part[wave] = v;
+  __syncthreads();
+  float s = part[0];
+  for (int w = 1; w < waves; ++w) s += part[w];
+  return s;
+}
+
+template <bool F16>
+__device__ __forceinline__ void unpack(const u4& w, float (&f)[8]) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    f[2 * p] = lo16<F16>(w[p]);
+    f[2 * p + 1] = hi16<F16>(w[p]);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ u4 pack(const float (&f)[8]) {
+  return (u4){pack16x2<F16>(f[0], f[1]), pack16x2<F16>(f[2], f[3]), pack16x2<F16>(f[4], f[5]),
+              pack16x2<F16>(f[6], f[7])};
+}
+
+// Normalise v in place (without its weight). `in` marks the lane's chunks that
+// lie in the row; `part` has 2 * kMaxWaves slots.
+__device__ __forceinline__ void normalise(float (&v)[4][8], const bool (&in)[4], NormKind kind,
+                                          float k, float eps, int waves, float* part) {
+  if (kind == NormKind::kLayer) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += v[i][e];  // chunks outside the row hold 0
+    const float mean = row_sum(s, waves, part + kMaxWaves) / k;  // a row of one value gives it back
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = in[i] ? v[i][e] - mean : 0.f;
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q = __builtin_fmaf(v[i][e], v[i][e], q);
+  const float r = 1.0f / sqrtf(row_sum(q, waves, part) / k + eps);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] *= r;
+}
+
+// G: 0 = h in 16 bits only, otherwise the rotation group of the quantized h
+// (1: none); a 16-bit h goes out as well where its pointer is set.
+template <int G, bool F16>
+__global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs a, SignMask sm,
+                                                                       int waves) {
+  __shared__ float part[4 * kMaxWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int64_t row = waves == 1 ? (int64_t)blockIdx.x * kRowsPerBlock + wave : blockIdx.x;
+  if (row >= a.m) return;  // one-wave rows only: no barrier follows
+  const int label = mx4_label(lane);
+  const int lab_in = label ^ kMx4LaneBits<G>;
+  const int tile = (waves == 1 ? 0 : wave * 8) + (lane >> 3);
+  const int col = tile * kMx4Tile + 8 * lab_in;  // + 64 i
+  const int64_t base = row * a.k + col;
+  const int64_t mod = row / a.rows_per_mod;
+  bool in[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) in[i] = col + 64 * i < a.k;
+  const u4 zero = {0, 0, 0, 0};
+  auto load = [&](const uint16_t* p, int i) {
+    return in[i] ? *reinterpret_cast<const u4*>(p + 64 * i) : zero;
+  };
+
+  u4 xw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) xw[i] = load(a.x + base, i);
+  float v[4][8];
+  if (a.o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack<F16>(load(a.o + base, i), v[i]);
+    if (a.post_norm != NormKind::kNone) {
+      normalise(v, in, a.post_norm, (float)a.k, a.eps, waves, part);
+      if (a.post_weight) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float w[8];
+          unpack<F16>(load(a.post_weight + col, i), w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
+        }
+      }
+    }
+    if (a.gate) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float w[8];
+        unpack<F16>(load(a.gate + mod * a.gate_stride + col, i), w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float w[8];
+      unpack<F16>(xw[i], w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] += v[i][e];
+      xw[i] = pack<F16>(w);
+      if (in[i]) *reinterpret_cast<u4*>(a.x_out + base + 64 * i) = xw[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    unpack<F16>(xw[i], v[i]);
+    if (!in[i]) {  // 0 * inf of an absent chunk's gate must not reach the sums
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+    }
+  }
+  normalise(v, in, a.norm, (float)a.k, a.eps, waves, part + 2 * kMaxWaves);
+  u4 hw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float w[8];
+    if (a.weight) {
+      unpack<F16>(load(a.weight + col, i), w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
+    }
+    if (a.scale) {
+      unpack<F16>(load(a.scale + mod * a.scale_stride + col, i), w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] *= 1.0f + w[e];
+    }
+    if (a.shift) {
+      unpack<F16>(load(a.shift + mod * a.shift_stride + col, i), w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] += w[e];
+    }
+    hw[i] = pack<F16>(v[i]);
+    if (a.h && in[i]) *reinterpret_cast<u4*>(a.h + base + 64 * i) = hw[i];
+  }
+  if constexpr (G > 0) {
+    uint32_t signs[4], eb[4], code[4];
+    mx4_sign_masks(sm, label, signs);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) hw[i] = in[i] ? hw[i] : zero;
+    mx4_quantize_tile<G, F16>(hw, label, signs, eb, code);
+    const int blocks = min(8, (a.k - tile * kMx4Tile) / kMx4Block);
+    if (blocks > 0)
+      mx4_store_tile(a.h_codes + row * (a.k / 2) + tile * (kMx4Tile / 2),
+                     a.h_scales + (tile * mx4_pad_rows(a.m) + row) * 8, label, blocks, eb, code);
+  }
+}
+
+template <int G>
+hipError_t launch_g(const NormArgs& a, const SignMask& sm, DType dt, hipStream_t st) {
+  const int waves = (a.k + kWaveElems - 1) / kWaveElems;
+  const dim3 grid((uint32_t)(waves == 1 ? (a.m + kRowsPerBlock - 1) / kRowsPerBlock : a.m));
+  const dim3 block(64 * (waves == 1 ? kRowsPerBlock : waves));
+  if (dt == DType::kF16)
+    norm_residual_kernel<G, true><<<grid, block, 0, st>>>(a, sm, waves);
+  else
+    norm_residual_kernel<G, false><<<grid, block, 0, st>>>(a, sm, waves);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm_residual(const NormArgs& a, int g, const SignMask& sm, DType dt,
+                                hipStream_t st) {
+  if (a.m == 0) return hipSuccess;
+  const SignMask t = g > 0 ? mx4_tile_signs(sm, g) : sm;
+  switch (g) {
+    case 0: return launch_g<0>(a, t, dt, st);
+    case 1: return launch_g<1>(a, t, dt, st);
+    case 4: return launch_g<4>(a, t, dt, st);
+    case 16: return launch_g<16>(a, t, dt, st);
+    case 64: return launch_g<64>(a, t, dt, st);
+    default: return launch_g<256>(a, t, dt, st);
+  }
+}
+
+}  // namespace convrot
