@@ -57,19 +57,65 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t mx4_dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
 }
-__device__ __forceinline__ float mx4_fma(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
-__device__ __forceinline__ double mx4_fma(double a, double b, double c) { return __builtin_fma(a, b, c); }
 constexpr int kDppXor1 = 0xB1;     // quad_perm [1,0,3,2]
 constexpr int kDppXor2 = 0x4E;     // quad_perm [2,3,0,1]
 constexpr int kDppMirror8 = 0x141; // row_half_mirror: lane j of 8 <- lane 7 - j
 
-// x . blockdiag(H_G) of the tile, unnormalised, in place; `label` is the
-// lane's own (output) label. T = float or double; sums in T.
-template <int G, typename T>
-__device__ __forceinline__ void mx4_hadamard(T (&v)[4][8], int label) {
+// One exchange level: v = v + s * (the partner's v).
+template <int CTRL>
+__device__ __forceinline__ void mx4_exchange(double (&v)[1][8], double s) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[0][e] = __builtin_fma(mx4_dpp<CTRL>(v[0][e]), s, v[0][e]);
+}
+
+// In fp32 the exchange folds into the multiply-add, which the compiler does
+// not do by itself (a move and a multiply-add per element: 556 instead of 460
+// instructions a wave for g = 256). A DPP operand must not have been written by
+// the last two instructions; the compiler does not look into the block for
+// that, so both ends wait.
+#define CONVROT_FMAC_DPP(CTRL_TEXT, a, b, s)                                                    \
+  asm volatile("s_nop 1\n\t"                                                                    \
+               "v_fmac_f32_dpp %0, %0, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"        \
+               "v_fmac_f32_dpp %1, %1, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"        \
+               "v_fmac_f32_dpp %2, %2, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"        \
+               "v_fmac_f32_dpp %3, %3, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"        \
+               "v_fmac_f32_dpp %4, %4, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"        \
+               "v_fmac_f32_dpp %5, %5, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"        \
+               "v_fmac_f32_dpp %6, %6, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"        \
+               "v_fmac_f32_dpp %7, %7, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"        \
+               "v_fmac_f32_dpp %8, %8, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"        \
+               "v_fmac_f32_dpp %9, %9, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"        \
+               "v_fmac_f32_dpp %10, %10, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"      \
+               "v_fmac_f32_dpp %11, %11, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"      \
+               "v_fmac_f32_dpp %12, %12, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"      \
+               "v_fmac_f32_dpp %13, %13, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"      \
+               "v_fmac_f32_dpp %14, %14, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"      \
+               "v_fmac_f32_dpp %15, %15, %16 " CTRL_TEXT " row_mask:0xf bank_mask:0xf\n\t"      \
+               "s_nop 1"                                                                        \
+               : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]), "+v"(a[4]), "+v"(a[5]),        \
+                 "+v"(a[6]), "+v"(a[7]), "+v"(b[0]), "+v"(b[1]), "+v"(b[2]), "+v"(b[3]),        \
+                 "+v"(b[4]), "+v"(b[5]), "+v"(b[6]), "+v"(b[7])                                 \
+               : "v"(s))
+
+template <int CTRL>
+__device__ __forceinline__ void mx4_exchange(float (&v)[4][8], float s) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    if constexpr (CTRL == kDppXor1) CONVROT_FMAC_DPP("quad_perm:[1,0,3,2]", v[i], v[i + 1], s);
+    if constexpr (CTRL == kDppXor2) CONVROT_FMAC_DPP("quad_perm:[2,3,0,1]", v[i], v[i + 1], s);
+    if constexpr (CTRL == kDppMirror8) CONVROT_FMAC_DPP("row_half_mirror", v[i], v[i + 1], s);
+  }
+}
+#undef CONVROT_FMAC_DPP
+
+// x . blockdiag(H_G) of the tile (or of a chunk i of it, for G <= 64),
+// unnormalised, in place; `label` is the lane's own (output) label. Sums in T.
+template <int G, typename T, int C>
+__device__ __forceinline__ void mx4_hadamard(T (&v)[C][8], int label) {
+  static_assert(C == 4 || G <= 64, "a group lies in the chunks at hand");
   constexpr int LE = G < 8 ? G : 8;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < C; ++i) {
 #pragma unroll
     for (int h = 1; h < LE; h <<= 1) {
 #pragma unroll
@@ -92,25 +138,10 @@ __device__ __forceinline__ void mx4_hadamard(T (&v)[4][8], int label) {
       v[3][e] = b - d;
     }
   }
-  if constexpr (G >= 16) {
-    const T s = (label & 1) ? T(-1) : T(1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = mx4_fma(mx4_dpp<kDppXor1>(v[i][e]), s, v[i][e]);
-  }
+  if constexpr (G >= 16) mx4_exchange<kDppXor1>(v, (label & 1) ? T(-1) : T(1));
   if constexpr (G >= 64) {
-    const T s = (label & 2) ? T(-1) : T(1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = mx4_fma(mx4_dpp<kDppXor2>(v[i][e]), s, v[i][e]);
-    const T t = (label & 4) ? T(-1) : T(1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[i][e] = mx4_fma(mx4_dpp<kDppMirror8>(v[i][e]), t, v[i][e]);
+    mx4_exchange<kDppXor2>(v, (label & 2) ? T(-1) : T(1));
+    mx4_exchange<kDppMirror8>(v, (label & 4) ? T(-1) : T(1));
   }
 }
 
@@ -143,45 +174,35 @@ __device__ __forceinline__ float mx4_pow2(uint32_t b) {
   return __uint_as_float(b == 0 ? 0x00400000u : b << 23);
 }
 
-// Quantize the rotated fp32 values of the lane: biased exponents per i and
-// codes without the rotation's signs. A block that holds a value that is not
-// finite gets exponent 255 and codes 0.
-__device__ __forceinline__ void mx4_encode(const float (&v)[4][8], uint32_t (&eb)[4],
-                                           uint32_t (&code)[4]) {
+// Quantize 8 rotated fp32 values of the lane (one i): the block's biased
+// exponent and the codes without the rotation's signs. A block that holds a
+// value that is not finite gets exponent 255 and codes 0.
+__device__ __forceinline__ void mx4_encode(const float (&v)[8], uint32_t& eb, uint32_t& code) {
+  // largest magnitude as an integer: orders finite < inf < NaN
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // largest magnitude as an integer: orders finite < inf < NaN
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
-    m = mx4_block_max(m);
-    const uint32_t field = m >> 23;
-    const bool bad = field == 255;
-    // floor(log2 max) - 2 from the exponent field; below 2^-125 (subnormals
-    // among them) it is clamped to -127
-    const uint32_t b = field > 2 ? field - 2 : 0;
-    eb[i] = bad ? 255 : b;
-    // at 2^-127 the conversion's divisor would be subnormal: both sides are
-    // doubled, exactly
-    const float up = b == 0 ? 2.0f : 1.0f;
-    const float unit = __uint_as_float((b == 0 ? 1u : b) << 23);
-    uint32_t w = 0;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][0] * up, v[i][1] * up, unit, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][2] * up, v[i][3] * up, unit, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][4] * up, v[i][5] * up, unit, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][6] * up, v[i][7] * up, unit, 3);
-    code[i] = bad ? 0 : w;
-  }
+  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  m = mx4_block_max(m);
+  const uint32_t field = m >> 23;
+  const bool bad = field == 255;
+  // floor(log2 max) - 2 from the exponent field; below 2^-125 (subnormals
+  // among them) it is clamped to -127
+  const uint32_t b = field > 2 ? field - 2 : 0;
+  eb = bad ? 255 : b;
+  // at 2^-127 the conversion's divisor would be subnormal: both sides are
+  // doubled, exactly
+  const float up = b == 0 ? 2.0f : 1.0f;
+  const float unit = __uint_as_float((b == 0 ? 1u : b) << 23);
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * up, v[1] * up, unit, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * up, v[3] * up, unit, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4] * up, v[5] * up, unit, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6] * up, v[7] * up, unit, 3);
+  code = bad ? 0 : w;
 }
 
-// Rotate and quantize a tile from its packed 16-bit elements (raw[i] = the 8
-// elements of label c ^ kMx4LaneBits<G>, i as above). Every sum is taken in
-// float64 and rounded once to fp32.
-template <int G, bool F16>
-__device__ __forceinline__ void mx4_quantize_tile(const u4 (&raw)[4], int label,
-                                                  const uint32_t (&signs)[4], uint32_t (&eb)[4],
-                                                  uint32_t (&code)[4]) {
-  float f[4][8];
+template <bool F16>
+__device__ __forceinline__ void mx4_unpack(const u4 (&raw)[4], float (&f)[4][8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -189,22 +210,110 @@ __device__ __forceinline__ void mx4_quantize_tile(const u4 (&raw)[4], int label,
       f[i][2 * p] = lo16<F16>(raw[i][p]);
       f[i][2 * p + 1] = hi16<F16>(raw[i][p]);
     }
-  if constexpr (G > 1) {
-    double d[4][8];
+}
+
+// The definition, for one i: sums in float64, rounded once to fp32, then the
+// codes. With g = 256 the transform over the four chunks comes first and yields
+// this i's row of it alone, so that only 8 sums are live.
+template <int G, bool F16>
+__device__ __forceinline__ void mx4_rotate_encode_f64(const u4 (&raw)[4], int i, int label,
+                                                      uint32_t& eb, uint32_t& code) {
+  double d[1][8] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int c = 0; c < 4; ++c) {
+    if (G < 256 && c != i) continue;
+    const double s = G == 256 && (__builtin_popcount(c & i) & 1) ? -1.0 : 1.0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[i][e] = f[i][e];
-    mx4_hadamard<G>(d, label);
-    constexpr double norm = 1.0 / (1 << (ilog2(G) / 2));
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] = (float)(d[i][e] * norm);
+    for (int p = 0; p < 4; ++p) {
+      uint32_t w = raw[c][p];
+      asm volatile("" : "+v"(w));  // keeps the conversions here, off the common path
+      d[0][2 * p] = __builtin_fma((double)lo16<F16>(w), s, d[0][2 * p]);
+      d[0][2 * p + 1] = __builtin_fma((double)hi16<F16>(w), s, d[0][2 * p + 1]);
+    }
   }
-  mx4_encode(f, eb, code);
+  mx4_hadamard<(G < 64 ? G : 64)>(d, label);
+  constexpr double norm = 1.0 / (1 << (ilog2(G) / 2));
+  float f[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) code[i] ^= G > 1 ? signs[i] : 0u;
+  for (int e = 0; e < 8; ++e) f[e] = (float)(d[0][e] * norm);
+  mx4_encode(f, eb, code);
+}
+
+// Rotate and quantize a tile from its packed 16-bit elements (raw[i] = the 8
+// elements of label c ^ kMx4LaneBits<G>, i as above): biased exponents and
+// codes per i.
+//
+// Sums in fp32 decide nearly all of it. Such a sum's error is at most delta =
+// log2(G) 2^-24 sum|x| over its group (each of the log2(G) additions on its way
+// rounds a partial sum of at most sum|x|). Rounding to fp32 and to codes are
+// monotone, so where v - delta and v + delta get the same code, and the
+// block's largest magnitude +- delta the same exponent, the float64 sum gets
+// them too. Where any lane of the wave is left open (or a block lies so low or
+// high that fp32 would lose bits of the definition) the wave takes the float64
+// sums of that i: one wave in ten or so for normal activations, a quarter of
+// the tile at a time. All of it in float64 took 126 us instead of EXACT_US at
+// 32760 x 5120, g = 256.
+template <int G, bool F16>
+__device__ __forceinline__ void mx4_quantize_tile(const u4 (&raw)[4], int label,
+                                                  const uint32_t (&signs)[4], uint32_t (&eb)[4],
+                                                  uint32_t (&code)[4]) {
+  float v[4][8];
+  mx4_unpack<F16>(raw, v);
+  if constexpr (G == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx4_encode(v[i], eb[i], code[i]);
+    return;
+  }
+  constexpr int lg = ilog2(G) / 2;  // sqrt(G) = 2^lg: the fp32 sums stay unnormalised
+  // sum|x| over the group, or over the block where a block holds several
+  float mass[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += __builtin_fabsf(v[i][e]);
+    mass[i] = s;
+  }
+  if constexpr (G == 256) mass[0] = (mass[0] + mass[1]) + (mass[2] + mass[3]);
+#pragma unroll
+  for (int i = 0; i < (G == 256 ? 1 : 4); ++i) {
+    mass[i] += mx4_dpp<kDppXor1>(mass[i]);
+    mass[i] += mx4_dpp<kDppXor2>(mass[i]);
+    if constexpr (G >= 64) mass[i] += mx4_dpp<kDppMirror8>(mass[i]);
+  }
+  if constexpr (G == 256) mass[1] = mass[2] = mass[3] = mass[0];
+  mx4_hadamard<G>(v, label);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // 1 + 2^-9 covers the roundings of the mass itself and of the product
+    constexpr float c = ilog2(G) * 0x1p-24f * (1.0f + 0x1p-9f);
+    const float delta = mass[i] * c;
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, __builtin_fabsf(v[i][e]));
+    top = fmaxf(top, mx4_dpp<kDppXor1>(top));
+    top = fmaxf(top, mx4_dpp<kDppXor2>(top));
+    const uint32_t field = __float_as_uint(top - delta) >> 23;
+    const bool zero = mass[i] == 0.f;
+    const float unit = __uint_as_float((zero ? 1u : field - 2) << 23);
+    uint32_t lo = 0, hi = 0;
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, v[i][0] - delta, v[i][1] - delta, unit, 0);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, v[i][0] + delta, v[i][1] + delta, unit, 0);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, v[i][2] - delta, v[i][3] - delta, unit, 1);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, v[i][2] + delta, v[i][3] + delta, unit, 1);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, v[i][4] - delta, v[i][5] - delta, unit, 2);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, v[i][4] + delta, v[i][5] + delta, unit, 2);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, v[i][6] - delta, v[i][7] - delta, unit, 3);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, v[i][6] + delta, v[i][7] + delta, unit, 3);
+    // the comparisons are false for a NaN mass, and |v| <= mass < 2^120; a block
+    // of zeros has v = delta = 0, exponent and codes 0
+    const bool done = lo == hi && (zero || (field == __float_as_uint(top + delta) >> 23 &&
+                                            field >= 40 + lg && mass[i] < 0x1p120f));
+    eb[i] = zero ? 0 : field - 2 - lg;
+    code[i] = lo;
+    if (__any(!done)) mx4_rotate_encode_f64<G, F16>(raw, i, label, eb[i], code[i]);
+    code[i] ^= signs[i];
+  }
 }
 
 // Write a quantized tile: word i of the lane covers elements 64 i + 8 c .. + 7

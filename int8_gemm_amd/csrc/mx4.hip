@@ -39,11 +39,15 @@ __global__ __launch_bounds__(64 * kWaves) void mx4_quantize_kernel(
   mx4_sign_masks(sm, label, signs);
   const int in = label ^ kMx4LaneBits<G>;
   u4 raw[4];
-  const uint16_t* src = x + row * K + kt * kMx4Tile + 8 * in;
+  // what lies outside the tensor reads its row's (or the last row's) first
+  // elements of the tile instead: no branch stands between the loads
+  const uint16_t* src = x + min(row, rows - 1) * K + kt * kMx4Tile;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    raw[i] = live && 2 * i + (in >> 2) < blocks ? *reinterpret_cast<const u4*>(src + 64 * i)
-                                                : (u4){0, 0, 0, 0};
+  for (int i = 0; i < 4; ++i) {
+    const bool here = 2 * i + (in >> 2) < blocks;
+    raw[i] = *reinterpret_cast<const u4*>(src + (here ? 64 * i + 8 * in : 0));
+    if (!here || !live) raw[i] = (u4){0, 0, 0, 0};
+  }
   uint32_t eb[4], code[4];
   mx4_quantize_tile<G, F16>(raw, label, signs, eb, code);
   if (live)

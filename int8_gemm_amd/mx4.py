@@ -18,6 +18,10 @@ __all__ = [
     "convrot_mx4_scales_size", "convrot_norm_residual", "convrot_norm_residual_mx4",
 ]
 
+# the address of a device's current stream, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
 _NORMS = {None: 0, "rms": 1, "layer": 2}
 
 
@@ -32,32 +36,36 @@ class _NormArgs(ctypes.Structure):
                    ("eps", ctypes.c_float)])
 
 
-def _tensor(t, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
-    """Check a tensor (dtype, shape, contiguity, device); its address."""
+# A small call lasts about as long on the GPU as its checks here, so each check
+# is one expression on the good path and works out what is wrong behind it.
+
+def _tensor(t, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    """Check a tensor (dtype, shape, contiguity, device index); its address."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _input16(x, name: str) -> int:
     """Check a 2-D bf16 / half input on a device; its convrot_dtype."""
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
         raise TypeError(f"{name} must be a bfloat16 or float16 tensor")
+    if x.is_cuda and x.dim() == 2 and x.is_contiguous():
+        return _DTYPES[x.dtype]
     if not x.is_cuda:
         raise ValueError(f"{name} must be on a ROCm device (got {x.device})")
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D (got shape {tuple(x.shape)})")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return _DTYPES[x.dtype]
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _dtype16(dtype) -> int:
@@ -67,39 +75,56 @@ def _dtype16(dtype) -> int:
 
 
 def _scales_shape(rows: int, k: int) -> tuple:
-    return (-(-k // 256), -(-rows // 16) * 16, 8)
+    return ((k + 255) // 256, (rows + 15) // 16 * 16, 8)
 
 
 def _quantized(codes, scales, name: str):
-    """Check a quantized tensor; (rows, k, codes address, scales address)."""
+    """Check a quantized tensor; (rows, k, codes address, scales address, device index)."""
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
-        raise TypeError(f"{name} codes must be a 2-D uint8 tensor")
-    if not codes.is_cuda:
-        raise ValueError(f"{name} codes must be on a ROCm device (got {codes.device})")
-    rows, half = codes.shape
-    dev = codes.device
-    return (rows, 2 * half, _tensor(codes, f"{name} codes", torch.uint8, (rows, half), dev),
-            _tensor(scales, f"{name} scales", torch.uint8, _scales_shape(rows, 2 * half), dev))
+        raise TypeError(f"{name}codes must be a 2-D uint8 tensor")
+    dev = codes.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}codes must be on a ROCm device (got {codes.device})")
+    rows, half = shape = codes.shape
+    return (rows, 2 * half, _tensor(codes, name + "codes", torch.uint8, shape, dev),
+            _tensor(scales, name + "scales", torch.uint8, _scales_shape(rows, 2 * half), dev), dev)
 
 
-def _new_quantized(rows: int, k: int, dev, codes, scales):
-    """The output pair of a quantization, allocated where not given."""
+def _new_quantized(rows: int, k: int, x: torch.Tensor, codes, scales):
+    """The output pair of a quantization of `x`, allocated where not given; with
+    its addresses."""
+    cs, ss = (rows, k // 2), _scales_shape(rows, k)
     if codes is None:
-        codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=dev)
-    if scales is None:
-        scales = torch.empty(_scales_shape(rows, k), dtype=torch.uint8, device=dev)
-    return (codes, scales, _tensor(codes, "codes", torch.uint8, (rows, k // 2), dev),
-            _tensor(scales, "scales", torch.uint8, _scales_shape(rows, k), dev))
-
-
-def _launch(fn, dev: torch.device, *args) -> None:
-    """Call an entry point on `dev`'s current stream (with `dev` current)."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, stream))
+        codes = torch.empty(cs, dtype=torch.uint8, device=x.device)
+        pc = codes.data_ptr()
     else:
+        pc = _tensor(codes, "codes", torch.uint8, cs, x.get_device())
+    if scales is None:
+        scales = torch.empty(ss, dtype=torch.uint8, device=x.device)
+        ps = scales.data_ptr()
+    else:
+        ps = _tensor(scales, "scales", torch.uint8, ss, x.get_device())
+    return codes, scales, pc, ps
+
+
+def _output(out, name: str, shape: tuple, dtype: torch.dtype, like: torch.Tensor):
+    """The output `out`, allocated beside `like` where it is None; with its address."""
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=like.device)
+        return out, out.data_ptr()
+    return out, _tensor(out, name, dtype, shape, like.get_device())
+
+
+def _launch(name: str, dev: int, *args) -> None:
+    """Call an entry point on device `dev`'s current stream (with `dev` current)."""
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream))
+            _launch(name, dev, *args)
+        return
+    status = fn(*args, _raw_stream(dev))
+    if status:
+        _check(status)
 
 
 def convrot_mx4_scales_size(rows: int, k: int) -> int:
@@ -114,9 +139,8 @@ def convrot_quantize_mx4(x: torch.Tensor, g: int, rot_seed: int = ROT_SEED, *,
     in groups of g (1: not rotated)."""
     dt = _input16(x, "x")
     rows, k = x.shape
-    codes, scales, pc, ps = _new_quantized(rows, k, x.device, codes, scales)
-    _launch(load_library().convrot_quantize_mx4, x.device, x.data_ptr(), dt, rows, k, g, rot_seed,
-            pc, ps)
+    codes, scales, pc, ps = _new_quantized(rows, k, x, codes, scales)
+    _launch("convrot_quantize_mx4", x.get_device(), x.data_ptr(), dt, rows, k, g, rot_seed, pc, ps)
     return codes, scales
 
 
@@ -126,11 +150,9 @@ def convrot_dequant_mx4(codes: torch.Tensor, scales: torch.Tensor, g: int,
     """The [rows, k] tensor in `dtype` that codes and scales stand for, rotated
     back in groups of g (1: the values as they are held)."""
     dt = _dtype16(dtype)
-    rows, k, pc, ps = _quantized(codes, scales, "")
-    dev = codes.device
-    out = torch.empty((rows, k), dtype=dtype, device=dev) if out is None else out
-    _launch(load_library().convrot_dequant_mx4, dev, pc, ps, rows, k, g, rot_seed,
-            _tensor(out, "out", dtype, (rows, k), dev), dt)
+    rows, k, pc, ps, dev = _quantized(codes, scales, "")
+    out, po = _output(out, "out", (rows, k), dtype, codes)
+    _launch("convrot_dequant_mx4", dev, pc, ps, rows, k, g, rot_seed, po, dt)
     return out
 
 
@@ -141,17 +163,14 @@ def convrot_gemm_mx4(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: tor
     """y [m, n] = x . w^T (+ bias) in `dtype` over two quantized tensors. `tile`
     != 0 forces a kernel variant (test / tuning hook)."""
     dt = _dtype16(dtype)
-    m, k, xc, xs = _quantized(x_codes, x_scales, "x")
-    n, kw, wc, ws = _quantized(w_codes, w_scales, "w")
-    dev = x_codes.device
-    if kw != k:
-        raise ValueError(f"K mismatch: x has {k}, w has {kw}")
-    if w_codes.device != dev:
-        raise ValueError(f"x is on {dev}, w on {w_codes.device}")
+    m, k, xc, xs, dev = _quantized(x_codes, x_scales, "x_")
+    n, kw, wc, ws, dev_w = _quantized(w_codes, w_scales, "w_")
+    if kw != k or dev_w != dev:
+        raise ValueError(f"x_codes [{m}, {k // 2}] on device {dev} do not fit w_codes "
+                         f"[{n}, {kw // 2}] on device {dev_w}")
     pb = None if bias is None else _tensor(bias, "bias", dtype, (n,), dev)
-    out = torch.empty((m, n), dtype=dtype, device=dev) if out is None else out
-    _launch(load_library().convrot_gemm_mx4, dev, xc, xs, wc, ws, pb, m, n, k,
-            _tensor(out, "out", dtype, (m, n), dev), dt, tile)
+    out, po = _output(out, "out", (m, n), dtype, x_codes)
+    _launch("convrot_gemm_mx4", dev, xc, xs, wc, ws, pb, m, n, k, po, dt, tile)
     return out
 
 
@@ -171,32 +190,30 @@ def convrot_linear_mx4(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.T
     `workspace` (uint8 on the device) defaults to the library's default size."""
     dt = _input16(x, "x")
     m, k = x.shape
-    dev = x.device
-    n, kw, wc, ws = _quantized(w_codes, w_scales, "w")
-    if kw != k:
-        raise ValueError(f"K mismatch: x has {k}, w has {kw}")
-    if w_codes.device != dev:
-        raise ValueError(f"x is on {dev}, w on {w_codes.device}")
+    n, kw, wc, ws, dev = _quantized(w_codes, w_scales, "w_")
+    if kw != k or x.get_device() != dev:
+        raise ValueError(f"x [{m}, {k}] on {x.device} does not fit w_codes [{n}, {kw // 2}] on "
+                         f"{w_codes.device}")
     pb = None if bias is None else _tensor(bias, "bias", x.dtype, (n,), dev)
-    lib = load_library()
     if workspace is None:
-        workspace = torch.empty(lib.convrot_linear_mx4_workspace_size(m, n, k),
-                                dtype=torch.uint8, device=dev)
-    pw = _tensor(workspace, "workspace", torch.uint8, tuple(workspace.shape), dev)
-    out = torch.empty((m, n), dtype=x.dtype, device=dev) if out is None else out
-    _launch(lib.convrot_linear_mx4, dev, x.data_ptr(), wc, ws, pb, m, n, k, g, rot_seed,
-            _tensor(out, "out", x.dtype, (m, n), dev), dt, pw, workspace.numel())
+        size = load_library().convrot_linear_mx4_workspace_size(m, n, k)
+        workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+        pw = workspace.data_ptr()
+    else:
+        pw = _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+        size = workspace.numel()
+    out, po = _output(out, "out", (m, n), x.dtype, x)
+    _launch("convrot_linear_mx4", dev, x.data_ptr(), wc, ws, pb, m, n, k, g, rot_seed, po, dt, pw,
+            size)
     return out
 
 
 def _modulation(t, name: str, x: torch.Tensor, samples: int):
     """Check a modulation ([k] or [b, k], rows of any stride); (address, stride, b)."""
-    if t is None:
-        return None, 0, samples
     k = x.shape[1]
     if not isinstance(t, torch.Tensor) or t.dtype != x.dtype:
         raise TypeError(f"{name} must be a {x.dtype} tensor")
-    if t.device != x.device:
+    if t.get_device() != x.get_device():
         raise ValueError(f"{name} is on {t.device}, expected {x.device}")
     if t.dim() not in (1, 2) or t.shape[-1] != k or t.stride(-1) != 1:
         raise ValueError(f"{name} must be [{k}] or [samples, {k}] with contiguous rows "
@@ -213,15 +230,14 @@ def _modulation(t, name: str, x: torch.Tensor, samples: int):
 def _norm_args(x, o, gate, post_norm, post_weight, norm, weight, scale, shift, eps, x_out):
     dt = _input16(x, "x")
     m, k = x.shape
-    dev, dtype = x.device, x.dtype
+    dev, dtype = x.get_device(), x.dtype
     if norm not in ("rms", "layer") or post_norm not in _NORMS:
         raise ValueError(f"norm={norm!r}, post_norm={post_norm!r}: 'rms' or 'layer'")
     a = _NormArgs(x=x.data_ptr(), m=m, k=k, dtype=dt, norm=_NORMS[norm],
                   post_norm=_NORMS[post_norm], eps=eps)
     if o is not None:
         a.o = _tensor(o, "o", dtype, (m, k), dev)
-        x_out = torch.empty((m, k), dtype=dtype, device=dev) if x_out is None else x_out
-        a.x_out = _tensor(x_out, "x_out", dtype, (m, k), dev)
+        x_out, a.x_out = _output(x_out, "x_out", (m, k), dtype, x)
     elif x_out is not None or gate is not None or post_norm is not None:
         raise ValueError("x_out, gate and post_norm need o")
     else:
@@ -231,9 +247,12 @@ def _norm_args(x, o, gate, post_norm, post_weight, norm, weight, scale, shift, e
     if weight is not None:
         a.weight = _tensor(weight, "weight", dtype, (k,), dev)
     samples = 0
-    a.gate, a.gate_stride, samples = _modulation(gate, "gate", x, samples)
-    a.scale, a.scale_stride, samples = _modulation(scale, "scale", x, samples)
-    a.shift, a.shift_stride, samples = _modulation(shift, "shift", x, samples)
+    if gate is not None:
+        a.gate, a.gate_stride, samples = _modulation(gate, "gate", x, samples)
+    if scale is not None:
+        a.scale, a.scale_stride, samples = _modulation(scale, "scale", x, samples)
+    if shift is not None:
+        a.shift, a.shift_stride, samples = _modulation(shift, "shift", x, samples)
     a.rows_per_mod = max(1, m // samples if samples else m)
     return a, x_out
 
@@ -252,9 +271,8 @@ def convrot_norm_residual(x: torch.Tensor, o: torch.Tensor | None = None, *,
     None. `x_out=x` updates x in place."""
     a, x_out = _norm_args(x, o, gate, post_norm, post_weight, norm, weight, scale, shift, eps,
                           x_out)
-    h = torch.empty_like(x) if h is None else h
-    a.h = _tensor(h, "h", x.dtype, tuple(x.shape), x.device)
-    _launch(load_library().convrot_norm_residual, x.device, ctypes.byref(a))
+    h, a.h = _output(h, "h", x.shape, x.dtype, x)
+    _launch("convrot_norm_residual", x.get_device(), ctypes.byref(a))
     return x_out, h
 
 
@@ -273,9 +291,9 @@ def convrot_norm_residual_mx4(x: torch.Tensor, o: torch.Tensor | None, g: int,
     convrot_quantize_mx4 of the 16-bit h. `h`, where given, is written too."""
     a, x_out = _norm_args(x, o, gate, post_norm, post_weight, norm, weight, scale, shift, eps,
                           x_out)
-    codes, scales, a.h_codes, a.h_scales = _new_quantized(*x.shape, x.device, codes, scales)
+    codes, scales, a.h_codes, a.h_scales = _new_quantized(*x.shape, x, codes, scales)
     a.g, a.rot_seed = g, rot_seed
     if h is not None:
-        a.h = _tensor(h, "h", x.dtype, tuple(x.shape), x.device)
-    _launch(load_library().convrot_norm_residual, x.device, ctypes.byref(a))
+        a.h = _tensor(h, "h", x.dtype, x.shape, x.get_device())
+    _launch("convrot_norm_residual", x.get_device(), ctypes.byref(a))
     return x_out, codes, scales

@@ -150,9 +150,9 @@ def test_binding_checks_tensors():
     with pytest.raises(TypeError):
         cr.convrot_dequant_mx4(u8, sc, 256, dtype=torch.float32)
     with pytest.raises(ValueError):
-        mx4._tensor(x, "x", torch.bfloat16, (4, 128), x.device)
+        mx4._tensor(x, "x", torch.bfloat16, (4, 128), -1)
     with pytest.raises(ValueError):
-        mx4._tensor(x.t(), "x", torch.bfloat16, (256, 4), x.device)
+        mx4._tensor(x.t(), "x", torch.bfloat16, (256, 4), -1)
 
 
 @pytest.mark.parametrize("cus", [256, 128, 3])
