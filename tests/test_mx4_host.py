@@ -157,10 +157,12 @@ def test_binding_checks_tensors():
 
 @pytest.mark.parametrize("cus", [256, 128, 3])
 def test_gemm_plans(lib, cus):
-    """Up to 64 rows take the few-rows kernel, whose blocks are 16 columns wide."""
+    """Up to 64 rows take the few-rows kernel, whose blocks are 16 to 64 columns
+    wide."""
     for m, tile in ((1, 16), (16, 16), (17, 32), (33, 64), (64, 64)):
         p = cr.convrot_plan_launch("gemm_mx4", m=m, n=3840, k=3840, compute_units=cus)
-        assert (p["tile_m"], p["tile_n"], p["grid"]) == (tile, 16, 240)
+        assert p["tile_m"] == tile and p["tile_n"] in (16, 32, 64)
+        assert p["grid"] == -(-3840 // p["tile_n"])
     p = cr.convrot_plan_launch("gemm_mx4", m=65, n=3840, k=3840, compute_units=cus)
     assert p["tile_m"] >= 128
     assert p["grid"] == -(-65 // p["tile_m"]) * -(-3840 // p["tile_n"])
