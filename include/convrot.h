@@ -454,10 +454,10 @@ convrot_status convrot_dequant_mx4(const uint8_t* codes, const uint8_t* scales, 
                                    convrot_dtype out_dtype, void* stream);
 
 /* y [m, n] = x . w^T (+ bias [n], nullable), x [m, k] and w [n, k] quantized.
- * tile: 0 = automatic; 16, 32 or 64 = the kernel for few rows (m <= tile);
- * 128, 192, 256 (tile x tile outputs), 384 (384 x 192): a test / tuning hook.
- * Any other value, or more rows than a few-rows tile holds, is
- * CONVROT_E_INVALID_ARG. */
+ * tile, a test / tuning hook: 0 = automatic; 16, 32 (m <= tile) and, for m <= 64,
+ * 64 = the kernel for few rows; otherwise 64, 128, 192, 256 (tile x tile
+ * outputs) or 384 (384 x 192). Any other value, or more rows than 16 or 32
+ * hold, is CONVROT_E_INVALID_ARG. */
 convrot_status convrot_gemm_mx4(const uint8_t* x_codes, const uint8_t* x_scales,
                                 const uint8_t* w_codes, const uint8_t* w_scales,
                                 const void* bias, int64_t m, int64_t n, int64_t k, void* y,

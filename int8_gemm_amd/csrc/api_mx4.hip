@@ -47,8 +47,8 @@ convrot_status check_mx4_gemm(const char* fn, int64_t m, int64_t n, int64_t k) {
     return fail(CONVROT_E_UNSUPPORTED_SHAPE,
                 "%s: need k %% 32 == 0, n %% 16 == 0, k <= %lld (m=%lld n=%lld k=%lld)", fn,
                 (long long)kMaxMx4K, (long long)m, (long long)n, (long long)k);
-  // the smallest block tile of the tiled kernel is 128 x 128: its count must fit the grid
-  if (((m + 127) / 128) * ((n + 127) / 128) >= kMaxDim)
+  // the smallest block tile of the tiled kernel is 64 x 64: its count must fit the grid
+  if (((m + 63) / 64) * ((n + 63) / 64) >= kMaxDim)
     return fail(CONVROT_E_UNSUPPORTED_SHAPE, "%s: output too large (m=%lld n=%lld)", fn,
                 (long long)m, (long long)n);
   return CONVROT_OK;
@@ -111,10 +111,10 @@ convrot_status convrot_gemm_mx4(const uint8_t* x_codes, const uint8_t* x_scales,
   const char* fn = "convrot_gemm_mx4";
   DType dt;
   if (!dtype_of(dtype, &dt)) return fail(CONVROT_E_INVALID_ARG, "%s: dtype=%d", fn, (int)dtype);
-  const bool few = tile == 16 || tile == 32 || tile == 64;
-  if (tile != 0 && !few && tile != 128 && tile != 192 && tile != 256 && tile != 384)
+  if (tile != 0 && tile != 16 && tile != 32 && tile != 64 && tile != 128 && tile != 192 &&
+      tile != 256 && tile != 384)
     return fail(CONVROT_E_INVALID_ARG, "%s: tile=%d not supported", fn, tile);
-  if (few && m > tile)
+  if ((tile == 16 || tile == 32) && m > tile)
     return fail(CONVROT_E_INVALID_ARG, "%s: tile=%d holds at most that many rows (m=%lld)", fn,
                 tile, (long long)m);
   if (convrot_status s = check_mx4_gemm(fn, m, n, k)) return s;

@@ -68,6 +68,18 @@ __device__ __forceinline__ v4f mfma16(v4i a, uint32_t sa, v4i b, uint32_t sb, v4
                                                           (int)sa, SEL, (int)sb);
 }
 
+// Wait until at most min(p, P) stages of LW copies are outstanding.
+template <int P, int LW>
+__device__ __forceinline__ void wait_stages(int p) {
+  if constexpr (P > 0) {
+    if (p < P) {
+      wait_stages<P - 1, LW>(p);
+      return;
+    }
+  }
+  wait_vmcnt<P * LW>();
+}
+
 template <int BM, int BN, int WM, int WN, int NS, int MINB, int NP, bool F16>
 __global__ __launch_bounds__(64 * (WM * WN + NP), MINB) void gemm_mx4_kernel(
     const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
@@ -176,20 +188,7 @@ __global__ __launch_bounds__(64 * (WM * WN + NP), MINB) void gemm_mx4_kernel(
 
   // a stage's copies are complete when at most the copies of the p later
   // stages are outstanding (copies complete in order)
-  auto wait_stage = [&](int p) {
-    if (p >= LA - 1) {
-      wait_vmcnt<(LA - 1) * LW>();
-      return;
-    }
-    if constexpr (LA - 1 > 1) {
-      if (p == 1) {
-        wait_vmcnt<(LA - 1 > 1 ? LW : 0)>();
-        return;
-      }
-    }
-    static_assert(LA <= 3, "one case per pending stage");
-    wait_vmcnt<0>();
-  };
+  auto wait_stage = [&](int p) { wait_stages<LA - 1, LW>(p); };
 
   // The output tile is staged in LDS (the ring is free after the K-loop), then
   // stored as whole rows in 16-byte pieces.
@@ -544,7 +543,9 @@ hipError_t launch_tile(const LaunchPlan& p, const Args& a) {
   switch (p.tile_m) {
     case 16: return launch_rows_n<F16, 1>(p.tile_n / 16, a);
     case 32: return launch_rows_n<F16, 2>(p.tile_n / 16, a);
-    case 64: return launch_rows_n<F16, 4>(p.tile_n / 16, a);
+    case 64:
+      if (a.m <= kFewRows) return launch_rows_n<F16, 4>(p.tile_n / 16, a);
+      return launch_cfg<F16, 64, 64, 2, 2, 4, 2>(a);
     case 128: return launch_cfg<F16, 128, 128, 2, 2, 2, 2>(a);
     case 192: return launch_cfg<F16, 192, 192, 2, 2, 3, 1, 4>(a);
     case 384: return launch_cfg<F16, 384, 192, 4, 2, 2, 1>(a);
@@ -555,20 +556,24 @@ hipError_t launch_tile(const LaunchPlan& p, const Args& a) {
 // The tiled kernel's tile of least estimated time: rounds of concurrent tiles
 // over the CUs times a round's measured duration relative to a 192 tile's
 // (K = 3840, all CUs busy: 384 x 192 39 us, 256 32-34, 192 21-24, 128 17-19 with
-// two blocks per CU and 13-15 with one). E.g. 4608 x 3840 x 3840 takes 41, 57,
-// 47 and 52 us, 16384 x 9216 x 3840 325, 304, 359 and 349 us.
+// two blocks per CU and 13-15 with one, 64 9-11 with up to two). E.g. 4608 x
+// 3840 x 3840 takes 41, 57, 47 and 52 us with the first four, 16384 x 9216 x
+// 3840 325, 304, 359 and 349 us; 128 x 3840 x 3840 8.5 us with the last, 12.7
+// with 128. Bits do not depend on the tile. Up to kFewRows rows the 64 tile is
+// left out (64 then names the few-rows kernel).
 int choose_tile(int64_t m, int64_t n, int cus) {
   const struct {
     int tile, bm, bn, per_cu;
     double round;
   } cands[] = {{384, 384, 192, 1, 1.75}, {256, 256, 256, 1, 1.45}, {192, 192, 192, 1, 1.0},
-               {128, 128, 128, 2, 0.85}};
+               {128, 128, 128, 2, 0.85}, {64, 64, 64, 2, 0.47}};
   int best = 128;
   double best_t = 1e300;
   for (const auto& c : cands) {
+    if (c.tile == 64 && m <= kFewRows) continue;
     const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
     const int64_t slots = (int64_t)(cus > 0 ? cus : 1) * c.per_cu;
-    const double rt = (c.per_cu == 2 && tiles <= cus) ? 0.65 : c.round;
+    const double rt = c.tile == 128 && tiles <= cus ? 0.65 : c.round;
     const double time = (double)((tiles + slots - 1) / slots) * rt;
     if (time < best_t * 0.999) {
       best_t = time;
@@ -589,10 +594,11 @@ LaunchPlan plan_mx4_gemm(int64_t m, int64_t n, int64_t k, int tile, int cus) {
   LaunchPlan p;
   if (tile == 0) tile = mx4_gemm_tile(m, n, m, cus);
   p.tile_m = tile;
-  p.tile_n = tile <= 64 ? 16 * rows_columns(m, n, cus > 0 ? cus : 1) : (tile == 384 ? 192 : tile);
-  p.block = tile == 128 ? 256 : 512;
+  const bool few = tile <= 64 && m <= kFewRows;
+  p.tile_n = few ? 16 * rows_columns(m, n, cus > 0 ? cus : 1) : (tile == 384 ? 192 : tile);
+  p.block = tile == 128 || (tile == 64 && !few) ? 256 : 512;
   p.grid = ((m + p.tile_m - 1) / p.tile_m) * ((n + p.tile_n - 1) / p.tile_n);
-  p.xcds = tile <= 64 ? 1 : xcd_count(cus);
+  p.xcds = few ? 1 : xcd_count(cus);
   p.passes = 1;
   return p;
 }

@@ -60,7 +60,7 @@ def test_gemm_refusals(lib):
     assert gemm(dt=7) == 1
     for tile in (-1, 1, 8, 48, 100, 512):
         assert gemm(tile=tile) == 1
-    assert gemm(m=17, tile=16) == 1 and gemm(m=65, tile=64) == 1   # more rows than it holds
+    assert gemm(m=17, tile=16) == 1 and gemm(m=33, tile=32) == 1   # more rows than it holds
     assert gemm(n=24) == 3 and gemm(k=272) == 3 and gemm(k=131104) == 3
     assert gemm(n=0) == 1 and gemm(k=0) == 1 and gemm(m=-1) == 1
     assert gemm(m=1 << 30, n=1 << 30) == 3
@@ -163,9 +163,10 @@ def test_gemm_plans(lib, cus):
         p = cr.convrot_plan_launch("gemm_mx4", m=m, n=3840, k=3840, compute_units=cus)
         assert p["tile_m"] == tile and p["tile_n"] in (16, 32, 64)
         assert p["grid"] == -(-3840 // p["tile_n"])
-    p = cr.convrot_plan_launch("gemm_mx4", m=65, n=3840, k=3840, compute_units=cus)
-    assert p["tile_m"] >= 128
-    assert p["grid"] == -(-65 // p["tile_m"]) * -(-3840 // p["tile_n"])
+    for m in (65, 1000, 32760):
+        p = cr.convrot_plan_launch("gemm_mx4", m=m, n=3840, k=3840, compute_units=cus)
+        assert p["tile_m"] in (64, 128, 192, 256, 384)
+        assert p["grid"] == -(-m // p["tile_m"]) * -(-3840 // p["tile_n"])
     with pytest.raises(cr.ConvrotError, match="UNSUPPORTED_SHAPE"):
         cr.convrot_plan_launch("gemm_mx4", m=8, n=24, k=64, compute_units=cus)
 
