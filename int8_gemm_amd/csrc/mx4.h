@@ -59,7 +59,8 @@ __device__ __forceinline__ uint32_t mx4_dpp(uint32_t v) {
 }
 constexpr int kDppXor1 = 0xB1;     // quad_perm [1,0,3,2]
 constexpr int kDppXor2 = 0x4E;     // quad_perm [2,3,0,1]
-constexpr int kDppMirror8 = 0x141; // row_half_mirror: lane j of 8 <- lane 7 - j
+constexpr int kDppMirror8 = 0x141;   // row_half_mirror: lane j of 8 <- lane 7 - j
+constexpr int kDppMirror16 = 0x140;  // row_mirror: lane j of 16 <- lane 15 - j
 
 // One exchange level: v = v + s * (the partner's v).
 template <int CTRL>

@@ -28,10 +28,19 @@ constexpr int kWaveElems = 64 * kLaneElems;     // ... and per wave
 constexpr int kRowsPerBlock = 4;                // when a row is one wave
 constexpr int kMaxWaves = 8;                    // K <= 16384
 
+// Sum over the wave, the same bits in every lane: DPP exchanges within 16
+// lanes, then swaps of 16-lane rows and of the wave's halves.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) v += __shfl_xor(v, s);
-  return v;
+  v += mx4_dpp<kDppXor1>(v);
+  v += mx4_dpp<kDppXor2>(v);
+  v += mx4_dpp<kDppMirror8>(v);
+  v += mx4_dpp<kDppMirror16>(v);
+  typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+  const uint32_t a = __float_as_uint(v);
+  const u2v r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t b = __float_as_uint(__uint_as_float(r.x) + __uint_as_float(r.y));
+  const u2v h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(h.x) + __uint_as_float(h.y);
 }
 
 // Sum over the row's waves; `part` holds one slot per wave. Two calls in a row
@@ -91,7 +100,11 @@ __device__ __forceinline__ void normalise(float (&v)[4][8], const bool (&in)[4],
 
 // G: 0 = h in 16 bits only, otherwise the rotation group of the quantized h
 // (1: none); a 16-bit h goes out as well where its pointer is set.
-template <int G, bool F16>
+// EARLY: a phase's vectors are loaded before its sums, so that their latencies
+// overlap (77 x 3840: 7.7 -> 6.5 us), otherwise where they are used, with
+// fewer registers and so more rows in flight (32760 x 5120: 244 instead of
+// 267 us).
+template <int G, bool F16, bool EARLY>
 __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs a, SignMask sm,
                                                                        int waves) {
   __shared__ float part[4 * kMaxWaves];
@@ -113,33 +126,40 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
     return in[i] ? *reinterpret_cast<const u4*>(p + 64 * i) : zero;
   };
 
-  u4 xw[4];
+  auto load4 = [&](u4 (&to)[4], const uint16_t* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) xw[i] = load(a.x + base, i);
+    for (int i = 0; i < 4; ++i) to[i] = load(p, i);
+  };
+  // v op= the unpacked chunks
+  auto multiply = [](float (&v)[4][8], const u4 (&by)[4], float add) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float w[8];
+      unpack<F16>(by[i], w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] *= add + w[e];
+    }
+  };
+
+  u4 xw[4], w1[4], w2[4], w3[4];
   float v[4][8];
+  load4(xw, a.x + base);
   if (a.o) {
+    load4(w3, a.o + base);
+    const uint16_t* gate = a.gate + mod * a.gate_stride + col;
+    if (EARLY && a.post_weight) load4(w1, a.post_weight + col);
+    if (EARLY && a.gate) load4(w2, gate);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpack<F16>(load(a.o + base, i), v[i]);
-    if (a.post_norm != NormKind::kNone) {
+    for (int i = 0; i < 4; ++i) unpack<F16>(w3[i], v[i]);
+    if (a.post_norm != NormKind::kNone)
       normalise(v, in, a.post_norm, (float)a.k, a.eps, waves, part);
-      if (a.post_weight) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float w[8];
-          unpack<F16>(load(a.post_weight + col, i), w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
-        }
-      }
+    if (a.post_weight) {
+      if (!EARLY) load4(w1, a.post_weight + col);
+      multiply(v, w1, 0.f);
     }
     if (a.gate) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float w[8];
-        unpack<F16>(load(a.gate + mod * a.gate_stride + col, i), w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
-      }
+      if (!EARLY) load4(w2, gate);
+      multiply(v, w2, 0.f);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -151,6 +171,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
       if (in[i]) *reinterpret_cast<u4*>(a.x_out + base + 64 * i) = xw[i];
     }
   }
+  const uint16_t* scale = a.scale + mod * a.scale_stride + col;
+  const uint16_t* shift = a.shift + mod * a.shift_stride + col;
+  if (EARLY && a.weight) load4(w1, a.weight + col);
+  if (EARLY && a.scale) load4(w2, scale);
+  if (EARLY && a.shift) load4(w3, shift);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     unpack<F16>(xw[i], v[i]);
@@ -160,22 +185,21 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
     }
   }
   normalise(v, in, a.norm, (float)a.k, a.eps, waves, part + 2 * kMaxWaves);
+  if (a.weight) {
+    if (!EARLY) load4(w1, a.weight + col);
+    multiply(v, w1, 0.f);
+  }
+  if (a.scale) {
+    if (!EARLY) load4(w2, scale);
+    multiply(v, w2, 1.f);
+  }
+  if (!EARLY && a.shift) load4(w3, shift);
   u4 hw[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float w[8];
-    if (a.weight) {
-      unpack<F16>(load(a.weight + col, i), w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
-    }
-    if (a.scale) {
-      unpack<F16>(load(a.scale + mod * a.scale_stride + col, i), w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] *= 1.0f + w[e];
-    }
     if (a.shift) {
-      unpack<F16>(load(a.shift + mod * a.shift_stride + col, i), w);
+      float w[8];
+      unpack<F16>(w3[i], w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] += w[e];
     }
@@ -200,10 +224,19 @@ hipError_t launch_g(const NormArgs& a, const SignMask& sm, DType dt, hipStream_t
   const int waves = (a.k + kWaveElems - 1) / kWaveElems;
   const dim3 grid((uint32_t)(waves == 1 ? (a.m + kRowsPerBlock - 1) / kRowsPerBlock : a.m));
   const dim3 block(64 * (waves == 1 ? kRowsPerBlock : waves));
-  if (dt == DType::kF16)
-    norm_residual_kernel<G, true><<<grid, block, 0, st>>>(a, sm, waves);
-  else
-    norm_residual_kernel<G, false><<<grid, block, 0, st>>>(a, sm, waves);
+  // 16 waves a CU is what the EARLY form's registers allow
+  const bool early = a.m * waves <= (int64_t)compute_units() * 16;
+  if (dt == DType::kF16) {
+    if (early)
+      norm_residual_kernel<G, true, true><<<grid, block, 0, st>>>(a, sm, waves);
+    else
+      norm_residual_kernel<G, true, false><<<grid, block, 0, st>>>(a, sm, waves);
+  } else {
+    if (early)
+      norm_residual_kernel<G, false, true><<<grid, block, 0, st>>>(a, sm, waves);
+    else
+      norm_residual_kernel<G, false, false><<<grid, block, 0, st>>>(a, sm, waves);
+  }
   return hipGetLastError();
 }
 

@@ -21,7 +21,10 @@ __all__ = [
 # the address of a device's current stream, without the Stream object around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+# no initialisation check: the callers hold device tensors
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
+_U8 = torch.uint8
 _NORMS = {None: 0, "rms": 1, "layer": 2}
 
 
@@ -80,14 +83,17 @@ def _scales_shape(rows: int, k: int) -> tuple:
 
 def _quantized(codes, scales, name: str):
     """Check a quantized tensor; (rows, k, codes address, scales address, device index)."""
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+    if (isinstance(codes, torch.Tensor) and codes.dtype is _U8 and codes.dim() == 2
+            and codes.is_cuda and codes.is_contiguous()):
+        rows, half = codes.shape
+        dev = codes.get_device()
+        return (rows, 2 * half, codes.data_ptr(),
+                _tensor(scales, name + "scales", _U8, _scales_shape(rows, 2 * half), dev), dev)
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2 or codes.dtype != _U8:
         raise TypeError(f"{name}codes must be a 2-D uint8 tensor")
-    dev = codes.get_device()
-    if dev < 0:
+    if not codes.is_cuda:
         raise ValueError(f"{name}codes must be on a ROCm device (got {codes.device})")
-    rows, half = shape = codes.shape
-    return (rows, 2 * half, _tensor(codes, name + "codes", torch.uint8, shape, dev),
-            _tensor(scales, name + "scales", torch.uint8, _scales_shape(rows, 2 * half), dev), dev)
+    raise ValueError(f"{name}codes must be contiguous")
 
 
 def _new_quantized(rows: int, k: int, x: torch.Tensor, codes, scales):
@@ -95,15 +101,15 @@ def _new_quantized(rows: int, k: int, x: torch.Tensor, codes, scales):
     its addresses."""
     cs, ss = (rows, k // 2), _scales_shape(rows, k)
     if codes is None:
-        codes = torch.empty(cs, dtype=torch.uint8, device=x.device)
+        codes = torch.empty(cs, dtype=_U8, device=x.device)
         pc = codes.data_ptr()
     else:
-        pc = _tensor(codes, "codes", torch.uint8, cs, x.get_device())
+        pc = _tensor(codes, "codes", _U8, cs, x.get_device())
     if scales is None:
-        scales = torch.empty(ss, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(ss, dtype=_U8, device=x.device)
         ps = scales.data_ptr()
     else:
-        ps = _tensor(scales, "scales", torch.uint8, ss, x.get_device())
+        ps = _tensor(scales, "scales", _U8, ss, x.get_device())
     return codes, scales, pc, ps
 
 
@@ -115,14 +121,19 @@ def _output(out, name: str, shape: tuple, dtype: torch.dtype, like: torch.Tensor
     return out, _tensor(out, name, dtype, shape, like.get_device())
 
 
+_entry = {}  # entry points by name, bound at their first call
+
+
 def _launch(name: str, dev: int, *args) -> None:
     """Call an entry point on device `dev`'s current stream (with `dev` current)."""
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() != dev:
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(load_library(), name)
+    if _current_device() != dev:
         with torch.cuda.device(dev):
-            _launch(name, dev, *args)
-        return
-    status = fn(*args, _raw_stream(dev))
+            status = fn(*args, _raw_stream(dev))
+    else:
+        status = fn(*args, _raw_stream(dev))
     if status:
         _check(status)
 
@@ -197,10 +208,10 @@ def convrot_linear_mx4(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.T
     pb = None if bias is None else _tensor(bias, "bias", x.dtype, (n,), dev)
     if workspace is None:
         size = load_library().convrot_linear_mx4_workspace_size(m, n, k)
-        workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(size, dtype=_U8, device=x.device)
         pw = workspace.data_ptr()
     else:
-        pw = _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+        pw = _tensor(workspace, "workspace", _U8, (workspace.numel(),), dev)
         size = workspace.numel()
     out, po = _output(out, "out", (m, n), x.dtype, x)
     _launch("convrot_linear_mx4", dev, x.data_ptr(), wc, ws, pb, m, n, k, g, rot_seed, po, dt, pw,

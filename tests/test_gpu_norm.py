@@ -233,6 +233,26 @@ def test_a_block_of_layers_captured_and_replayed():
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), rep
 
 
+def test_grids_that_fill_the_card_give_the_same_bits():
+    """Rows beyond what the CUs hold at once take a form with fewer registers; a
+    card of one CU takes it for a few rows already."""
+    rng = np.random.default_rng(12)
+    for k in (1024, 5120):
+        x, o, kw = build(rng, 24, k, torch.bfloat16, 2, "layer", True, True)
+        want = cr.convrot_norm_residual(x, o, **kw)
+        quantized = cr.convrot_norm_residual_mx4(x, o, 256, SEED, **kw)
+        try:
+            cr.convrot_set_compute_units(1)
+            got = cr.convrot_norm_residual(x, o, **kw)
+            again = cr.convrot_norm_residual_mx4(x, o, 256, SEED, **kw)
+        finally:
+            cr.convrot_set_compute_units(0)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        check(x, o, got[0], got[1], kw)
+        assert torch.equal(again[1], quantized[1])
+        assert torch.equal(again[2][:, :24], quantized[2][:, :24])
+
+
 def test_no_rows():
     x = torch.empty((0, 256), dtype=torch.bfloat16, device=DEV)
     x_out, h = cr.convrot_norm_residual(x, torch.empty_like(x))
