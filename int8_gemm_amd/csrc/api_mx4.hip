@@ -143,7 +143,7 @@ size_t convrot_linear_mx4_workspace_for_rows(int64_t rows, int64_t k) {
 size_t convrot_linear_mx4_workspace_size(int64_t m, int64_t n, int64_t k) {
   if (m < 0 || n <= 0 || k <= 0) return 0;
   // at least 8192 rows: a narrow layer's short slices are bound by their launches
-  // (5518 x 144 x 6080 in 13 slices of 432 rows 298 us, in one NARROW_US)
+  // (5518 x 144 x 6080 in 13 slices of 432 rows 298 us, in one 30)
   int64_t rows = 3 * n > 8192 ? 3 * n : 8192;
   if (rows > m) rows = m < 1 ? 1 : m;
   return convrot_linear_mx4_workspace_for_rows(rows, k);

@@ -11,7 +11,9 @@
 // pre() reads x' as it was rounded, so that h is a function of the x' that the
 // caller gets. Everything else is fp32.
 //
-// Bound by memory: x and o are read once, x' and h written once; the row stays
+// Bound by memory: x and o are read once, x' and h written once (32760 x 5120:
+// 1.34 GB, 242 us = 5.5 TB/s, a large device copy reaches 5.1; with h quantized
+// 265 us, 4.1 TB/s, the rotation's arithmetic on top); the row stays
 // in registers between the norms (32 elements a lane, in the tile layout of
 // mx4.h). A row takes ceil(K / 2048) waves; rows of one wave share a block of
 // four. Variances are taken in two passes over the registers, around the mean.

@@ -3,6 +3,8 @@ call, sizes and launch plans are host arithmetic, and the oracle's own pins."""
 
 import ctypes
 import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -170,6 +172,40 @@ def test_gemm_plans(lib, cus):
         assert p["grid"] == -(-m // p["tile_m"]) * -(-3840 // p["tile_n"])
     with pytest.raises(cr.ConvrotError, match="UNSUPPORTED_SHAPE"):
         cr.convrot_plan_launch("gemm_mx4", m=8, n=24, k=64, compute_units=cus)
+
+
+def test_header_compiles_and_links_as_c99(lib, tmp_path):
+    cc = shutil.which("gcc")
+    if cc is None:
+        pytest.skip("no gcc")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = os.path.join(root, "tests", "c", "header_mx4_c99.c")
+    r = subprocess.run([cc, "-std=c99", "-pedantic", "-Wall", "-Werror", "-fPIC", "-shared",
+                        "-I", os.path.join(root, "include"), src, "-o", str(tmp_path / "h.so"),
+                        cr.library_path(), "-Wl,--no-undefined",
+                        "-Wl,--unresolved-symbols=ignore-in-shared-libs"],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_norm_args_match_the_header(lib, tmp_path):
+    """The binding's structure has the size and offsets of convrot_norm_args."""
+    cc = shutil.which("gcc")
+    if cc is None:
+        pytest.skip("no gcc")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    fields = [f for f, _ in mx4._NormArgs._fields_]
+    src = tmp_path / "o.c"
+    src.write_text("#include <stdio.h>\n#include <stddef.h>\n#include \"convrot.h\"\nint main(void) {"
+                   + "".join(f'printf("%zu ", offsetof(convrot_norm_args, {f}));' for f in fields)
+                   + 'printf("%zu", sizeof(convrot_norm_args)); return 0; }')
+    exe = tmp_path / "o"
+    subprocess.run([cc, "-std=c99", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)],
+                   check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    assert got == [getattr(mx4._NormArgs, f).offset for f in fields] \
+        + [ctypes.sizeof(mx4._NormArgs)]
 
 
 def test_oracle_pins():
