@@ -433,8 +433,9 @@ size_t convrot_linear_int8_workspace_size(int64_t m, int64_t n, int64_t k);
  *             last bit can differ between calls on either side of that.
  *   linear:   gemm(quantize(x), w), whatever the slices.
  *
- * Shapes: k % 32 == 0, k % g == 0, k <= 131072; n % 16 == 0 for the product;
- * rows < 2^31. Alignment: 16 bytes (bias 8, workspace 256). The conventions at
+ * Shapes: k % 32 == 0, k % g == 0, k <= 131072, ceil(rows/8) * ceil(k/256) <
+ * 2^26; for the product n % 16 == 0, n < 2^27 and ceil(m/64) * ceil(n/64) < 2^24.
+ * Alignment: 16 bytes (bias 8, workspace 256). The conventions at
  * the top of this file hold, m == 0 included; dtype is the 16-bit format of x,
  * bias, y and out. */
 
@@ -495,7 +496,8 @@ size_t convrot_linear_mx4_workspace_size(int64_t m, int64_t n, int64_t k);
  *   gate, scale, shift: one [k] row per sample; row r of x takes modulation
  *     row r / rows_per_mod, `*_stride` elements apart (a multiple of 8; 0 = one
  *     row for all), so they can be column ranges of one wider tensor.
- * k % 8 == 0, k <= 16384; quantized also k % 32 == 0 and k % g == 0. */
+ * k % 8 == 0, k <= 16384, m * ceil(k/2048) < 2^26; quantized also k % 32 == 0 and
+ * k % g == 0. */
 typedef enum convrot_norm_kind {
   CONVROT_NORM_NONE = 0,
   CONVROT_NORM_RMS = 1,

@@ -30,8 +30,8 @@ convrot_status check_mx4(const char* fn, int64_t rows, int64_t k, int g) {
                 (long long)k, g);
   if (k % kMx4Block || k > kMaxMx4K || rows >= kMaxDim || !mx4_grid_fits(rows, k))
     return fail(CONVROT_E_UNSUPPORTED_SHAPE,
-                "%s: need k %% 32 == 0, k <= %lld, rows < 2^31 (rows=%lld k=%lld)", fn,
-                (long long)kMaxMx4K, (long long)rows, (long long)k);
+                "%s: need k %% 32 == 0, k <= %lld, ceil(rows/8) * ceil(k/256) < 2^26 "
+                "(rows=%lld k=%lld)", fn, (long long)kMaxMx4K, (long long)rows, (long long)k);
   return CONVROT_OK;
 }
 
@@ -47,8 +47,10 @@ convrot_status check_mx4_gemm(const char* fn, int64_t m, int64_t n, int64_t k) {
     return fail(CONVROT_E_UNSUPPORTED_SHAPE,
                 "%s: need k %% 32 == 0, n %% 16 == 0, k <= %lld (m=%lld n=%lld k=%lld)", fn,
                 (long long)kMaxMx4K, (long long)m, (long long)n, (long long)k);
-  // the smallest block tile of the tiled kernel is 64 x 64: its count must fit the grid
-  if (((m + 63) / 64) * ((n + 63) / 64) >= kMaxDim)
+  // grids: 64 x 64 tiles of four waves, 16 columns a block of eight waves for few rows;
+  // the kernels' row indices run up to a tile beyond m and n
+  if (((m + 63) / 64) * ((n + 63) / 64) * 4 > kMaxLaunchWaves || n / 16 * 8 > kMaxLaunchWaves ||
+      m > kMaxDim - 1024)
     return fail(CONVROT_E_UNSUPPORTED_SHAPE, "%s: output too large (m=%lld n=%lld)", fn,
                 (long long)m, (long long)n);
   return CONVROT_OK;
@@ -225,9 +227,9 @@ convrot_status convrot_norm_residual(const convrot_norm_args* args, void* stream
   if (quantized) {
     if (convrot_status s = check_mx4(fn, m, k, a.g)) return s;
   }
-  if (k % 8 || k > kMaxNormK || m >= kMaxDim)
+  if (k % 8 || k > kMaxNormK || m >= kMaxDim || !norm_grid_fits(m, k))
     return fail(CONVROT_E_UNSUPPORTED_SHAPE,
-                "%s: need k %% 8 == 0, k <= %lld, m < 2^31 (m=%lld k=%lld)", fn,
+                "%s: need k %% 8 == 0, k <= %lld, m * ceil(k/2048) < 2^26 (m=%lld k=%lld)", fn,
                 (long long)kMaxNormK, (long long)m, (long long)k);
   const bool mods = a.gate || a.scale || a.shift;
   if (mods && a.rows_per_mod < 1)
@@ -291,7 +293,7 @@ convrot_status convrot_norm_residual(const convrot_norm_args* args, void* stream
   n.h_codes = a.h_codes;
   n.h_scales = a.h_scales;
   n.m = m;
-  n.rows_per_mod = mods ? a.rows_per_mod : m;
+  n.rows_per_mod = mods && a.rows_per_mod < m ? a.rows_per_mod : m;
   n.k = (int)k;
   n.post_norm = (NormKind)a.post_norm;
   n.norm = (NormKind)a.norm;

@@ -37,6 +37,7 @@
 // stream of x: 13824 x 5120 (37.6 MB) takes 10.4 us with one row, 3.6 TB/s of
 // the weight's bytes, 13 with 32 and 24 with 64.
 
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -505,12 +506,17 @@ hipError_t launch_cfg(const Args& a) {
   constexpr int lds_bytes = ring_bytes > tile_bytes ? ring_bytes : tile_bytes;
   static_assert(lds_bytes <= 160 * 1024, "LDS");
   auto kern = gemm_mx4_kernel<BM, BN, WM, WN, NS, MINB, NP, F16>;
-  static bool attr = false;  // benign race: the call is idempotent
-  if (!attr) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
+  // once per device (a second thread may repeat it: the call is idempotent)
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
     if (e != hipSuccess) return e;
-    attr = true;
+    done.fetch_or(bit, std::memory_order_relaxed);
   }
   const int tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + BN - 1) / BN;
   hipLaunchKernelGGL(kern, dim3(tiles_m * tiles_n), dim3(64 * (WM * WN + NP)), lds_bytes, a.st,

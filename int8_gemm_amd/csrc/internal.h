@@ -100,6 +100,8 @@ hipError_t launch_check_rows(const uint16_t* x, const uint16_t* w_hat, const uin
 
 
 // ---- microscaled 4-bit (MXFP4) tensors; layout in mx4.h ----
+// Waves of one launch: a grid counts its threads in 32 bits.
+constexpr int64_t kMaxLaunchWaves = ((int64_t)1 << 26) - 1;
 // The signs of one group, repeated over a 256-element tile.
 SignMask mx4_tile_signs(const SignMask& sm, int g);
 // Whether [rows, k] fits the grids of the two kernels below.
@@ -128,6 +130,7 @@ struct NormArgs {
   NormKind post_norm, norm;
   float eps;
 };
+bool norm_grid_fits(int64_t m, int64_t k);
 // g = 0: h in 16 bits; otherwise h is also rotated in groups of g (1: not) and quantized.
 hipError_t launch_norm_residual(const NormArgs& a, int g, const SignMask& sm, DType dt,
                                 hipStream_t st);

@@ -35,7 +35,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx4_quantize_kernel(
     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   const int lane = threadIdx.x & 63;
   const int label = mx4_label(lane);
-  const uint32_t unit = blockIdx.x * kWaves + (threadIdx.x >> 6);  // < 2^31 (checked by the host)
+  const uint32_t unit = blockIdx.x * kWaves + (threadIdx.x >> 6);  // < 2^26 (checked by the host)
   const int kt = (int)(unit % (uint32_t)tiles);
   const int64_t row = (int64_t)(unit / (uint32_t)tiles) * kRowsPerWave + (lane >> 3);
   const int blocks = min(8, (K - kt * kMx4Tile) / kMx4Block);
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx4_dequant_kernel(
     SignMask sm, int tiles, uint16_t* __restrict__ out) {
   const int lane = threadIdx.x & 63;
   const int label = mx4_label(lane);
-  const uint32_t unit = blockIdx.x * kWaves + (threadIdx.x >> 6);  // < 2^31 (checked by the host)
+  const uint32_t unit = blockIdx.x * kWaves + (threadIdx.x >> 6);
   const int kt = (int)(unit % (uint32_t)tiles);
   const int64_t row = (int64_t)(unit / (uint32_t)tiles) * kRowsPerWave + (lane >> 3);
   const int blocks = min(8, (K - kt * kMx4Tile) / kMx4Block);
@@ -164,7 +164,7 @@ SignMask mx4_tile_signs(const SignMask& sm, int g) {
 }
 
 bool mx4_grid_fits(int64_t rows, int64_t k) {
-  return wave_units(rows, (k + kMx4Tile - 1) / kMx4Tile) < ((int64_t)1 << 31) - kWaves;
+  return wave_units(rows, (k + kMx4Tile - 1) / kMx4Tile) <= kMaxLaunchWaves - kWaves;
 }
 
 hipError_t launch_mx4_quantize(const uint16_t* x, int64_t rows, int K, int g, const SignMask& sm,

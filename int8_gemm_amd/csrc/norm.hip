@@ -119,7 +119,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
   const int tile = (waves == 1 ? 0 : wave * 8) + (lane >> 3);
   const int col = tile * kMx4Tile + 8 * lab_in;  // + 64 i
   const int64_t base = row * a.k + col;
-  const int64_t mod = row / a.rows_per_mod;
+  const int64_t mod = (uint32_t)row / (uint32_t)a.rows_per_mod;  // both below 2^31
   bool in[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) in[i] = col + 64 * i < a.k;
@@ -243,6 +243,10 @@ hipError_t launch_g(const NormArgs& a, const SignMask& sm, DType dt, hipStream_t
 }
 
 }  // namespace
+
+bool norm_grid_fits(int64_t m, int64_t k) {
+  return m * ((k + kWaveElems - 1) / kWaveElems) <= kMaxLaunchWaves - kRowsPerBlock;
+}
 
 hipError_t launch_norm_residual(const NormArgs& a, int g, const SignMask& sm, DType dt,
                                 hipStream_t st) {

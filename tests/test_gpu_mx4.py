@@ -146,6 +146,27 @@ def test_quantize_leaves_padding_rows_and_what_lies_behind():
     assert_quantized(codes[:m], scales, f64(x), 16)
 
 
+@pytest.mark.parametrize("g", [4, 16, 64, 256])
+def test_quantize_of_values_on_every_border(g):
+    """Small integers and repeated values: most rotated elements lie on borders
+    of codes or exponents, where sums in fp32 with an error bound decide nothing."""
+    rng = np.random.default_rng(g)
+    k = 2048
+    x = np.zeros((40, k))
+    x[:8] = rng.integers(-2, 3, (8, k))
+    x[8:12] = rng.choice([-1.0, 1.0], (4, k))
+    x[12:16] = np.repeat(rng.integers(-9, 10, (4, k // 64)), 64, -1)
+    x[16:20, ::g] = rng.integers(-9, 10, (4, k // g))
+    x[20] = 1.0
+    x[21] = 2.0 ** -60
+    x[22:30] = rng.integers(-128, 129, (8, k)) * 2.0 ** 40
+    x[30:, :1024] = rng.standard_normal((10, 1024))    # half a row of zeros
+    for dtype in DTYPES:
+        t = dev(np.where(np.abs(x) < 60000, x, 1.0) if dtype == torch.float16 else x, dtype)
+        codes, scales = cr.convrot_quantize_mx4(t, g, SEED)
+        assert_quantized(codes, scales, f64(t), g)
+
+
 @pytest.mark.parametrize("seed", [0, 2 ** 64 - 1])
 def test_quantize_takes_the_rotation_seed(seed):
     rng = np.random.default_rng(7)

@@ -184,6 +184,24 @@ def test_quantized_h_is_the_16_bit_h_quantized(g, m, k, dtype):
     assert torch.equal(again[1], want[0])
 
 
+def test_last_sample_may_be_short():
+    """The C call: row r takes modulation row r / rows_per_mod, here 4, 4 and 2 rows."""
+    import ctypes
+
+    from int8_gemm_amd import mx4
+    rng = np.random.default_rng(8)
+    m, k = 10, 264
+    x = dev(rng.standard_normal((m, k)), torch.float16)
+    scale = dev(rng.standard_normal((3, 2 * k)), torch.float16)
+    h = torch.empty_like(x)
+    a = mx4._NormArgs(x=x.data_ptr(), h=h.data_ptr(), m=m, k=k, rows_per_mod=4, norm=1, dtype=1,
+                      eps=EPS, scale=scale.data_ptr(), scale_stride=2 * k)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert cr.load_library().convrot_norm_residual(ctypes.byref(a), stream) == 0
+    full = scale[[0, 0, 0, 0, 1, 1, 1, 1, 2, 2], :k]
+    check(x, None, x, h, {"scale": full})
+
+
 def test_a_block_of_layers_captured_and_replayed():
     """Two blocks as a model would run them: norm into 4 bits, projection, gated
     residual and norm into the next projection; graph replays equal eager runs,

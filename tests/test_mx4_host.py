@@ -42,6 +42,9 @@ def test_quantize_and_dequant_refusals(lib):
     assert q(A, 2, 8, 256, 1, 1, B, C, None) == 1          # format
     assert q(A, 0, -1, 256, 1, 1, B, C, None) == 1
     assert q(A, 0, 1 << 31, 256, 1, 1, B, C, None) == 3
+    # grids count their threads in 32 bits
+    assert q(A, 0, 1 << 29, 32, 1, 1, B, C, None) == 3
+    assert d(A, B, 1 << 20, 131072, 1, 1, C, 0, None) == 3
     for bad in ((None, B, C), (A, None, C), (A, B, None)):
         assert q(bad[0], 0, 8, 256, 1, 1, bad[1], bad[2], None) == 1
         assert d(bad[0], bad[1], 8, 256, 1, 1, bad[2], 0, None) == 1
@@ -65,7 +68,8 @@ def test_gemm_refusals(lib):
     assert gemm(m=17, tile=16) == 1 and gemm(m=33, tile=32) == 1   # more rows than it holds
     assert gemm(n=24) == 3 and gemm(k=272) == 3 and gemm(k=131104) == 3
     assert gemm(n=0) == 1 and gemm(k=0) == 1 and gemm(m=-1) == 1
-    assert gemm(m=1 << 30, n=1 << 30) == 3
+    assert gemm(m=1 << 30, n=1 << 30) == 3 and gemm(m=(1 << 31) - 1) == 3
+    assert gemm(n=1 << 27) == 3 and gemm(m=1 << 30, n=16, k=32) == 3
     for name in ("xc", "xs", "wc", "ws", "y"):
         assert gemm(**{name: None}) == 1
         assert gemm(**{name: F + 8}) == 4
@@ -113,7 +117,7 @@ def test_norm_refusals(lib):
     assert st(dtype=2) == 1 and st(norm=0) == 1 and st(norm=3) == 1 and st(post_norm=4) == 1
     assert st(eps=float("nan")) == 1 and st(eps=-1.0) == 1 and st(eps=float("inf")) == 1
     assert st(m=-1) == 1 and st(k=0) == 1 and st(k=12) == 3 and st(k=16392) == 3
-    assert st(m=1 << 31) == 3
+    assert st(m=1 << 31) == 3 and st(m=1 << 26, k=8) == 3 and st(m=1 << 25, k=2056) == 3
     assert st(x=None) == 1 and st(h=None) == 1 and st(x_out=None) == 1
     # what needs o
     assert st(o=None) == 1 and st(o=None, x_out=None, gate=E) == 1
