@@ -96,17 +96,22 @@ def _quantized(codes, scales, name: str):
     raise ValueError(f"{name}codes must be contiguous")
 
 
+def _empty(rows: int, cols: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """torch.empty((rows, cols)) at a quarter less host time."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 def _new_quantized(rows: int, k: int, x: torch.Tensor, codes, scales):
     """The output pair of a quantization of `x`, allocated where not given; with
     its addresses."""
     cs, ss = (rows, k // 2), _scales_shape(rows, k)
     if codes is None:
-        codes = torch.empty(cs, dtype=_U8, device=x.device)
+        codes = _empty(rows, k // 2, _U8, x.device)
         pc = codes.data_ptr()
     else:
         pc = _tensor(codes, "codes", _U8, cs, x.get_device())
     if scales is None:
-        scales = torch.empty(ss, dtype=_U8, device=x.device)
+        scales = torch.empty_strided(ss, (8 * ss[1], 8, 1), dtype=_U8, device=x.device)
         ps = scales.data_ptr()
     else:
         ps = _tensor(scales, "scales", _U8, ss, x.get_device())
@@ -116,7 +121,7 @@ def _new_quantized(rows: int, k: int, x: torch.Tensor, codes, scales):
 def _output(out, name: str, shape: tuple, dtype: torch.dtype, like: torch.Tensor):
     """The output `out`, allocated beside `like` where it is None; with its address."""
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=like.device)
+        out = _empty(*shape, dtype, like.device)
         return out, out.data_ptr()
     return out, _tensor(out, name, dtype, shape, like.get_device())
 
@@ -208,7 +213,7 @@ def convrot_linear_mx4(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.T
     pb = None if bias is None else _tensor(bias, "bias", x.dtype, (n,), dev)
     if workspace is None:
         size = load_library().convrot_linear_mx4_workspace_size(m, n, k)
-        workspace = torch.empty(size, dtype=_U8, device=x.device)
+        workspace = torch.empty_strided((size,), (1,), dtype=_U8, device=x.device)
         pw = workspace.data_ptr()
     else:
         pw = _tensor(workspace, "workspace", _U8, (workspace.numel(),), dev)
