@@ -224,23 +224,25 @@ def convrot_linear_mx4(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.T
     return out
 
 
-def _modulation(t, name: str, x: torch.Tensor, samples: int):
-    """Check a modulation ([k] or [b, k], rows of any stride); (address, stride, b)."""
-    k = x.shape[1]
+def _modulation(t, name: str, x: torch.Tensor, m: int, k: int, samples: int):
+    """Check a modulation ([k] or [b, k], rows of any stride) against the `samples`
+    of those before it (0: none yet); (address, row stride, samples)."""
     if not isinstance(t, torch.Tensor) or t.dtype != x.dtype:
         raise TypeError(f"{name} must be a {x.dtype} tensor")
+    shape, strides = t.shape, t.stride()
     if t.get_device() != x.get_device():
         raise ValueError(f"{name} is on {t.device}, expected {x.device}")
-    if t.dim() not in (1, 2) or t.shape[-1] != k or t.stride(-1) != 1:
+    if len(shape) not in (1, 2) or shape[-1] != k or strides[-1] != 1:
         raise ValueError(f"{name} must be [{k}] or [samples, {k}] with contiguous rows "
-                         f"(got shape {tuple(t.shape)}, strides {t.stride()})")
-    if t.dim() == 1 or t.shape[0] == 1:
+                         f"(got shape {tuple(shape)}, strides {strides})")
+    b = shape[0]
+    if len(shape) == 1 or b == 1:
         return t.data_ptr(), 0, samples
-    if samples not in (0, t.shape[0]):
-        raise ValueError(f"{name} has {t.shape[0]} samples, another modulation {samples}")
-    if t.shape[0] == 0 or x.shape[0] % t.shape[0]:
-        raise ValueError(f"{x.shape[0]} rows do not divide into {t.shape[0]} samples")
-    return t.data_ptr(), t.stride(0), t.shape[0]
+    if samples not in (0, b):
+        raise ValueError(f"{name} has {b} samples, another modulation {samples}")
+    if b == 0 or m % b:
+        raise ValueError(f"{m} rows do not divide into {b} samples")
+    return t.data_ptr(), strides[0], b
 
 
 def _norm_args(x, o, gate, post_norm, post_weight, norm, weight, scale, shift, eps, x_out):
@@ -264,11 +266,11 @@ def _norm_args(x, o, gate, post_norm, post_weight, norm, weight, scale, shift, e
         a.weight = _tensor(weight, "weight", dtype, (k,), dev)
     samples = 0
     if gate is not None:
-        a.gate, a.gate_stride, samples = _modulation(gate, "gate", x, samples)
+        a.gate, a.gate_stride, samples = _modulation(gate, "gate", x, m, k, samples)
     if scale is not None:
-        a.scale, a.scale_stride, samples = _modulation(scale, "scale", x, samples)
+        a.scale, a.scale_stride, samples = _modulation(scale, "scale", x, m, k, samples)
     if shift is not None:
-        a.shift, a.shift_stride, samples = _modulation(shift, "shift", x, samples)
+        a.shift, a.shift_stride, samples = _modulation(shift, "shift", x, m, k, samples)
     a.rows_per_mod = max(1, m // samples if samples else m)
     return a, x_out
 

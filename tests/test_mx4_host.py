@@ -162,6 +162,22 @@ def test_binding_checks_tensors():
         mx4._tensor(x.t(), "x", torch.bfloat16, (256, 4), -1)
 
 
+def test_binding_checks_modulations():
+    x = torch.zeros((8, 64), dtype=torch.bfloat16)
+    mod = torch.zeros((4, 192), dtype=torch.bfloat16)
+
+    def call(t, samples=0):
+        return mx4._modulation(t, "gate", x, 8, 64, samples)
+    assert call(mod[:, 64:128]) == (mod.data_ptr() + 128, 192, 4)
+    assert call(mod[:1, :64]) == (mod.data_ptr(), 0, 0) and call(mod[0, :64], 4)[1:] == (0, 4)
+    with pytest.raises(TypeError):
+        call(mod.float())
+    for bad, samples in ((mod, 0), (mod[:3, :64], 0), (mod[:, :64], 2), (mod[:, ::3], 0),
+                         (mod[:0, :64], 0), (mod[None, :, :64], 0)):
+        with pytest.raises(ValueError):
+            call(bad, samples)
+
+
 @pytest.mark.parametrize("cus", [256, 128, 3])
 def test_gemm_plans(lib, cus):
     """Up to 64 rows take the few-rows kernel, whose blocks are 16 to 64 columns
