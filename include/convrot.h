@@ -429,8 +429,9 @@ size_t convrot_linear_int8_workspace_size(int64_t m, int64_t n, int64_t k);
  *   dequant:  W_hat = RN16((v 2^e) . blockdiag(R)^T), sums in fp32.
  *   gemm:     y = RN16(sum over k in fp32 [+ bias[n] in fp32]); a NaN block makes
  *             its row (column) of y NaN. Results are bit-identical from run to
- *             run. The order of the sum depends on whether m <= 64, so a row's
- *             last bit can differ between calls on either side of that.
+ *             run and do not depend on the device's compute units. The order
+ *             of the sum is one of two, chosen by (m, n, k) for m <= 64, so a
+ *             row's last bit can differ between calls of different m.
  *   linear:   gemm(quantize(x), w), whatever the slices.
  *
  * Shapes: k % 32 == 0, k % g == 0, k <= 131072, ceil(rows/8) * ceil(k/256) <
@@ -455,10 +456,9 @@ convrot_status convrot_dequant_mx4(const uint8_t* codes, const uint8_t* scales, 
                                    convrot_dtype out_dtype, void* stream);
 
 /* y [m, n] = x . w^T (+ bias [n], nullable), x [m, k] and w [n, k] quantized.
- * tile, a test / tuning hook: 0 = automatic; 16, 32 (m <= tile) and, for m <= 64,
- * 64 = the kernel for few rows; otherwise 64, 128, 192, 256 (tile x tile
- * outputs) or 384 (384 x 192). Any other value, or more rows than 16 or 32
- * hold, is CONVROT_E_INVALID_ARG. */
+ * tile, a test / tuning hook: 0 = automatic, 16 = the kernel for few rows (m <=
+ * 64), 64, 128, 192, 256 (tile x tile outputs) or 384 (384 x 192) = the tiled
+ * kernel. Any other value, or 16 with more rows, is CONVROT_E_INVALID_ARG. */
 convrot_status convrot_gemm_mx4(const uint8_t* x_codes, const uint8_t* x_scales,
                                 const uint8_t* w_codes, const uint8_t* w_scales,
                                 const void* bias, int64_t m, int64_t n, int64_t k, void* y,

@@ -113,12 +113,12 @@ convrot_status convrot_gemm_mx4(const uint8_t* x_codes, const uint8_t* x_scales,
   const char* fn = "convrot_gemm_mx4";
   DType dt;
   if (!dtype_of(dtype, &dt)) return fail(CONVROT_E_INVALID_ARG, "%s: dtype=%d", fn, (int)dtype);
-  if (tile != 0 && tile != 16 && tile != 32 && tile != 64 && tile != 128 && tile != 192 &&
-      tile != 256 && tile != 384)
+  if (tile != 0 && tile != 16 && tile != 64 && tile != 128 && tile != 192 && tile != 256 &&
+      tile != 384)
     return fail(CONVROT_E_INVALID_ARG, "%s: tile=%d not supported", fn, tile);
-  if ((tile == 16 || tile == 32) && m > tile)
-    return fail(CONVROT_E_INVALID_ARG, "%s: tile=%d holds at most that many rows (m=%lld)", fn,
-                tile, (long long)m);
+  if (tile == 16 && m > 64)
+    return fail(CONVROT_E_INVALID_ARG, "%s: tile=16 takes at most 64 rows (m=%lld)", fn,
+                (long long)m);
   if (convrot_status s = check_mx4_gemm(fn, m, n, k)) return s;
   if (!w_codes || !w_scales) return fail(CONVROT_E_INVALID_ARG, "%s: null pointer", fn);
   if (m == 0) return ok();  // the M-sized buffers may be null
@@ -199,7 +199,7 @@ convrot_status convrot_linear_mx4(const void* x, const uint8_t* w_codes, const u
     if (e != hipSuccess) return hip_status(e, fn);
     e = launch_mx4_gemm(codes, scales, w_codes, w_scales, static_cast<const uint16_t*>(bias), rows,
                         n, k, static_cast<uint16_t*>(y) + r0 * n,
-                        mx4_gemm_tile(rows, n, m, compute_units()), dt, st);
+                        mx4_gemm_tile(rows, n, k, m, compute_units()), dt, st);
     if (e != hipSuccess) return hip_status(e, fn);
   }
   return ok();

@@ -34,8 +34,9 @@
 // 16 rows of the weight straight into registers, 128 bytes of a row at a time,
 // each weight byte once for all rows; the partial sums are joined in LDS in
 // wave order. Bound by the weight's bytes and, with more rows, by each CU's
-// stream of x: 13824 x 5120 (37.6 MB) takes 10.4 us with one row, 3.6 TB/s of
-// the weight's bytes, 13 with 32 and 24 with 64.
+// loads of x: 13824 x 5120 (37.6 MB) takes 9.9 us with one row, 3.8 TB/s of the
+// weight's bytes. Where those loads take longer than the copies of 64 x 64
+// tiles would, the tiled kernel is taken (few_rows below).
 
 #include <atomic>
 #include <type_traits>
@@ -532,21 +533,40 @@ hipError_t launch_rows(const Args& a) {
   return hipGetLastError();
 }
 
-// Columns per block of the few-rows kernel, in groups of 16. A block streams
-// its own rows of the weight and all of x, so a CU's bytes go with (columns + m)
-// times the blocks that it gets.
-int rows_columns(int64_t m, int64_t n, int cus) {
-  int best = 1;
-  int64_t best_c = INT64_MAX;
-  for (int nf = 1; nf <= 4; nf *= 2) {
-    const int64_t blocks = (n + 16 * nf - 1) / (16 * nf);
-    const int64_t cost = (blocks + cus - 1) / cus * (16 * nf + m);
-    if (cost < best_c) {
-      best_c = cost;
-      best = nf;
+// groups of 16 rows of the few-rows kernel
+int row_groups(int64_t m) { return m <= 16 ? 1 : (m <= 32 ? 2 : 4); }
+
+// The few-rows kernel's bytes through the busiest of `cus` CUs, in rows of K: a
+// block streams its 16 nf rows of the weight and all of x. *nf: the columns per
+// block, in groups of 16, of the least.
+int64_t rows_cost(int64_t m, int64_t n, int64_t cus, int* nf) {
+  int64_t best = INT64_MAX;
+  for (int f = 1; f <= 4; f *= 2) {
+    const int64_t blocks = (n + 16 * f - 1) / (16 * f);
+    const int64_t cost = (blocks + cus - 1) / cus * (16 * f + m);
+    if (cost < best) {
+      best = cost;
+      *nf = f;
     }
   }
   return best;
+}
+
+// Which kernel takes m rows. Estimated from measurements on 256 CUs: few rows
+// 3.7 us + 32 KB per us through a CU; 64 x 64 tiles 4.4 us + 0.285 us a K-step
+// (0.43 with two blocks on a CU). Measured, few rows / tiles: 13824 x 5120 with
+// 16, 32, 64 rows 10.2, 12.0, 19.8 / 10.1, 10.3, 10.6 us; 5120 x 13824 13.6,
+// 17.8, 25.0 / 19.8, 19.8, 20.0; 3840 x 3840 5.5, 6.5, 8.6 / 8.5, 8.5, 8.7. The
+// two add in different orders, so the choice goes by the shape alone and not
+// by the device's CUs.
+bool few_rows(int64_t m, int64_t n, int64_t k) {
+  if (m > kFewRows) return false;
+  constexpr int64_t cus = 256;
+  int nf;
+  const double rows_us = 3.7 + (double)rows_cost(m, n, cus, &nf) * (double)(k / 2) / 32e3;
+  const int64_t tiles = (n + 63) / 64, steps = (k + kMx4Tile - 1) / kMx4Tile;
+  const double step_us = tiles <= cus ? 0.285 : 0.43 * (double)((tiles + 2 * cus - 1) / (2 * cus));
+  return rows_us < 4.4 + step_us * (double)steps;
 }
 
 template <bool F16, int MF>
@@ -559,11 +579,13 @@ hipError_t launch_rows_n(int nf, const Args& a) {
 template <bool F16>
 hipError_t launch_tile(const LaunchPlan& p, const Args& a) {
   switch (p.tile_m) {
-    case 16: return launch_rows_n<F16, 1>(p.tile_n / 16, a);
-    case 32: return launch_rows_n<F16, 2>(p.tile_n / 16, a);
-    case 64:
-      if (a.m <= kFewRows) return launch_rows_n<F16, 4>(p.tile_n / 16, a);
-      return launch_cfg<F16, 64, 64, 2, 2, 4, 2>(a);
+    case 16:
+      switch (row_groups(a.m)) {
+        case 1: return launch_rows_n<F16, 1>(p.tile_n / 16, a);
+        case 2: return launch_rows_n<F16, 2>(p.tile_n / 16, a);
+        default: return launch_rows_n<F16, 4>(p.tile_n / 16, a);
+      }
+    case 64: return launch_cfg<F16, 64, 64, 2, 2, 4, 2>(a);
     case 128: return launch_cfg<F16, 128, 128, 2, 2, 2, 2>(a);
     case 192: return launch_cfg<F16, 192, 192, 2, 2, 3, 1, 4>(a);
     case 384: return launch_cfg<F16, 384, 192, 4, 2, 2, 1>(a);
@@ -577,8 +599,7 @@ hipError_t launch_tile(const LaunchPlan& p, const Args& a) {
 // two blocks per CU and 13-15 with one, 64 9-11 with up to two). E.g. 4608 x
 // 3840 x 3840 takes 41, 57, 47 and 52 us with the first four, 16384 x 9216 x
 // 3840 325, 304, 359 and 349 us; 128 x 3840 x 3840 8.5 us with the last, 12.7
-// with 128. Bits do not depend on the tile. Up to kFewRows rows the 64 tile is
-// left out (64 then names the few-rows kernel).
+// with 128. Bits do not depend on the tile.
 int choose_tile(int64_t m, int64_t n, int cus) {
   const struct {
     int tile, bm, bn, per_cu;
@@ -588,7 +609,6 @@ int choose_tile(int64_t m, int64_t n, int cus) {
   int best = 128;
   double best_t = 1e300;
   for (const auto& c : cands) {
-    if (c.tile == 64 && m <= kFewRows) continue;
     const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
     const int64_t slots = (int64_t)(cus > 0 ? cus : 1) * c.per_cu;
     const double rt = c.tile == 128 && tiles <= cus ? 0.65 : c.round;
@@ -603,20 +623,27 @@ int choose_tile(int64_t m, int64_t n, int cus) {
 
 }  // namespace
 
-int mx4_gemm_tile(int64_t m, int64_t n, int64_t call_rows, int cus) {
-  if (call_rows <= kFewRows) return m <= 16 ? 16 : (m <= 32 ? 32 : 64);
-  return choose_tile(m, n, cus);
+int mx4_gemm_tile(int64_t m, int64_t n, int64_t k, int64_t call_rows, int cus) {
+  return few_rows(call_rows, n, k) ? 16 : choose_tile(m, n, cus);
 }
 
 LaunchPlan plan_mx4_gemm(int64_t m, int64_t n, int64_t k, int tile, int cus) {
   LaunchPlan p;
-  if (tile == 0) tile = mx4_gemm_tile(m, n, m, cus);
-  p.tile_m = tile;
-  const bool few = tile <= 64 && m <= kFewRows;
-  p.tile_n = few ? 16 * rows_columns(m, n, cus > 0 ? cus : 1) : (tile == 384 ? 192 : tile);
-  p.block = tile == 128 || (tile == 64 && !few) ? 256 : 512;
-  p.grid = ((m + p.tile_m - 1) / p.tile_m) * ((n + p.tile_n - 1) / p.tile_n);
-  p.xcds = few ? 1 : xcd_count(cus);
+  if (tile == 0) tile = mx4_gemm_tile(m, n, k, m, cus);
+  if (tile == 16) {
+    int nf = 1;
+    rows_cost(m, n, cus > 0 ? cus : 1, &nf);
+    p.tile_m = 16;
+    p.tile_n = 16 * nf;
+    p.block = 64 * kRowWaves;
+    p.grid = (n + p.tile_n - 1) / p.tile_n;
+  } else {
+    p.tile_m = tile;
+    p.tile_n = tile == 384 ? 192 : tile;
+    p.block = tile <= 128 ? 256 : 512;
+    p.grid = ((m + p.tile_m - 1) / p.tile_m) * ((n + p.tile_n - 1) / p.tile_n);
+    p.xcds = xcd_count(cus);
+  }
   p.passes = 1;
   return p;
 }

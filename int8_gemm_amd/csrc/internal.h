@@ -136,8 +136,8 @@ hipError_t launch_norm_residual(const NormArgs& a, int g, const SignMask& sm, DT
                                 hipStream_t st);
 // The tile for `m` rows of a call that has `call_rows` rows in all: the two
 // kernels sum in different orders, so one call keeps to one of them whatever
-// its slices are.
-int mx4_gemm_tile(int64_t m, int64_t n, int64_t call_rows, int cus);
+// its slices are. 16: the few-rows kernel.
+int mx4_gemm_tile(int64_t m, int64_t n, int64_t k, int64_t call_rows, int cus);
 LaunchPlan plan_mx4_gemm(int64_t m, int64_t n, int64_t k, int tile, int cus);
 
 }  // namespace convrot

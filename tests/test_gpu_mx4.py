@@ -244,11 +244,32 @@ def test_gemm_matches_oracle(m, n, k, dtype, bias):
                hi=134 if dtype == torch.bfloat16 else 128, fill=255)
 
 
-@pytest.mark.parametrize("tile", [16, 32, 64, 128, 192, 256, 384])
+@pytest.mark.parametrize("tile", [16, 64, 128, 192, 256, 384])
 @pytest.mark.parametrize("n,k", [(16, 32), (416, 256), (592, 800), (208, 2272)])
 def test_gemm_forced_variants(tile, n, k):
-    for m in {1, tile // 2 + 3, tile, *((tile + 1, 2 * tile + 37) if tile >= 64 else ())}:
+    for m in ((1, 11, 16, 17, 32, 33, 64) if tile == 16 else
+              (1, tile // 2 + 3, tile, tile + 1, 2 * tile + 37)):
         check_gemm(m, n, k, torch.bfloat16, True, tile)
+
+
+@pytest.mark.parametrize("m", [5, 30, 64])
+def test_gemm_few_rows_at_every_block_width(m):
+    """Blocks of 16, 32 and 64 columns: fewer compute units make them wider."""
+    rng = np.random.default_rng(m)
+    xc, xs, _ = held(rng, m, 1056)
+    wc, ws, _ = held(rng, 432, 1056)
+    want = cr.convrot_gemm_mx4(xc, xs, wc, ws, tile=16)
+    widths = set()
+    try:
+        for cus in (256, 24, 12, 7, 1):
+            cr.convrot_set_compute_units(cus)
+            if cr.convrot_plan_launch("gemm_mx4", m=m, n=432, k=1056)["tile_m"] == 16:
+                widths.add(cr.convrot_plan_launch("gemm_mx4", m=m, n=432, k=1056)["tile_n"])
+            assert torch.equal(cr.convrot_gemm_mx4(xc, xs, wc, ws, tile=16), want), cus
+    finally:
+        cr.convrot_set_compute_units(0)
+    assert len(widths) >= 2
+    check_gemm(m, 432, 1056, torch.bfloat16, True, 16)
 
 
 @pytest.mark.parametrize("m", [3, 40, 130, 700])
@@ -396,7 +417,16 @@ def test_gemm_bits_do_not_depend_on_the_tile():
     want = cr.convrot_gemm_mx4(xc, xs, wc, ws)
     for tile in (64, 128, 192, 256, 384):
         assert torch.equal(cr.convrot_gemm_mx4(xc, xs, wc, ws, tile=tile), want), tile
-    few = cr.convrot_gemm_mx4(xc[:16], xs[:, :16].contiguous(), wc, ws)
-    for tile in (16, 32, 64):
-        assert torch.equal(cr.convrot_gemm_mx4(xc[:16], xs[:, :16].contiguous(), wc, ws,
-                                               tile=tile), few), tile
+    # ... nor on the compute units, automatic choice included
+    try:
+        for cus in (256, 128, 3):
+            cr.convrot_set_compute_units(cus)
+            assert torch.equal(cr.convrot_gemm_mx4(xc, xs, wc, ws), want), cus
+            for m in (1, 20, 50):
+                part = (xc[:m], xs[:, :-(-m // 16) * 16].contiguous())
+                got = cr.convrot_gemm_mx4(*part, wc, ws)
+                cr.convrot_set_compute_units(256)
+                assert torch.equal(cr.convrot_gemm_mx4(*part, wc, ws), got), (cus, m)
+                cr.convrot_set_compute_units(cus)
+    finally:
+        cr.convrot_set_compute_units(0)

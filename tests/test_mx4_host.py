@@ -63,9 +63,9 @@ def test_gemm_refusals(lib):
     def gemm(xc=A, xs=B, wc=C, ws=D, bias=None, m=8, n=32, k=256, y=E, dt=0, tile=0):
         return lib.convrot_gemm_mx4(xc, xs, wc, ws, bias, m, n, k, y, dt, tile, None)
     assert gemm(dt=7) == 1
-    for tile in (-1, 1, 8, 48, 100, 512):
+    for tile in (-1, 1, 8, 32, 48, 100, 512):
         assert gemm(tile=tile) == 1
-    assert gemm(m=17, tile=16) == 1 and gemm(m=33, tile=32) == 1   # more rows than it holds
+    assert gemm(m=65, tile=16) == 1   # more rows than it holds
     assert gemm(n=24) == 3 and gemm(k=272) == 3 and gemm(k=131104) == 3
     assert gemm(n=0) == 1 and gemm(k=0) == 1 and gemm(m=-1) == 1
     assert gemm(m=1 << 30, n=1 << 30) == 3 and gemm(m=(1 << 31) - 1) == 3
@@ -180,12 +180,14 @@ def test_binding_checks_modulations():
 
 @pytest.mark.parametrize("cus", [256, 128, 3])
 def test_gemm_plans(lib, cus):
-    """Up to 64 rows take the few-rows kernel, whose blocks are 16 to 64 columns
-    wide."""
-    for m, tile in ((1, 16), (16, 16), (17, 32), (33, 64), (64, 64)):
-        p = cr.convrot_plan_launch("gemm_mx4", m=m, n=3840, k=3840, compute_units=cus)
-        assert p["tile_m"] == tile and p["tile_n"] in (16, 32, 64)
-        assert p["grid"] == -(-3840 // p["tile_n"])
+    """Up to 64 rows take the few-rows kernel (blocks of 16 to 64 columns) or
+    tiles, by the shape alone; more rows take tiles."""
+    for m, n, k, few in ((1, 3840, 3840, True), (16, 5120, 13824, True), (64, 16, 256, True),
+                         (64, 13824, 5120, False), (32, 11520, 3840, False), (40, 512, 8192, True)):
+        p = cr.convrot_plan_launch("gemm_mx4", m=m, n=n, k=k, compute_units=cus)
+        assert (p["tile_m"] == 16) == few
+        if few:
+            assert p["tile_n"] in (16, 32, 64) and p["grid"] == -(-n // p["tile_n"])
     for m in (65, 1000, 32760):
         p = cr.convrot_plan_launch("gemm_mx4", m=m, n=3840, k=3840, compute_units=cus)
         assert p["tile_m"] in (64, 128, 192, 256, 384)
