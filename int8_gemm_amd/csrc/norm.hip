@@ -13,7 +13,7 @@
 //
 // Bound by memory: x and o are read once, x' and h written once (32760 x 5120:
 // 1.34 GB, 242 us = 5.5 TB/s, a large device copy reaches 5.1; with h quantized
-// 265 us, 4.1 TB/s, the rotation's arithmetic on top); the row stays
+// 258 us, 4.2 TB/s, the rotation's arithmetic on top); the row stays
 // in registers between the norms (32 elements a lane, in the tile layout of
 // mx4.h). A row takes ceil(K / 2048) waves; rows of one wave share a block of
 // four. Variances are taken in two passes over the registers, around the mean.
@@ -73,7 +73,8 @@ __device__ __forceinline__ u4 pack(const float (&f)[8]) {
 }
 
 // Normalise v in place (without its weight). `in` marks the lane's chunks that
-// lie in the row; `part` has 2 * kMaxWaves slots.
+// lie in the row; the others come in as 0 and go out as anything. `part` has 2 *
+// kMaxWaves slots.
 __device__ __forceinline__ void normalise(float (&v)[4][8], const bool (&in)[4], NormKind kind,
                                           float k, float eps, int waves, float* part) {
   if (kind == NormKind::kLayer) {
@@ -86,13 +87,16 @@ __device__ __forceinline__ void normalise(float (&v)[4][8], const bool (&in)[4],
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = in[i] ? v[i][e] - mean : 0.f;
+      for (int e = 0; e < 8; ++e) v[i][e] -= mean;
   }
   float q = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4; ++i) {
+    float c = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q = __builtin_fmaf(v[i][e], v[i][e], q);
+    for (int e = 0; e < 8; ++e) c = __builtin_fmaf(v[i][e], v[i][e], c);
+    q += in[i] ? c : 0.f;
+  }
   const float r = 1.0f / sqrtf(row_sum(q, waves, part) / k + eps);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -132,14 +136,15 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
 #pragma unroll
     for (int i = 0; i < 4; ++i) to[i] = load(p, i);
   };
-  // v op= the unpacked chunks
-  auto multiply = [](float (&v)[4][8], const u4 (&by)[4], float add) {
+  // v = v * by (+ v)
+  auto multiply = [](float (&v)[4][8], const u4 (&by)[4], bool plus) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float w[8];
       unpack<F16>(by[i], w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] *= add + w[e];
+      for (int e = 0; e < 8; ++e)
+        v[i][e] = plus ? __builtin_fmaf(v[i][e], w[e], v[i][e]) : v[i][e] * w[e];
     }
   };
 
@@ -157,11 +162,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
       normalise(v, in, a.post_norm, (float)a.k, a.eps, waves, part);
     if (a.post_weight) {
       if (!EARLY) load4(w1, a.post_weight + col);
-      multiply(v, w1, 0.f);
+      multiply(v, w1, false);
     }
     if (a.gate) {
       if (!EARLY) load4(w2, gate);
-      multiply(v, w2, 0.f);
+      multiply(v, w2, false);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -169,7 +174,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
       unpack<F16>(xw[i], w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] += v[i][e];
-      xw[i] = pack<F16>(w);
+      xw[i] = in[i] ? pack<F16>(w) : zero;
       if (in[i]) *reinterpret_cast<u4*>(a.x_out + base + 64 * i) = xw[i];
     }
   }
@@ -179,21 +184,15 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
   if (EARLY && a.scale) load4(w2, scale);
   if (EARLY && a.shift) load4(w3, shift);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    unpack<F16>(xw[i], v[i]);
-    if (!in[i]) {  // 0 * inf of an absent chunk's gate must not reach the sums
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-    }
-  }
+  for (int i = 0; i < 4; ++i) unpack<F16>(xw[i], v[i]);
   normalise(v, in, a.norm, (float)a.k, a.eps, waves, part + 2 * kMaxWaves);
   if (a.weight) {
     if (!EARLY) load4(w1, a.weight + col);
-    multiply(v, w1, 0.f);
+    multiply(v, w1, false);
   }
   if (a.scale) {
     if (!EARLY) load4(w2, scale);
-    multiply(v, w2, 1.f);
+    multiply(v, w2, true);
   }
   if (!EARLY && a.shift) load4(w3, shift);
   u4 hw[4];
