@@ -12,11 +12,13 @@
 // caller gets. Everything else is fp32.
 //
 // Bound by memory: x and o are read once, x' and h written once (32760 x 5120:
-// 1.34 GB, 242 us = 5.5 TB/s, a large device copy reaches 5.1; with h quantized
-// 258 us, 4.2 TB/s, the rotation's arithmetic on top); the row stays
-// in registers between the norms (32 elements a lane, in the tile layout of
-// mx4.h). A row takes ceil(K / 2048) waves; rows of one wave share a block of
-// four. Variances are taken in two passes over the registers, around the mean.
+// 1.34 GB, 234-244 us = 5.5-5.7 TB/s, a large device copy reaches 5.1; with h
+// quantized 258 us, 4.2 TB/s, the rotation's arithmetic on top); the row stays in
+// registers between the norms (32 elements a lane, in the tile layout of
+// mx4.h). A row takes ceil(K / 2048) waves or, up to 1024 elements, 8, 16 or 32
+// lanes of one (32760 x 256: 14 us, with a wave per row 39); rows of up to one
+// wave share blocks of four waves. Variances are taken in two passes over the
+// registers, around the mean.
 
 #include "internal.h"
 #include "mx4.h"
@@ -27,34 +29,45 @@ namespace {
 
 constexpr int kLaneElems = 32;                  // elements of a row per lane
 constexpr int kWaveElems = 64 * kLaneElems;     // ... and per wave
-constexpr int kRowsPerBlock = 4;                // when a row is one wave
+constexpr int kBlockWaves = 4;                  // when a row is at most one wave
 constexpr int kMaxWaves = 8;                    // K <= 16384
 
-// Sum over the wave, the same bits in every lane: DPP exchanges within 16
-// lanes, then swaps of 16-lane rows and of the wave's halves.
-__device__ __forceinline__ float wave_sum(float v) {
+// How a row lies: on `waves` waves of a block, or on 2^shift lanes of one.
+struct RowShape {
+  int waves, shift;
+};
+
+// Sum over 2^shift lanes, the same bits in each: DPP exchanges within 16 lanes,
+// then swaps of 16-lane rows and of the wave's halves.
+__device__ __forceinline__ float lanes_sum(float v, int shift) {
+  typedef uint32_t u2v __attribute__((ext_vector_type(2)));
   v += mx4_dpp<kDppXor1>(v);
   v += mx4_dpp<kDppXor2>(v);
   v += mx4_dpp<kDppMirror8>(v);
-  v += mx4_dpp<kDppMirror16>(v);
-  typedef uint32_t u2v __attribute__((ext_vector_type(2)));
-  const uint32_t a = __float_as_uint(v);
-  const u2v r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-  const uint32_t b = __float_as_uint(__uint_as_float(r.x) + __uint_as_float(r.y));
-  const u2v h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return __uint_as_float(h.x) + __uint_as_float(h.y);
+  if (shift > 3) v += mx4_dpp<kDppMirror16>(v);
+  if (shift > 4) {
+    const uint32_t a = __float_as_uint(v);
+    const u2v r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    v = __uint_as_float(r.x) + __uint_as_float(r.y);
+  }
+  if (shift > 5) {
+    const uint32_t a = __float_as_uint(v);
+    const u2v r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    v = __uint_as_float(r.x) + __uint_as_float(r.y);
+  }
+  return v;
 }
 
-// Sum over the row's waves; `part` holds one slot per wave. Two calls in a row
-// use different slots, so one barrier each is enough.
-__device__ __forceinline__ float row_sum(float v, int waves, float* part) {
-  v = wave_sum(v);
-  if (waves == 1) return v;
+// Sum over the row; `part` holds one slot per wave. Two calls in a row use
+// different slots, so one barrier each is enough.
+__device__ __forceinline__ float row_sum(float v, RowShape rs, float* part) {
+  v = lanes_sum(v, rs.shift);
+  if (rs.waves == 1) return v;
   const int wave = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0) part[wave] = v;
   __syncthreads();
   float s = part[0];
-  for (int w = 1; w < waves; ++w) s += part[w];
+  for (int w = 1; w < rs.waves; ++w) s += part[w];
   return s;
 }
 
@@ -76,14 +89,14 @@ __device__ __forceinline__ u4 pack(const float (&f)[8]) {
 // lie in the row; the others come in as 0 and go out as anything. `part` has 2 *
 // kMaxWaves slots.
 __device__ __forceinline__ void normalise(float (&v)[4][8], const bool (&in)[4], NormKind kind,
-                                          float k, float eps, int waves, float* part) {
+                                          float k, float eps, RowShape rs, float* part) {
   if (kind == NormKind::kLayer) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += v[i][e];  // chunks outside the row hold 0
-    const float mean = row_sum(s, waves, part + kMaxWaves) / k;  // a row of one value gives it back
+    const float mean = row_sum(s, rs, part + kMaxWaves) / k;  // a row of one value gives it back
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -97,7 +110,7 @@ __device__ __forceinline__ void normalise(float (&v)[4][8], const bool (&in)[4],
     for (int e = 0; e < 8; ++e) c = __builtin_fmaf(v[i][e], v[i][e], c);
     q += in[i] ? c : 0.f;
   }
-  const float r = 1.0f / sqrtf(row_sum(q, waves, part) / k + eps);
+  const float r = 1.0f / sqrtf(row_sum(q, rs, part) / k + eps);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -112,15 +125,18 @@ __device__ __forceinline__ void normalise(float (&v)[4][8], const bool (&in)[4],
 // 267 us).
 template <int G, bool F16, bool EARLY>
 __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs a, SignMask sm,
-                                                                       int waves) {
+                                                                       RowShape rs) {
   __shared__ float part[4 * kMaxWaves];
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
-  const int64_t row = waves == 1 ? (int64_t)blockIdx.x * kRowsPerBlock + wave : blockIdx.x;
-  if (row >= a.m) return;  // one-wave rows only: no barrier follows
+  const int64_t at = rs.waves == 1 ? (((int64_t)blockIdx.x * kBlockWaves + wave) << (6 - rs.shift)) +
+                                         (lane >> rs.shift)
+                                   : blockIdx.x;
+  const bool live = at < a.m;  // lanes behind the last row go through it and write nothing
+  const int64_t row = live ? at : a.m - 1;
   const int label = mx4_label(lane);
   const int lab_in = label ^ kMx4LaneBits<G>;
-  const int tile = (waves == 1 ? 0 : wave * 8) + (lane >> 3);
+  const int tile = (rs.waves == 1 ? 0 : wave * 8) + ((lane & ((1 << rs.shift) - 1)) >> 3);
   const int col = tile * kMx4Tile + 8 * lab_in;  // + 64 i
   const int64_t base = row * a.k + col;
   const int64_t mod = (uint32_t)row / (uint32_t)a.rows_per_mod;  // both below 2^31
@@ -159,7 +175,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
 #pragma unroll
     for (int i = 0; i < 4; ++i) unpack<F16>(w3[i], v[i]);
     if (a.post_norm != NormKind::kNone)
-      normalise(v, in, a.post_norm, (float)a.k, a.eps, waves, part);
+      normalise(v, in, a.post_norm, (float)a.k, a.eps, rs, part);
     if (a.post_weight) {
       if (!EARLY) load4(w1, a.post_weight + col);
       multiply(v, w1, false);
@@ -175,7 +191,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] += v[i][e];
       xw[i] = in[i] ? pack<F16>(w) : zero;
-      if (in[i]) *reinterpret_cast<u4*>(a.x_out + base + 64 * i) = xw[i];
+      if (in[i] && live) *reinterpret_cast<u4*>(a.x_out + base + 64 * i) = xw[i];
     }
   }
   const uint16_t* scale = a.scale + mod * a.scale_stride + col;
@@ -185,7 +201,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
   if (EARLY && a.shift) load4(w3, shift);
 #pragma unroll
   for (int i = 0; i < 4; ++i) unpack<F16>(xw[i], v[i]);
-  normalise(v, in, a.norm, (float)a.k, a.eps, waves, part + 2 * kMaxWaves);
+  normalise(v, in, a.norm, (float)a.k, a.eps, rs, part + 2 * kMaxWaves);
   if (a.weight) {
     if (!EARLY) load4(w1, a.weight + col);
     multiply(v, w1, false);
@@ -205,7 +221,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
       for (int e = 0; e < 8; ++e) v[i][e] += w[e];
     }
     hw[i] = pack<F16>(v[i]);
-    if (a.h && in[i]) *reinterpret_cast<u4*>(a.h + base + 64 * i) = hw[i];
+    if (a.h && in[i] && live) *reinterpret_cast<u4*>(a.h + base + 64 * i) = hw[i];
   }
   if constexpr (G > 0) {
     uint32_t signs[4], eb[4], code[4];
@@ -214,7 +230,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
     for (int i = 0; i < 4; ++i) hw[i] = in[i] ? hw[i] : zero;
     mx4_quantize_tile<G, F16>(hw, label, signs, eb, code);
     const int blocks = min(8, (a.k - tile * kMx4Tile) / kMx4Block);
-    if (blocks > 0)
+    if (blocks > 0 && live)
       mx4_store_tile(a.h_codes + row * (a.k / 2) + tile * (kMx4Tile / 2),
                      a.h_scales + (tile * mx4_pad_rows(a.m) + row) * 8, label, blocks, eb, code);
   }
@@ -222,21 +238,23 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
 
 template <int G>
 hipError_t launch_g(const NormArgs& a, const SignMask& sm, DType dt, hipStream_t st) {
-  const int waves = (a.k + kWaveElems - 1) / kWaveElems;
-  const dim3 grid((uint32_t)(waves == 1 ? (a.m + kRowsPerBlock - 1) / kRowsPerBlock : a.m));
-  const dim3 block(64 * (waves == 1 ? kRowsPerBlock : waves));
+  RowShape rs = {(a.k + kWaveElems - 1) / kWaveElems, 6};
+  while (rs.shift > 3 && a.k <= kLaneElems << (rs.shift - 1)) --rs.shift;
+  const int64_t rows = (int64_t)kBlockWaves << (6 - rs.shift);  // of a block, if it has several
+  const dim3 grid((uint32_t)(rs.waves == 1 ? (a.m + rows - 1) / rows : a.m));
+  const dim3 block(64 * (rs.waves == 1 ? kBlockWaves : rs.waves));
   // 16 waves a CU is what the EARLY form's registers allow
-  const bool early = a.m * waves <= (int64_t)compute_units() * 16;
+  const bool early = (int64_t)grid.x * (block.x / 64) <= (int64_t)compute_units() * 16;
   if (dt == DType::kF16) {
     if (early)
-      norm_residual_kernel<G, true, true><<<grid, block, 0, st>>>(a, sm, waves);
+      norm_residual_kernel<G, true, true><<<grid, block, 0, st>>>(a, sm, rs);
     else
-      norm_residual_kernel<G, true, false><<<grid, block, 0, st>>>(a, sm, waves);
+      norm_residual_kernel<G, true, false><<<grid, block, 0, st>>>(a, sm, rs);
   } else {
     if (early)
-      norm_residual_kernel<G, false, true><<<grid, block, 0, st>>>(a, sm, waves);
+      norm_residual_kernel<G, false, true><<<grid, block, 0, st>>>(a, sm, rs);
     else
-      norm_residual_kernel<G, false, false><<<grid, block, 0, st>>>(a, sm, waves);
+      norm_residual_kernel<G, false, false><<<grid, block, 0, st>>>(a, sm, rs);
   }
   return hipGetLastError();
 }
@@ -244,7 +262,7 @@ hipError_t launch_g(const NormArgs& a, const SignMask& sm, DType dt, hipStream_t
 }  // namespace
 
 bool norm_grid_fits(int64_t m, int64_t k) {
-  return m * ((k + kWaveElems - 1) / kWaveElems) <= kMaxLaunchWaves - kRowsPerBlock;
+  return m * ((k + kWaveElems - 1) / kWaveElems) <= kMaxLaunchWaves - kBlockWaves;
 }
 
 hipError_t launch_norm_residual(const NormArgs& a, int g, const SignMask& sm, DType dt,

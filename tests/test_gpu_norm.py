@@ -96,7 +96,8 @@ def build(rng, m, k, dtype, samples, post, weights, mods, residual=True):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
 @pytest.mark.parametrize("norm,post", [("rms", "rms"), ("layer", None), ("rms", "layer"),
                                        ("layer", "rms")])
-@pytest.mark.parametrize("m,k,samples", [(1, 8, 1), (3, 264, 3), (10, 1024, 2), (6, 2048, 3),
+@pytest.mark.parametrize("m,k,samples", [(1, 8, 1), (67, 256, 1), (3, 264, 3), (36, 512, 4),
+                                         (10, 1024, 2), (9, 1032, 1), (6, 2048, 3),
                                          (5, 2056, 1), (4, 3840, 2), (3, 5120, 1), (2, 16384, 2)])
 def test_norm_residual_matches_oracle(m, k, samples, norm, post, dtype):
     rng = np.random.default_rng(m + k)
@@ -167,7 +168,8 @@ def test_modulation_rows_of_any_stride():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
 @pytest.mark.parametrize("g,m,k", [(1, 3, 96), (4, 5, 288), (16, 2, 2080), (64, 9, 1088),
-                                   (256, 1, 256), (256, 6, 3840), (256, 3, 16384)])
+                                   (256, 1, 256), (256, 41, 256), (64, 19, 512), (16, 5, 1024),
+                                   (256, 6, 3840), (256, 3, 16384)])
 def test_quantized_h_is_the_16_bit_h_quantized(g, m, k, dtype):
     rng = np.random.default_rng(g + k)
     x, o, kw = build(rng, m, k, dtype, 1, "rms", True, True)
