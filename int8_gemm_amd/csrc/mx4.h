@@ -201,15 +201,26 @@ __device__ __forceinline__ void mx4_encode(const float (&v)[8], uint32_t& eb, ui
   code = bad ? 0 : w;
 }
 
+// Two packed 16-bit values -> fp32, exact (the sign of a half zero aside). Half
+// goes through the mixed-precision multiply-add, x * 1 + 0: the conversion
+// instruction runs at a quarter of its rate (gated norm with two layer norms and
+// quantized h, 32760 x 5120 half, g = 256: 331 us with conversions, 252 with
+// this).
 template <bool F16>
-__device__ __forceinline__ void mx4_unpack(const u4 (&raw)[4], float (&f)[4][8]) {
+__device__ __forceinline__ void mx4_unpack2(uint32_t w, float& lo, float& hi) {
+  if constexpr (F16) {
+    asm("v_fma_mix_f32 %0, %1, 1.0, 0 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(lo) : "v"(w));
+    asm("v_fma_mix_f32 %0, %1, 1.0, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(hi) : "v"(w));
+  } else {
+    lo = bf16lo(w);
+    hi = bf16hi(w);
+  }
+}
+
+template <bool F16>
+__device__ __forceinline__ void mx4_unpack8(const u4& w, float (&f)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      f[i][2 * p] = lo16<F16>(raw[i][p]);
-      f[i][2 * p + 1] = hi16<F16>(raw[i][p]);
-    }
+  for (int p = 0; p < 4; ++p) mx4_unpack2<F16>(w[p], f[2 * p], f[2 * p + 1]);
 }
 
 // The definition, for one i: sums in float64, rounded once to fp32, then the
@@ -252,16 +263,28 @@ __device__ __forceinline__ void mx4_rotate_encode_f64(const u4 (&raw)[4], int i,
 // high that fp32 would lose bits of the definition) the wave takes the float64
 // sums of that i: one wave in ten or so for normal activations, a quarter of
 // the tile at a time. All of it in float64 took 126 us instead of 105 at 32760 x
-// 5120, g = 256.
+// 5120, g = 256; inputs that lie on borders throughout (all ones) take 198.
+// Sums of four bf16 values hit borders in most waves, and their float64 form
+// has no exchanges: g = 4 takes it for bf16 at once (86 us instead of 99; half,
+// with finer values, 86 instead of 80).
 template <int G, bool F16>
 __device__ __forceinline__ void mx4_quantize_tile(const u4 (&raw)[4], int label,
                                                   const uint32_t (&signs)[4], uint32_t (&eb)[4],
                                                   uint32_t (&code)[4]) {
   float v[4][8];
-  mx4_unpack<F16>(raw, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mx4_unpack8<F16>(raw[i], v[i]);
   if constexpr (G == 1) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) mx4_encode(v[i], eb[i], code[i]);
+    return;
+  }
+  if constexpr (G == 4 && !F16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mx4_rotate_encode_f64<G, F16>(raw, i, label, eb[i], code[i]);
+      code[i] ^= signs[i];
+    }
     return;
   }
   constexpr int lg = ilog2(G) / 2;  // sqrt(G) = 2^lg: the fp32 sums stay unnormalised

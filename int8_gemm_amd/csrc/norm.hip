@@ -72,14 +72,6 @@ __device__ __forceinline__ float row_sum(float v, RowShape rs, float* part) {
 }
 
 template <bool F16>
-__device__ __forceinline__ void unpack(const u4& w, float (&f)[8]) {
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    f[2 * p] = lo16<F16>(w[p]);
-    f[2 * p + 1] = hi16<F16>(w[p]);
-  }
-}
-template <bool F16>
 __device__ __forceinline__ u4 pack(const float (&f)[8]) {
   return (u4){pack16x2<F16>(f[0], f[1]), pack16x2<F16>(f[2], f[3]), pack16x2<F16>(f[4], f[5]),
               pack16x2<F16>(f[6], f[7])};
@@ -157,7 +149,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float w[8];
-      unpack<F16>(by[i], w);
+      mx4_unpack8<F16>(by[i], w);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         v[i][e] = plus ? __builtin_fmaf(v[i][e], w[e], v[i][e]) : v[i][e] * w[e];
@@ -173,7 +165,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
     if (EARLY && a.post_weight) load4(w1, a.post_weight + col);
     if (EARLY && a.gate) load4(w2, gate);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpack<F16>(w3[i], v[i]);
+    for (int i = 0; i < 4; ++i) mx4_unpack8<F16>(w3[i], v[i]);
     if (a.post_norm != NormKind::kNone)
       normalise(v, in, a.post_norm, (float)a.k, a.eps, rs, part);
     if (a.post_weight) {
@@ -187,7 +179,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float w[8];
-      unpack<F16>(xw[i], w);
+      mx4_unpack8<F16>(xw[i], w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] += v[i][e];
       xw[i] = in[i] ? pack<F16>(w) : zero;
@@ -200,7 +192,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
   if (EARLY && a.scale) load4(w2, scale);
   if (EARLY && a.shift) load4(w3, shift);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) unpack<F16>(xw[i], v[i]);
+  for (int i = 0; i < 4; ++i) mx4_unpack8<F16>(xw[i], v[i]);
   normalise(v, in, a.norm, (float)a.k, a.eps, rs, part + 2 * kMaxWaves);
   if (a.weight) {
     if (!EARLY) load4(w1, a.weight + col);
@@ -216,7 +208,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
   for (int i = 0; i < 4; ++i) {
     if (a.shift) {
       float w[8];
-      unpack<F16>(w3[i], w);
+      mx4_unpack8<F16>(w3[i], w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] += w[e];
     }

@@ -110,6 +110,19 @@ def test_quantize_at_the_ends_of_the_range(g, exp):
     assert_quantized(codes, scales, f64(x), g)
 
 
+@pytest.mark.parametrize("exp", [-24, -22, -17, -14, 8, 12])
+@pytest.mark.parametrize("g", [1, 4, 16, 256])
+def test_quantize_half_at_the_ends_of_its_range(g, exp):
+    """Subnormal halves among them; every half value and sign."""
+    rng = np.random.default_rng(exp + 300)
+    x = dev(rng.integers(-15, 16, (16, 512)) * 2.0 ** exp, torch.float16)
+    codes, scales = cr.convrot_quantize_mx4(x, g, SEED)
+    assert_quantized(codes, scales, f64(x), g)
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.float16)
+    every = every[torch.isfinite(every)].reshape(-1, 2048).to(DEV)
+    assert_quantized(*cr.convrot_quantize_mx4(every, g, SEED), f64(every), g)
+
+
 @pytest.mark.parametrize("g", [1, 64, 256])
 def test_quantize_marks_blocks_that_are_not_finite(g):
     rng = np.random.default_rng(5)
