@@ -474,8 +474,8 @@ convrot_status convrot_linear_mx4(const void* x, const uint8_t* w_codes, const u
                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes for slices of `rows` rows, and the default: min(m, 3n) rows,
- * less than the 16-bit weight that the default path would unpack, or min(m,
- * 8192) rows where that is more. 0 for invalid dimensions. */
+ * less than the 16-bit weight that the default path would unpack, or the rows
+ * that 64 MiB hold where that is more. 0 for invalid dimensions. */
 size_t convrot_linear_mx4_workspace_for_rows(int64_t rows, int64_t k);
 size_t convrot_linear_mx4_workspace_size(int64_t m, int64_t n, int64_t k);
 

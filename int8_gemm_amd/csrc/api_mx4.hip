@@ -10,6 +10,7 @@ namespace {
 
 constexpr int64_t kMaxMx4K = 131072;
 constexpr int64_t kMaxNormK = 16384;
+constexpr int64_t kDefaultWorkspace = (int64_t)64 << 20;
 
 size_t codes_bytes(int64_t rows, int64_t k) { return (size_t)(rows * (k / 2)); }
 size_t scales_bytes(int64_t rows, int64_t k) {
@@ -144,9 +145,12 @@ size_t convrot_linear_mx4_workspace_for_rows(int64_t rows, int64_t k) {
 
 size_t convrot_linear_mx4_workspace_size(int64_t m, int64_t n, int64_t k) {
   if (m < 0 || n <= 0 || k <= 0) return 0;
-  // at least 8192 rows: a narrow layer's short slices are bound by their launches
-  // (5518 x 144 x 6080 in 13 slices of 432 rows 298 us, in one 30)
-  int64_t rows = 3 * n > 8192 ? 3 * n : 8192;
+  // at least what 64 MiB hold: a narrow layer's short slices are bound by their
+  // launches (5518 x 144 x 6080 in 13 slices of 432 rows 298 us, in one 30;
+  // 21017 x 304 x 768 in 3 slices of 8192 rows 41 us, in one 23)
+  const int64_t per_row = k / 2 + (k + kMx4Tile - 1) / kMx4Tile * 8;
+  const int64_t held = kDefaultWorkspace / per_row;
+  int64_t rows = 3 * n > held ? 3 * n : held;
   if (rows > m) rows = m < 1 ? 1 : m;
   return convrot_linear_mx4_workspace_for_rows(rows, k);
 }

@@ -86,8 +86,10 @@ def test_linear_refusals_and_workspace(lib):
     assert size(1, 256) == 256 + 16 * 8 and size(3, 320) == 512 + 2 * 16 * 8
     assert size(17, 256) == 17 * 128 + 128 + 32 * 8          # codes rounded up to 256
     assert size(0, 256) == 0 and size(1, 0) == 0
-    assert cr.convrot_linear_mx4_workspace_size(100000, 16, 256) == size(8192, 256)
-    assert cr.convrot_linear_mx4_workspace_size(100000, 4096, 256) == size(12288, 256)
+    rows = (64 << 20) // (128 + 8)      # at least 64 MiB ...
+    assert cr.convrot_linear_mx4_workspace_size(10 ** 6, 16, 256) == size(rows, 256)
+    # ... or three rows per output column
+    assert cr.convrot_linear_mx4_workspace_size(10 ** 6, 1 << 18, 256) == size(3 << 18, 256)
     assert cr.convrot_linear_mx4_workspace_size(10, 16, 256) == size(10, 256)
     assert cr.convrot_linear_mx4_workspace_size(0, 16, 256) == size(1, 256)
     assert cr.convrot_mx4_scales_size(17, 288) == 2 * 32 * 8
