@@ -278,3 +278,17 @@ def test_no_rows():
     x_out, h = cr.convrot_norm_residual(x, torch.empty_like(x))
     assert h.shape == (0, 256)
     assert cr.convrot_norm_residual_mx4(x, None, 256)[1].shape == (0, 128)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_sign_of_zero(dtype):
+    """-0 + -0 is -0 in x', and the norm keeps the sign; -0 + 0 is 0."""
+    x = dev(np.full((3, 64), -0.0), dtype)
+    o = x.clone()
+    o[:, ::2] = 0.0
+    x_out, h = cr.convrot_norm_residual(x, o)
+    want = torch.zeros(64, dtype=torch.bool)
+    want[1::2] = True
+    for t in (x_out, h):
+        assert (t == 0).all()
+        assert torch.equal(torch.signbit(t).cpu(), want.expand(3, 64))
