@@ -594,28 +594,37 @@ hipError_t launch_tile(const LaunchPlan& p, const Args& a) {
 }
 
 // The tiled kernel's tile of least estimated time: rounds of concurrent tiles
-// over the CUs times a round's measured duration relative to a 192 tile's
-// (K = 3840, all CUs busy: 384 x 192 39 us, 256 32-34, 192 21-24, 128 17-19 with
-// two blocks per CU and 13-15 with one, 64 9-11 with up to two). E.g. 4608 x
-// 3840 x 3840 takes 41, 57, 47 and 52 us with the first four, 16384 x 9216 x
-// 3840 325, 304, 359 and 349 us; 128 x 3840 x 3840 8.5 us with the last, 12.7
-// with 128. Bits do not depend on the tile.
-int choose_tile(int64_t m, int64_t n, int cus) {
+// over the CUs times a round's duration, `start` (first copies, epilogue) and
+// `step` for each 256 of K, in us. The two small tiles run two to a CU, and a
+// last round that leaves one to a CU is shorter. With long rows the steps count,
+// with short ones start and epilogue: 512 x 13824 x 13824 takes 192 tiles (58
+// us, 128 74, 64 108), 4096 x 13824 x 768 128 tiles (44, 192 58, 256 54),
+// 32760 x 13824 x 5120 256 tiles. Fitted to 398 shapes (m 80 to 8192, n and k 768
+// to 13824); over 240 other random ones (m to 20000, k 512 to 14400) it is 0.5%
+// behind each shape's best tile on average and 13% at most, rounds of one length
+// whatever K is 2.0% and 26%. Bits do not depend on the tile.
+int choose_tile(int64_t m, int64_t n, int64_t k, int cus) {
   const struct {
     int tile, bm, bn, per_cu;
-    double round;
-  } cands[] = {{384, 384, 192, 1, 1.75}, {256, 256, 256, 1, 1.45}, {192, 192, 192, 1, 1.0},
-               {128, 128, 128, 2, 0.85}, {64, 64, 64, 2, 0.47}};
+    double start, step;      // all CUs with per_cu tiles
+    double start1, step1;    // one tile per CU
+  } cands[] = {{384, 384, 192, 1, 8.2, 1.27, 8.2, 1.27},
+               {256, 256, 256, 1, 6.5, 1.20, 6.5, 1.20},
+               {192, 192, 192, 1, 6.0, 0.64, 6.0, 0.64},
+               {128, 128, 128, 2, 1.9, 0.89, 1.2, 0.73},
+               {64, 64, 64, 2, 2.2, 0.46, 1.1, 0.29}};
+  const int64_t c = cus > 0 ? cus : 1;
+  const double steps = (double)((k + kMx4Tile - 1) / kMx4Tile);
   int best = 128;
   double best_t = 1e300;
-  for (const auto& c : cands) {
-    const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
-    const int64_t slots = (int64_t)(cus > 0 ? cus : 1) * c.per_cu;
-    const double rt = c.tile == 128 && tiles <= cus ? 0.65 : c.round;
-    const double time = (double)((tiles + slots - 1) / slots) * rt;
-    if (time < best_t * 0.999) {
+  for (const auto& t : cands) {
+    const int64_t tiles = ((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn);
+    const int64_t full = tiles / (c * t.per_cu), rest = tiles % (c * t.per_cu);
+    double time = (double)full * (t.start + t.step * steps);
+    if (rest > 0) time += rest <= c ? t.start1 + t.step1 * steps : t.start + t.step * steps;
+    if (time < best_t) {
       best_t = time;
-      best = c.tile;
+      best = t.tile;
     }
   }
   return best;
@@ -624,7 +633,7 @@ int choose_tile(int64_t m, int64_t n, int cus) {
 }  // namespace
 
 int mx4_gemm_tile(int64_t m, int64_t n, int64_t k, int64_t call_rows, int cus) {
-  return few_rows(call_rows, n, k) ? 16 : choose_tile(m, n, cus);
+  return few_rows(call_rows, n, k) ? 16 : choose_tile(m, n, k, cus);
 }
 
 LaunchPlan plan_mx4_gemm(int64_t m, int64_t n, int64_t k, int tile, int cus) {
