@@ -114,8 +114,8 @@ convrot_status convrot_gemm_mx4(const uint8_t* x_codes, const uint8_t* x_scales,
   const char* fn = "convrot_gemm_mx4";
   DType dt;
   if (!dtype_of(dtype, &dt)) return fail(CONVROT_E_INVALID_ARG, "%s: dtype=%d", fn, (int)dtype);
-  if (tile != 0 && tile != 16 && tile != 64 && tile != 128 && tile != 192 && tile != 256 &&
-      tile != 384)
+  if (tile != 0 && tile != 16 && tile != 64 && tile != 96 && tile != 128 && tile != 160 &&
+      tile != 192 && tile != 256 && tile != 384)
     return fail(CONVROT_E_INVALID_ARG, "%s: tile=%d not supported", fn, tile);
   if (tile == 16 && m > 64)
     return fail(CONVROT_E_INVALID_ARG, "%s: tile=16 takes at most 64 rows (m=%lld)", fn,

@@ -19,11 +19,16 @@
 // power limit: the clock falls to 1.64 GHz and the MFMA pipes are busy 0.54 of
 // it (with nearly no copies the same loop takes 0.95 ms, without its LDS reads
 // as well 0.90; reads from LDS alone cost 2-4%). Grids that leave the power
-// alone are bound by the rate at which a CU streams operands from L2, some 26
-// bytes per cycle: 4608 x 3840 x 3840 41 us (2.23 GHz, busy 0.35), and a lone
-// block's K-step takes a time proportional to its tile's rows. Tried without
-// gain: reading the fragments of a whole K-step ahead (128 and 64 tiles), four-
-// stage rings for the 128 tile, starting the first blocks at different times.
+// alone are bound by their operands' way into the XCDs' L2: copies without
+// any arithmetic take 0.46 us a K-step for 216 tiles of 128, with three stages
+// or four, the product 0.48 (lines that L2 holds already come at 52-62 bytes per
+// cycle and CU, these at 30). Up to 192 rows a tile, four waves do all
+// the copies: issued between the MFMAs of the waves that compute, they cost 512 x
+// 5120 x 5120 17.8 instead of 13.2 us. The two large tiles' accumulators leave no
+// registers for that (4608 x 3840 x 3840 39-41 us, 2.28 GHz, busy 0.35). Tried
+// without gain: reading the fragments of a whole K-step ahead, a fourth stage,
+// eight computing or eight copying waves, starting the first blocks at different
+// times.
 //
 // The end of K: what stands in the place of columns behind a row's end are
 // codes of the next row (the copies stop at the tensor's end) with both
@@ -345,7 +350,7 @@ __global__ __launch_bounds__(64 * (WM * WN + NP), MINB) void gemm_mx4_kernel(
     if constexpr (NP == 0) wait_stage(min(LA - 2, nk - 2 - s));  // stage s + 1 landed
     wait_lgkm0();  // this wave's reads of stage s are done
     lds_barrier();
-    const bool late = NP == 0 && NW == 8 && wave >= 4;
+    const bool late = NP == 0 && wave >= 4;
     if constexpr (NP == 0) {
       if (!late && s + LA < nk) issue(s + LA, (s + LA) % NS);
     }
@@ -552,21 +557,60 @@ int64_t rows_cost(int64_t m, int64_t n, int64_t cus, int* nf) {
   return best;
 }
 
-// Which kernel takes m rows. Estimated from measurements on 256 CUs: few rows
-// 3.7 us + 32 KB per us through a CU; 64 x 64 tiles 4.4 us + 0.285 us a K-step
-// (0.43 with two blocks on a CU). Measured, few rows / tiles: 13824 x 5120 with
-// 16, 32, 64 rows 10.2, 12.0, 19.8 / 10.1, 10.3, 10.6 us; 5120 x 13824 13.6,
-// 17.8, 25.0 / 19.8, 19.8, 20.0; 3840 x 3840 5.5, 6.5, 8.6 / 8.5, 8.5, 8.7. The
-// two add in different orders, so the choice goes by the shape alone and not
-// by the device's CUs.
+// The tiled kernel's tiles by the number that names them, and what a round of
+// them over the CUs (per_cu to a CU) takes in us: `start` (first copies,
+// epilogue) and `step` for each 256 of K; a last round that leaves one to a CU
+// is shorter (start1, step1).
+struct Tile {
+  int tile, bm, bn, per_cu;
+  double start, step, start1, step1;
+};
+constexpr Tile kTiles[] = {
+    {384, 384, 192, 1, 6.7, 1.24, 6.7, 1.24}, {256, 256, 256, 1, 5.1, 1.14, 5.1, 1.14},
+    {192, 192, 192, 1, 5.2, 0.65, 5.2, 0.65}, {160, 128, 192, 1, 2.75, 0.67, 2.75, 0.67},
+    {128, 128, 128, 2, 2.3, 0.85, 2.3, 0.48}, {96, 64, 128, 2, 2.0, 0.57, 1.35, 0.38},
+    {64, 64, 64, 2, 4.1, 0.40, 1.0, 0.30}};
+
+// The tile of least estimated time, and that time in us. Measured on 620 shapes
+// with weights in the last-level cache (m 70 to 20000, n 512 to 14400, k 512 to
+// 14400): 0.3% behind each shape's best tile on average, 11% at most; with weights
+// from memory 0.4% and 34% (140 x 5504 x 12256, just more 64 tiles than CUs). The
+// small tiles earn their places where a few big ones leave CUs idle, best / next
+// best of the others: 64 x 128 tiles 256 x 5120 x 13824 19.9 / 23.6 us, 128 tiles
+// with one to a CU 512 x 5120 x 13824 26.8 / 30.3, with two 2048 x 9216 x 768 19.3 /
+// 21.5, 128 x 192 tiles 1024 x 5120 x 5120 20.2 / 22.2; 384 x 192 tiles 4608 x 3840 x
+// 3840 41.7 / 46.4. Bits do not depend on the tile.
+double tile_us(int64_t m, int64_t n, int64_t k, int cus, int* tile) {
+  const int64_t c = cus > 0 ? cus : 1;
+  const double steps = (double)((k + kMx4Tile - 1) / kMx4Tile);
+  double best = 1e300;
+  for (const Tile& t : kTiles) {
+    const int64_t tiles = ((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn);
+    const int64_t full = tiles / (c * t.per_cu), rest = tiles % (c * t.per_cu);
+    double us = (double)full * (t.start + t.step * steps);
+    if (rest > 0) us += rest <= c ? t.start1 + t.step1 * steps : t.start + t.step * steps;
+    if (us < best) {
+      best = us;
+      *tile = t.tile;
+    }
+  }
+  return best;
+}
+
+// Whether the few-rows kernel takes m rows: 3 us + 22 KB per us through a CU
+// against the tiles' time or, with long weights, 4.2 TB/s of their bytes.
+// Measured, few rows / 64 tiles, weights from memory: 13824 x 5120 with 8, 16, 32,
+// 64 rows 9.7, 10.2, 12.1, 23.0 / 9.9, 9.9, 10.4, 12.0 us; 5120 x 13824 11.7, 13.1,
+// 17.7, 24.9 / 17.4, 17.4, 17.8, 20.2; over 344 shapes 0.5% behind the better one
+// on average, over 286 with weights in the last-level cache 0.6%. The two add in different orders, so the choice goes by the shape alone and
+// not by the device's CUs.
 bool few_rows(int64_t m, int64_t n, int64_t k) {
   if (m > kFewRows) return false;
-  constexpr int64_t cus = 256;
-  int nf;
-  const double rows_us = 3.7 + (double)rows_cost(m, n, cus, &nf) * (double)(k / 2) / 32e3;
-  const int64_t tiles = (n + 63) / 64, steps = (k + kMx4Tile - 1) / kMx4Tile;
-  const double step_us = tiles <= cus ? 0.285 : 0.43 * (double)((tiles + 2 * cus - 1) / (2 * cus));
-  return rows_us < 4.4 + step_us * (double)steps;
+  constexpr int cus = 256;
+  int nf, tile;
+  const double rows_us = 3.0 + (double)rows_cost(m, n, cus, &nf) * (double)(k / 2) / 22e3;
+  const double weight_us = (double)n * (double)k * (17.0 / 32) / 4.2e6;
+  return rows_us < fmax(3.0 + tile_us(m, n, k, cus, &tile), weight_us);
 }
 
 template <bool F16, int MF>
@@ -577,63 +621,33 @@ hipError_t launch_rows_n(int nf, const Args& a) {
 }
 
 template <bool F16>
-hipError_t launch_tile(const LaunchPlan& p, const Args& a) {
-  switch (p.tile_m) {
+hipError_t launch_tile(const LaunchPlan& p, int tile, const Args& a) {
+  switch (tile) {
     case 16:
       switch (row_groups(a.m)) {
         case 1: return launch_rows_n<F16, 1>(p.tile_n / 16, a);
         case 2: return launch_rows_n<F16, 2>(p.tile_n / 16, a);
         default: return launch_rows_n<F16, 4>(p.tile_n / 16, a);
       }
-    case 64: return launch_cfg<F16, 64, 64, 2, 2, 4, 2>(a);
-    case 128: return launch_cfg<F16, 128, 128, 2, 2, 2, 2>(a);
+    case 64: return launch_cfg<F16, 64, 64, 2, 2, 4, 2, 4>(a);
+    case 96: return launch_cfg<F16, 64, 128, 2, 2, 3, 2, 4>(a);
+    case 128:  // one tile to a CU with a longer ring, or two
+      if (p.grid <= compute_units()) return launch_cfg<F16, 128, 128, 2, 2, 3, 1, 4>(a);
+      return launch_cfg<F16, 128, 128, 2, 2, 2, 2, 4>(a);
+    case 160: return launch_cfg<F16, 128, 192, 2, 2, 3, 1, 4>(a);
     case 192: return launch_cfg<F16, 192, 192, 2, 2, 3, 1, 4>(a);
     case 384: return launch_cfg<F16, 384, 192, 4, 2, 2, 1>(a);
     default: return launch_cfg<F16, 256, 256, 2, 4, 2, 1>(a);
   }
 }
 
-// The tiled kernel's tile of least estimated time: rounds of concurrent tiles
-// over the CUs times a round's duration, `start` (first copies, epilogue) and
-// `step` for each 256 of K, in us. The two small tiles run two to a CU, and a
-// last round that leaves one to a CU is shorter. With long rows the steps count,
-// with short ones start and epilogue: 512 x 13824 x 13824 takes 192 tiles (58
-// us, 128 74, 64 108), 4096 x 13824 x 768 128 tiles (44, 192 58, 256 54),
-// 32760 x 13824 x 5120 256 tiles. Fitted to 398 shapes (m 80 to 8192, n and k 768
-// to 13824); over 240 other random ones (m to 20000, k 512 to 14400) it is 0.5%
-// behind each shape's best tile on average and 13% at most, rounds of one length
-// whatever K is 2.0% and 26%. Bits do not depend on the tile.
-int choose_tile(int64_t m, int64_t n, int64_t k, int cus) {
-  const struct {
-    int tile, bm, bn, per_cu;
-    double start, step;      // all CUs with per_cu tiles
-    double start1, step1;    // one tile per CU
-  } cands[] = {{384, 384, 192, 1, 8.2, 1.27, 8.2, 1.27},
-               {256, 256, 256, 1, 6.5, 1.20, 6.5, 1.20},
-               {192, 192, 192, 1, 6.0, 0.64, 6.0, 0.64},
-               {128, 128, 128, 2, 1.9, 0.89, 1.2, 0.73},
-               {64, 64, 64, 2, 2.2, 0.46, 1.1, 0.29}};
-  const int64_t c = cus > 0 ? cus : 1;
-  const double steps = (double)((k + kMx4Tile - 1) / kMx4Tile);
-  int best = 128;
-  double best_t = 1e300;
-  for (const auto& t : cands) {
-    const int64_t tiles = ((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn);
-    const int64_t full = tiles / (c * t.per_cu), rest = tiles % (c * t.per_cu);
-    double time = (double)full * (t.start + t.step * steps);
-    if (rest > 0) time += rest <= c ? t.start1 + t.step1 * steps : t.start + t.step * steps;
-    if (time < best_t) {
-      best_t = time;
-      best = t.tile;
-    }
-  }
-  return best;
-}
-
 }  // namespace
 
 int mx4_gemm_tile(int64_t m, int64_t n, int64_t k, int64_t call_rows, int cus) {
-  return few_rows(call_rows, n, k) ? 16 : choose_tile(m, n, k, cus);
+  if (few_rows(call_rows, n, k)) return 16;
+  int tile = 0;
+  tile_us(m, n, k, cus, &tile);
+  return tile;
 }
 
 LaunchPlan plan_mx4_gemm(int64_t m, int64_t n, int64_t k, int tile, int cus) {
@@ -647,9 +661,12 @@ LaunchPlan plan_mx4_gemm(int64_t m, int64_t n, int64_t k, int tile, int cus) {
     p.block = 64 * kRowWaves;
     p.grid = (n + p.tile_n - 1) / p.tile_n;
   } else {
-    p.tile_m = tile;
-    p.tile_n = tile == 384 ? 192 : tile;
-    p.block = tile <= 128 ? 256 : 512;
+    for (const Tile& t : kTiles) {
+      if (t.tile != tile) continue;
+      p.tile_m = t.bm;
+      p.tile_n = t.bn;
+    }
+    p.block = 512;
     p.grid = ((m + p.tile_m - 1) / p.tile_m) * ((n + p.tile_n - 1) / p.tile_n);
     p.xcds = xcd_count(cus);
   }
@@ -661,9 +678,10 @@ hipError_t launch_mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* 
                            const uint8_t* ws, const uint16_t* bias, int64_t m, int64_t n,
                            int64_t k, uint16_t* y, int tile, DType dt, hipStream_t st) {
   if (m == 0) return hipSuccess;
+  if (tile == 0) tile = mx4_gemm_tile(m, n, k, m, compute_units());
   const LaunchPlan p = plan_mx4_gemm(m, n, k, tile, compute_units());
   const Args a = {xc, xs, wc, ws, bias, (int)m, (int)n, (int)k, y, p.xcds, st};
-  return dt == DType::kF16 ? launch_tile<true>(p, a) : launch_tile<false>(p, a);
+  return dt == DType::kF16 ? launch_tile<true>(p, tile, a) : launch_tile<false>(p, tile, a);
 }
 
 }  // namespace convrot

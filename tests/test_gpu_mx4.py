@@ -443,3 +443,27 @@ def test_gemm_bits_do_not_depend_on_the_tile():
                 cr.convrot_set_compute_units(cus)
     finally:
         cr.convrot_set_compute_units(0)
+
+
+@pytest.mark.parametrize("tile,bm", [(96, 64), (160, 128)])
+@pytest.mark.parametrize("n,k", [(16, 32), (416, 256), (592, 800), (208, 2272)])
+def test_gemm_rectangular_tiles(tile, bm, n, k):
+    for m in (1, bm // 2 + 3, bm, bm + 1, 2 * bm + 37):
+        check_gemm(m, n, k, torch.bfloat16, True, tile)
+
+
+@pytest.mark.parametrize("m,n,k", [(129, 144, 32), (300, 400, 544), (700, 272, 4352)])
+def test_gemm_128_tiles_one_and_two_to_a_cu(m, n, k):
+    """A grid of up to one tile per CU takes the longer copy ring; the bits agree."""
+    rng = np.random.default_rng(m)
+    xc, xs, _ = held(rng, m, k, 110, 140)
+    wc, ws, _ = held(rng, n, k, 110, 140)
+    want = cr.convrot_gemm_mx4(xc, xs, wc, ws, tile=256)
+    try:
+        for cus in (256, 1):
+            cr.convrot_set_compute_units(cus)
+            for tile in (96, 128, 160):
+                assert torch.equal(cr.convrot_gemm_mx4(xc, xs, wc, ws, tile=tile), want), (cus, tile)
+            check_gemm(m, n, k, torch.float16, True, 128, lo=121, hi=128)
+    finally:
+        cr.convrot_set_compute_units(0)
