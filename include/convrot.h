@@ -457,9 +457,10 @@ convrot_status convrot_dequant_mx4(const uint8_t* codes, const uint8_t* scales, 
 
 /* y [m, n] = x . w^T (+ bias [n], nullable), x [m, k] and w [n, k] quantized.
  * tile, a test / tuning hook: 0 = automatic, 16 = the kernel for few rows (m <=
- * 64), 64, 128, 192, 256 (tile x tile outputs), 96 (64 x 128), 160 (128 x 192)
- * or 384 (384 x 192) = the tiled kernel. Any other value, or 16 with more rows,
- * is CONVROT_E_INVALID_ARG. */
+ * 64), 64, 128, 192, 256 (tile x tile outputs), 40 (64 x 32), 96 (64 x 128), 160
+ * (128 x 192) or 384 (384 x 192) = the tiled kernel. Any other value, or 16 with
+ * more rows, is CONVROT_E_INVALID_ARG; a forced tile of which there would be 2^23
+ * or more (40: 2^24) CONVROT_E_UNSUPPORTED_SHAPE. */
 convrot_status convrot_gemm_mx4(const uint8_t* x_codes, const uint8_t* x_scales,
                                 const uint8_t* w_codes, const uint8_t* w_scales,
                                 const void* bias, int64_t m, int64_t n, int64_t k, void* y,

@@ -48,8 +48,8 @@ convrot_status check_mx4_gemm(const char* fn, int64_t m, int64_t n, int64_t k) {
     return fail(CONVROT_E_UNSUPPORTED_SHAPE,
                 "%s: need k %% 32 == 0, n %% 16 == 0, k <= %lld (m=%lld n=%lld k=%lld)", fn,
                 (long long)kMaxMx4K, (long long)m, (long long)n, (long long)k);
-  // grids: 64 x 64 tiles of four waves, 16 columns a block of eight waves for few rows;
-  // the kernels' row indices run up to a tile beyond m and n
+  // grids: the tiles that the choice is left with fit far beyond this, 16 columns a block of
+  // eight waves for few rows; the kernels' row indices run up to a tile beyond m and n
   if (((m + 63) / 64) * ((n + 63) / 64) * 4 > kMaxLaunchWaves || n / 16 * 8 > kMaxLaunchWaves ||
       m > kMaxDim - 1024)
     return fail(CONVROT_E_UNSUPPORTED_SHAPE, "%s: output too large (m=%lld n=%lld)", fn,
@@ -114,13 +114,16 @@ convrot_status convrot_gemm_mx4(const uint8_t* x_codes, const uint8_t* x_scales,
   const char* fn = "convrot_gemm_mx4";
   DType dt;
   if (!dtype_of(dtype, &dt)) return fail(CONVROT_E_INVALID_ARG, "%s: dtype=%d", fn, (int)dtype);
-  if (tile != 0 && tile != 16 && tile != 64 && tile != 96 && tile != 128 && tile != 160 &&
-      tile != 192 && tile != 256 && tile != 384)
+  if (tile != 0 && tile != 16 && tile != 40 && tile != 64 && tile != 96 && tile != 128 &&
+      tile != 160 && tile != 192 && tile != 256 && tile != 384)
     return fail(CONVROT_E_INVALID_ARG, "%s: tile=%d not supported", fn, tile);
   if (tile == 16 && m > 64)
     return fail(CONVROT_E_INVALID_ARG, "%s: tile=16 takes at most 64 rows (m=%lld)", fn,
                 (long long)m);
   if (convrot_status s = check_mx4_gemm(fn, m, n, k)) return s;
+  if (tile != 0 && !mx4_gemm_grid_fits(m, n, tile))
+    return fail(CONVROT_E_UNSUPPORTED_SHAPE, "%s: too many tiles for tile=%d (m=%lld n=%lld)", fn,
+                tile, (long long)m, (long long)n);
   if (!w_codes || !w_scales) return fail(CONVROT_E_INVALID_ARG, "%s: null pointer", fn);
   if (m == 0) return ok();  // the M-sized buffers may be null
   if (!x_codes || !x_scales || !y) return fail(CONVROT_E_INVALID_ARG, "%s: null pointer", fn);

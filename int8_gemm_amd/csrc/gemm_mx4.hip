@@ -39,9 +39,9 @@
 // 16 rows of the weight straight into registers, 128 bytes of a row at a time,
 // each weight byte once for all rows; the partial sums are joined in LDS in
 // wave order. Bound by the weight's bytes and, with more rows, by each CU's
-// loads of x: 13824 x 5120 (37.6 MB) takes 9.9 us with one row, 3.8 TB/s of the
-// weight's bytes. Where those loads take longer than the copies of 64 x 64
-// tiles would, the tiled kernel is taken (few_rows below).
+// loads of x: 13824 x 5120 (37.6 MB) takes 9.5 us with one row, 4.0 TB/s of the
+// weight's bytes (8.4 us with weights in the last-level cache). Where the loads of
+// x take longer than small tiles would, the tiled kernel is taken (few_rows below).
 
 #include <atomic>
 #include <type_traits>
@@ -562,21 +562,22 @@ int64_t rows_cost(int64_t m, int64_t n, int64_t cus, int* nf) {
 // epilogue) and `step` for each 256 of K; a last round that leaves one to a CU
 // is shorter (start1, step1).
 struct Tile {
-  int tile, bm, bn, per_cu;
+  int tile, bm, bn, waves, per_cu;
   double start, step, start1, step1;
 };
 constexpr Tile kTiles[] = {
-    {384, 384, 192, 1, 6.7, 1.24, 6.7, 1.24}, {256, 256, 256, 1, 5.1, 1.14, 5.1, 1.14},
-    {192, 192, 192, 1, 5.2, 0.65, 5.2, 0.65}, {160, 128, 192, 1, 2.75, 0.67, 2.75, 0.67},
-    {128, 128, 128, 2, 2.3, 0.85, 2.3, 0.48}, {96, 64, 128, 2, 2.0, 0.57, 1.35, 0.38},
-    {64, 64, 64, 2, 4.1, 0.40, 1.0, 0.30}};
+    {384, 384, 192, 8, 1, 6.7, 1.24, 6.7, 1.24}, {256, 256, 256, 8, 1, 5.1, 1.14, 5.1, 1.14},
+    {192, 192, 192, 8, 1, 5.2, 0.65, 5.2, 0.65}, {160, 128, 192, 8, 1, 2.75, 0.67, 2.75, 0.67},
+    {128, 128, 128, 8, 2, 2.3, 0.85, 2.3, 0.48}, {96, 64, 128, 8, 2, 2.0, 0.57, 1.35, 0.38},
+    {64, 64, 64, 8, 2, 4.1, 0.40, 1.0, 0.30},   {40, 64, 32, 4, 2, 2.0, 0.34, 1.0, 0.28}};
 
 // The tile of least estimated time, and that time in us. Measured on 620 shapes
 // with weights in the last-level cache (m 70 to 20000, n 512 to 14400, k 512 to
 // 14400): 0.3% behind each shape's best tile on average, 11% at most; with weights
 // from memory 0.4% and 34% (140 x 5504 x 12256, just more 64 tiles than CUs). The
 // small tiles earn their places where a few big ones leave CUs idle, best / next
-// best of the others: 64 x 128 tiles 256 x 5120 x 13824 19.9 / 23.6 us, 128 tiles
+// best of the others: 64 x 32 tiles 64 x 5120 x 13824 12.8 / 14.1 us (weights from
+// memory 16.1 / 19.7), 64 x 128 tiles 256 x 5120 x 13824 19.9 / 23.6, 128 tiles
 // with one to a CU 512 x 5120 x 13824 26.8 / 30.3, with two 2048 x 9216 x 768 19.3 /
 // 21.5, 128 x 192 tiles 1024 x 5120 x 5120 20.2 / 22.2; 384 x 192 tiles 4608 x 3840 x
 // 3840 41.7 / 46.4. Bits do not depend on the tile.
@@ -586,6 +587,7 @@ double tile_us(int64_t m, int64_t n, int64_t k, int cus, int* tile) {
   double best = 1e300;
   for (const Tile& t : kTiles) {
     const int64_t tiles = ((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn);
+    if (tiles * t.waves > kMaxLaunchWaves) continue;
     const int64_t full = tiles / (c * t.per_cu), rest = tiles % (c * t.per_cu);
     double us = (double)full * (t.start + t.step * steps);
     if (rest > 0) us += rest <= c ? t.start1 + t.step1 * steps : t.start + t.step * steps;
@@ -599,18 +601,19 @@ double tile_us(int64_t m, int64_t n, int64_t k, int cus, int* tile) {
 
 // Whether the few-rows kernel takes m rows: 3 us + 22 KB per us through a CU
 // against the tiles' time or, with long weights, 4.2 TB/s of their bytes.
-// Measured, few rows / 64 tiles, weights from memory: 13824 x 5120 with 8, 16, 32,
-// 64 rows 9.7, 10.2, 12.1, 23.0 / 9.9, 9.9, 10.4, 12.0 us; 5120 x 13824 11.7, 13.1,
-// 17.7, 24.9 / 17.4, 17.4, 17.8, 20.2; over 344 shapes 0.5% behind the better one
-// on average, over 286 with weights in the last-level cache 0.6%. The two add in different orders, so the choice goes by the shape alone and
-// not by the device's CUs.
+// Measured, few rows / tiles, weights from memory: 13824 x 5120 with 8, 16, 32, 64
+// rows 9.5, 10.0, 11.9, 22.5 / 9.6, 9.7, 10.2, 11.7 us; 5120 x 13824 11.6, 13.0, 17.5,
+// 24.7 / 15.8, 15.6, 15.6, 16.1; over 302 shapes of up to 256 rows 0.4% behind the best
+// kernel on average, over 221 with weights in the last-level cache 0.3%. The two
+// add in different orders, so the choice goes by the shape alone and not by the
+// device's CUs.
 bool few_rows(int64_t m, int64_t n, int64_t k) {
   if (m > kFewRows) return false;
   constexpr int cus = 256;
   int nf, tile;
   const double rows_us = 3.0 + (double)rows_cost(m, n, cus, &nf) * (double)(k / 2) / 22e3;
   const double weight_us = (double)n * (double)k * (17.0 / 32) / 4.2e6;
-  return rows_us < fmax(3.0 + tile_us(m, n, k, cus, &tile), weight_us);
+  return rows_us < fmax(4.0 + tile_us(m, n, k, cus, &tile), weight_us);
 }
 
 template <bool F16, int MF>
@@ -629,6 +632,7 @@ hipError_t launch_tile(const LaunchPlan& p, int tile, const Args& a) {
         case 2: return launch_rows_n<F16, 2>(p.tile_n / 16, a);
         default: return launch_rows_n<F16, 4>(p.tile_n / 16, a);
       }
+    case 40: return launch_cfg<F16, 64, 32, 2, 1, 4, 2, 2>(a);
     case 64: return launch_cfg<F16, 64, 64, 2, 2, 4, 2, 4>(a);
     case 96: return launch_cfg<F16, 64, 128, 2, 2, 3, 2, 4>(a);
     case 128:  // one tile to a CU with a longer ring, or two
@@ -642,6 +646,15 @@ hipError_t launch_tile(const LaunchPlan& p, int tile, const Args& a) {
 }
 
 }  // namespace
+
+bool mx4_gemm_grid_fits(int64_t m, int64_t n, int tile) {
+  if (tile == 16) return n / 16 * kRowWaves <= kMaxLaunchWaves;
+  for (const Tile& t : kTiles)
+    if (t.tile == tile &&
+        ((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn) * t.waves <= kMaxLaunchWaves)
+      return true;
+  return false;
+}
 
 int mx4_gemm_tile(int64_t m, int64_t n, int64_t k, int64_t call_rows, int cus) {
   if (few_rows(call_rows, n, k)) return 16;
@@ -665,8 +678,8 @@ LaunchPlan plan_mx4_gemm(int64_t m, int64_t n, int64_t k, int tile, int cus) {
       if (t.tile != tile) continue;
       p.tile_m = t.bm;
       p.tile_n = t.bn;
+      p.block = t.waves * 64;
     }
-    p.block = 512;
     p.grid = ((m + p.tile_m - 1) / p.tile_m) * ((n + p.tile_n - 1) / p.tile_n);
     p.xcds = xcd_count(cus);
   }

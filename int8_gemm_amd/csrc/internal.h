@@ -138,6 +138,8 @@ hipError_t launch_norm_residual(const NormArgs& a, int g, const SignMask& sm, DT
 // kernels sum in different orders, so one call keeps to one of them whatever
 // its slices are. 16: the few-rows kernel.
 int mx4_gemm_tile(int64_t m, int64_t n, int64_t k, int64_t call_rows, int cus);
+// A grid of the tile's blocks counts its threads in 32 bits.
+bool mx4_gemm_grid_fits(int64_t m, int64_t n, int tile);
 LaunchPlan plan_mx4_gemm(int64_t m, int64_t n, int64_t k, int tile, int cus);
 
 }  // namespace convrot

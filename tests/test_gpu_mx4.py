@@ -445,7 +445,7 @@ def test_gemm_bits_do_not_depend_on_the_tile():
         cr.convrot_set_compute_units(0)
 
 
-@pytest.mark.parametrize("tile,bm", [(96, 64), (160, 128)])
+@pytest.mark.parametrize("tile,bm", [(40, 64), (96, 64), (160, 128)])
 @pytest.mark.parametrize("n,k", [(16, 32), (416, 256), (592, 800), (208, 2272)])
 def test_gemm_rectangular_tiles(tile, bm, n, k):
     for m in (1, bm // 2 + 3, bm, bm + 1, 2 * bm + 37):
@@ -462,7 +462,7 @@ def test_gemm_128_tiles_one_and_two_to_a_cu(m, n, k):
     try:
         for cus in (256, 1):
             cr.convrot_set_compute_units(cus)
-            for tile in (96, 128, 160):
+            for tile in (40, 96, 128, 160):
                 assert torch.equal(cr.convrot_gemm_mx4(xc, xs, wc, ws, tile=tile), want), (cus, tile)
             check_gemm(m, n, k, torch.float16, True, 128, lo=121, hi=128)
     finally:

@@ -253,3 +253,17 @@ def test_oracle_pins():
     assert codes.shape == (5, 144) and scales.shape == (2, 16, 8)
     back = ref.unpack(codes, scales)
     assert np.array_equal(back[0], code) and np.array_equal(back[1], exps)
+
+
+def test_gemm_grids_of_many_tiles(lib):
+    """Grids count their threads in 32 bits: a forced small tile is refused where
+    there are too many, and the automatic choice passes it over."""
+    def gemm(m, n, tile):
+        return lib.convrot_gemm_mx4(A, B, C, D, None, m, n, 32, E, 0, tile, None)
+    m, n = 64 << 13, 64 << 10       # 2^23 tiles of 64 x 64
+    assert gemm(m, n, 64) == 3 and gemm(m, n, 40) == 3
+    assert gemm(2 * m, n, 0) == 3   # 2^24: beyond the documented sizes
+    for cus in (256, 1):
+        p = cr.convrot_plan_launch("gemm_mx4", m=2 * m - 64, n=n, k=32, compute_units=cus)
+        assert p["grid"] * p["block"] < 1 << 32
+        assert p["tile_m"] * p["tile_n"] > 64 * 64
