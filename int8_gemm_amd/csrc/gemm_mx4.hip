@@ -18,17 +18,19 @@
 // Measured: 32760 x 13824 x 5120 1.18-1.24 ms, 3.7-3.9 PFLOP/s, under the
 // power limit: the clock falls to 1.64 GHz and the MFMA pipes are busy 0.54 of
 // it (with nearly no copies the same loop takes 0.95 ms, without its LDS reads
-// as well 0.90; reads from LDS alone cost 2-4%). Grids that leave the power
-// alone are bound by their operands' way into the XCDs' L2: copies without
-// any arithmetic take 0.46 us a K-step for 216 tiles of 128, with three stages
-// or four, the product 0.48 (lines that L2 holds already come at 52-62 bytes per
-// cycle and CU, these at 30). Up to 192 rows a tile, four waves do all
-// the copies: issued between the MFMAs of the waves that compute, they cost 512 x
-// 5120 x 5120 17.8 instead of 13.2 us. The two large tiles' accumulators leave no
-// registers for that (4608 x 3840 x 3840 39-41 us, 2.28 GHz, busy 0.35). Tried
-// without gain: reading the fragments of a whole K-step ahead, a fourth stage,
-// eight computing or eight copying waves, starting the first blocks at different
-// times.
+// as well 0.90; reads from LDS alone cost 2-4%). So are grids of some 240 large
+// tiles: a K-step of a 384 x 192 tile takes 0.97 us without its copies and 1.16
+// with them when 20 CUs work, 1.69 and 1.99 when 240 do (4608 x 3840 x 3840 39-45
+// us). Smaller grids are bound by their operands' way into the XCDs' L2: copies
+// without any arithmetic take 0.46 us a K-step for 216 tiles of 128, with three
+// stages or four, the product 0.48 (lines that L2 holds already come at 52-62 bytes
+// per cycle and CU, these at 30). Up to 192 rows a tile, waves of their own do the
+// copies: issued between the MFMAs of the waves that compute, they cost 512 x 5120 x
+// 5120 17.8 instead of 13.3 us. The two large tiles' accumulators leave no registers
+// for that. Tried without gain: reading the fragments of a whole K-step ahead,
+// a fourth stage for the 128 tile, eight computing or eight copying waves, K-steps
+// of half the length with twice the stages (copies alone 17.3 -> 21.8 us at 4608 x
+// 3840 x 3840), starting the first blocks at different times.
 //
 // The end of K: what stands in the place of columns behind a row's end are
 // codes of the next row (the copies stop at the tensor's end) with both
