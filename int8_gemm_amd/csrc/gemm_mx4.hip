@@ -30,7 +30,8 @@
 // for that. Tried without gain: reading the fragments of a whole K-step ahead,
 // a fourth stage for the 128 tile, eight computing or eight copying waves, K-steps
 // of half the length with twice the stages (copies alone 17.3 -> 21.8 us at 4608 x
-// 3840 x 3840), starting the first blocks at different times.
+// 3840 x 3840), a wave that touches the lines four stages ahead (512 x 5120 x 5120
+// 13.0 -> 16.4), starting the first blocks at different times.
 //
 // The end of K: what stands in the place of columns behind a row's end are
 // codes of the next row (the copies stop at the tensor's end) with both
