@@ -68,7 +68,8 @@ __device__ __forceinline__ v8i wide(v4i a) { return __builtin_shufflevector(a, a
 
 // global -> LDS copy of 16 bytes per lane (as dma16) from a per-lane address,
 // by the lanes of `lanes` only; the mask is set inside the asm block because a
-// divergent branch around the copy would split the K-loop's schedule
+// divergent branch around the copy would split the K-loop's schedule. The two
+// moves of the mask stand for the wait state that the copy needs behind M0.
 __device__ __forceinline__ void dma16_at(const uint8_t* p, uint32_t lds_base, uint64_t lanes) {
   uint64_t saved;
   asm volatile(
