@@ -21,11 +21,15 @@ __device__ __forceinline__ void wait_vmcnt() {
 // LDS write of the builtin form as pending LDS traffic and drains it around
 // every later LDS read) stays out of the way; completion is tracked by the
 // explicit vmcnt waits of the K-loop. The instruction has no VGPR result.
-// A copy to LDS must follow a scalar write of M0 by one wait state at least,
-// else it may still take the old M0; the compiler adds none inside the block.
+// The compiler fills no wait states inside the block. Two are asked for: one
+// between a scalar write of M0 and a copy to LDS, and five between a vector
+// instruction that writes an SGPR (v_readfirstlane of the base) and a memory
+// access that reads it. The scalar copy of the base is the one, and needs none
+// itself, so the access reads an SGPR that no vector instruction wrote.
 __device__ __forceinline__ void dma16(const int8_t* sbase, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :
+  const int8_t* base;
+  asm volatile("s_mov_b32 m0, %3\n\ts_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
+               : "=&s"(base)
                : "v"(voff), "s"(sbase), "s"(lds_base)
                : "memory", "m0");
 }

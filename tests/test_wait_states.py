@@ -4,7 +4,9 @@ The compiler keeps the distances that the hardware asks for between its own
 instructions but does not look into blocks of inline assembly, which the
 global -> LDS copies are written in (csrc/lds_copy.h). Checked along the
 straight-line order of every kernel:
-  - a scalar write of M0, then a copy to LDS: one wait state."""
+  - a scalar write of M0, then a copy to LDS: one wait state;
+  - a vector instruction's write of an SGPR, then a memory access that reads
+    it: five."""
 
 import os
 import re
@@ -64,6 +66,14 @@ def before(lines, at, states):
         states -= int(args[0]) + 1 if op == "s_nop" else 1
 
 
+def sgprs(operand):
+    """The numbers of the SGPRs that an operand names."""
+    found = set()
+    for m in re.finditer(r"\bs(\d+)\b|\bs\[(\d+):(\d+)\]", operand):
+        found |= {int(m[1])} if m[1] else set(range(int(m[2]), int(m[3]) + 1))
+    return found
+
+
 def copies(lines):
     return [i for i, line in enumerate(lines) if split(line)[0].startswith("global_load_lds")]
 
@@ -76,5 +86,25 @@ def test_copies_wait_for_m0(kernels):
             for op, args in before(lines, i, 1):
                 if op.startswith("s_") and args[0] == "m0":
                     bad.append((name, lines[i - 1], lines[i]))
+    assert seen > 100
+    assert not bad, f"{len(bad)} of {seen}: {bad[0]}"
+
+
+def test_accesses_wait_for_sgprs_that_vector_instructions_write(kernels):
+    seen, bad = 0, []
+    for (_, name), lines in kernels.items():
+        for i, line in enumerate(lines):
+            op, args = split(line)
+            if not re.match(r"(global|flat|buffer|scratch)_", op):
+                continue
+            read = set().union(*(sgprs(a) for a in args))
+            seen += bool(read)
+            for was, to in before(lines, i, 5) if read else ():
+                if was.startswith("s_"):
+                    read = read - sgprs(to[0])  # a scalar write since
+                # results: the first operand, or the first two (carries)
+                elif was.startswith("v_") and \
+                        sgprs(to[0] + " " + (to[1] if "_co_" in was else "")) & read:
+                    bad.append((name, was, to, line))
     assert seen > 100
     assert not bad, f"{len(bad)} of {seen}: {bad[0]}"
