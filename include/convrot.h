@@ -490,7 +490,8 @@ size_t convrot_linear_mx4_workspace_size(int64_t m, int64_t n, int64_t k);
  *   CONVROT_NORM_RMS    v / sqrt(mean(v^2) + eps) [* weight]
  *   CONVROT_NORM_LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) [* weight]
  * (post_norm may be CONVROT_NORM_NONE). norm() reads x' as it was rounded; all
- * else is fp32. h goes out in 16 bits (h), rotated and quantized for
+ * else is fp32, and a norm takes finite rows of any magnitude (a power of two is
+ * taken out of a row whose squares fp32 does not hold). h goes out in 16 bits (h), rotated and quantized for
  * convrot_gemm_mx4 (h_codes, h_scales, g, rot_seed: bit for bit what
  * convrot_quantize_mx4 gives for the 16-bit h), or both.
  *   x, o, x_out, h [m, k]; post_weight, weight [k]; all in dtype. Null: absent.

@@ -77,12 +77,51 @@ __device__ __forceinline__ u4 pack(const float (&f)[8]) {
               pack16x2<F16>(f[6], f[7])};
 }
 
+// The largest |v| of a row by its bits (finite < inf < NaN), likewise.
+__device__ __forceinline__ uint32_t row_max(uint32_t v, RowShape rs, float* part) {
+  typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+  v = max(v, mx4_dpp<kDppXor1>(v));
+  v = max(v, mx4_dpp<kDppXor2>(v));
+  v = max(v, mx4_dpp<kDppMirror8>(v));
+  if (rs.shift > 3) v = max(v, mx4_dpp<kDppMirror16>(v));
+  if (rs.shift > 4) {
+    const u2v r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(r.x, r.y);
+  }
+  if (rs.shift > 5) {
+    const u2v r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(r.x, r.y);
+  }
+  if (rs.waves == 1) return v;
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) part[wave] = __uint_as_float(v);
+  __syncthreads();
+  uint32_t m = __float_as_uint(part[0]);
+  for (int w = 1; w < rs.waves; ++w) m = max(m, __float_as_uint(part[w]));
+  return m;
+}
+
 // Normalise v in place (without its weight). `in` marks the lane's chunks that
-// lie in the row; the others come in as 0 and go out as anything. `part` has 2 *
-// kMaxWaves slots.
+// lie in the row; the others come in as 0 and go out as anything. `part` has
+// kPartSlots slots. reload(i, c): chunk i of v again.
+//
+// Squares in fp32 reach their range's ends where bf16 values do not: above 2^64
+// they overflow, and below 2^-75 they vanish, which counts where eps is as small.
+// v / sqrt(mean(v^2) + eps) stays the same when v is divided by 2^by and eps by
+// 2^(2 by), exactly, so a row whose mean square lies outside [2^-100, inf) is
+// taken once more with the larger of its largest value and sqrt(eps) brought to
+// 2^40. All waves of a row see the same sums and go the same way; rows that share
+// a wave with such a one repeat their own with by = 0, to the same bits. The
+// repetition reads the row from memory chunk by chunk, which leaves the registers
+// of the common path as they are.
+constexpr int kPartSlots = 5 * kMaxWaves;
+
+template <typename Reload>
 __device__ __forceinline__ void normalise(float (&v)[4][8], const bool (&in)[4], NormKind kind,
-                                          float k, float eps, RowShape rs, float* part) {
-  if (kind == NormKind::kLayer) {
+                                          float k, float eps, RowShape rs, float* part,
+                                          Reload reload) {
+  const bool layer = kind == NormKind::kLayer;
+  if (layer) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -102,7 +141,47 @@ __device__ __forceinline__ void normalise(float (&v)[4][8], const bool (&in)[4],
     for (int e = 0; e < 8; ++e) c = __builtin_fmaf(v[i][e], v[i][e], c);
     q += in[i] ? c : 0.f;
   }
-  const float r = 1.0f / sqrtf(row_sum(q, rs, part) / k + eps);
+  float ms = row_sum(q, rs, part) / k + eps;
+  const bool again = !(ms >= 0x1p-100f && ms < __builtin_inff());
+  if (__builtin_expect(__any(again), 0)) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float c[8];
+      reload(i, c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(c[e]) & 0x7FFFFFFFu);
+    }
+    top = row_max(top, rs, part + 2 * kMaxWaves) >> 23;
+    int by = max((int)top - 127, ((int)(__float_as_uint(eps) >> 23) - 127) >> 1) - 40;
+    if (!again || top == 255) by = 0;  // an infinity or a NaN gives what it gave
+    float mean = 0.f;
+    if (layer) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float c[8];
+        reload(i, c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += __builtin_ldexpf(c[e], -by);
+      }
+      mean = row_sum(s, rs, part + 3 * kMaxWaves) / k;
+    }
+    q = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      reload(i, v[i]);
+      float c = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[i][e] = __builtin_ldexpf(v[i][e], -by) - mean;
+        c = __builtin_fmaf(v[i][e], v[i][e], c);
+      }
+      q += in[i] ? c : 0.f;
+    }
+    ms = row_sum(q, rs, part + 4 * kMaxWaves) / k + __builtin_ldexpf(eps, -2 * by);
+  }
+  const float r = 1.0f / sqrtf(ms);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -114,11 +193,12 @@ __device__ __forceinline__ void normalise(float (&v)[4][8], const bool (&in)[4],
 // EARLY: a phase's vectors are loaded before its sums, so that their latencies
 // overlap (77 x 3840: 7.7 -> 6.5 us), otherwise where they are used, with
 // fewer registers and so more rows in flight (32760 x 5120: 244 instead of
-// 267 us).
+// 267 us). Five waves a SIMD are asked for where the allocator misses their 96
+// registers by one (g = 1, 32760 x 5120: 244 -> 226 us).
 template <int G, bool F16, bool EARLY>
-__global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs a, SignMask sm,
-                                                                       RowShape rs) {
-  __shared__ float part[4 * kMaxWaves];
+__global__ __launch_bounds__(64 * kMaxWaves, G == 1 && !EARLY ? 5 : 1) void norm_residual_kernel(
+    NormArgs a, SignMask sm, RowShape rs) {
+  __shared__ float part[2 * kPartSlots];
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
   const int64_t at = rs.waves == 1 ? (((int64_t)blockIdx.x * kBlockWaves + wave) << (6 - rs.shift)) +
@@ -144,6 +224,15 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
 #pragma unroll
     for (int i = 0; i < 4; ++i) to[i] = load(p, i);
   };
+  // a chunk of the lane's elements of x' or o again, as fp32; the empty asm
+  // keeps addresses and values from being held in registers up to there
+  auto again_from = [&](const uint16_t* p) {
+    return [&, p](int i, float (&c)[8]) {
+      int64_t from = base;
+      asm volatile("" : "+v"(from));
+      mx4_unpack8<F16>(load(p + from, i), c);
+    };
+  };
   // v = v * by (+ v)
   auto multiply = [](float (&v)[4][8], const u4 (&by)[4], bool plus) {
 #pragma unroll
@@ -167,7 +256,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
 #pragma unroll
     for (int i = 0; i < 4; ++i) mx4_unpack8<F16>(w3[i], v[i]);
     if (a.post_norm != NormKind::kNone)
-      normalise(v, in, a.post_norm, (float)a.k, a.eps, rs, part);
+      normalise(v, in, a.post_norm, (float)a.k, a.eps, rs, part, again_from(a.o));
     if (a.post_weight) {
       if (!EARLY) load4(w1, a.post_weight + col);
       multiply(v, w1, false);
@@ -193,7 +282,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_residual_kernel(NormArgs 
   if (EARLY && a.shift) load4(w3, shift);
 #pragma unroll
   for (int i = 0; i < 4; ++i) mx4_unpack8<F16>(xw[i], v[i]);
-  normalise(v, in, a.norm, (float)a.k, a.eps, rs, part + 2 * kMaxWaves);
+  normalise(v, in, a.norm, (float)a.k, a.eps, rs, part + kPartSlots,
+            again_from(a.o ? a.x_out : a.x));
   if (a.weight) {
     if (!EARLY) load4(w1, a.weight + col);
     multiply(v, w1, false);

@@ -292,3 +292,76 @@ def test_sign_of_zero(dtype):
     for t in (x_out, h):
         assert (t == 0).all()
         assert torch.equal(torch.signbit(t).cpu(), want.expand(3, 64))
+
+
+def check_norm(x, h, kind, eps):
+    """h against the norm of x with this eps; the bounds of the file's head, which hold
+    for any magnitude (a row's power of two is taken out of it before it is squared)."""
+    v, eps = f64(x), float(np.float32(eps))
+    y = ref.norm(v, kind, None, eps)
+    half, tiny = H16[x.dtype]
+    err = 64 * U * np.abs(y)
+    if kind == "layer":
+        err = err + 49 * U * np.abs(v).mean(-1, keepdims=True) \
+            / np.sqrt(v.var(-1, keepdims=True) + eps)
+    assert (np.abs(f64(h) - y) <= (half + 2 * U) * np.abs(y) + tiny + err * (1 + half)).all()
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("k", [8, 256, 520, 1024, 3840, 16384])
+def test_rows_of_every_magnitude(k, norm):
+    """bf16 rows whose squares leave the range of fp32 at either end, beside ordinary
+    rows of the same wave, which keep their bits; one large element; the largest
+    and smallest values of the format."""
+    rng = np.random.default_rng(k)
+    x = rng.standard_normal((24, k)) + 0.25
+    for r, e in enumerate((-132, -125, -100, -80, -60, -45, 40, 60, 64, 90, 120, 124)):
+        x[2 * r] *= 2.0 ** e
+    x[1] = np.where(rng.random(k) < 0.5, 1, -1) * float(torch.finfo(torch.bfloat16).max)
+    x[3] = 2.0 ** -133 * rng.integers(1, 4, k)
+    x[5, 3] = 1e30
+    x[7, 3] = -3e38
+    t = dev(x, torch.bfloat16)
+    plain = [9, 11, 13, 15, 17, 19, 21, 23]
+    for eps in (1e-6, 0.0, 1e-38, 1e-30, 1e30, 3e38):
+        _, h = cr.convrot_norm_residual(t, norm=norm, eps=eps)
+        assert torch.isfinite(h).all()
+        check_norm(t, h, norm, eps)
+        _, alone = cr.convrot_norm_residual(t[plain].contiguous(), norm=norm, eps=eps)
+        assert torch.equal(h[plain], alone)
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("k", [512, 5120])
+def test_post_norms_of_every_magnitude_and_in_place(k, norm):
+    """The same for o, with x' written over x, and for an x' that is large itself;
+    the quantized h is the 16-bit h quantized."""
+    rng = np.random.default_rng(k + 1)
+    x = rng.standard_normal((8, k))
+    o = rng.standard_normal((8, k)) * np.exp2([[-130], [-90], [-50], [0], [50], [70], [100], [125]])
+    x[1] *= 2.0 ** 100
+    o, t = dev(o, torch.bfloat16), dev(x, torch.bfloat16)
+    given = t.clone()
+    for eps in (0.0, 1e-6):
+        y, h = cr.convrot_norm_residual(t, o, post_norm=norm, norm=norm, eps=eps)
+        post = torch.zeros_like(t)
+        check_norm(o, cr.convrot_norm_residual(o, norm=norm, eps=eps)[1], norm, eps)
+        cr.convrot_norm_residual(post, o, post_norm=norm, x_out=post, norm=norm, eps=eps)
+        check_norm(o, post, norm, eps)      # 0 + post(o)
+        check_norm(y, h, norm, eps)
+        out, also = cr.convrot_norm_residual(given, o, post_norm=norm, x_out=given, norm=norm,
+                                             eps=eps)
+        assert torch.equal(out, y) and torch.equal(also, h)
+        given.copy_(t)
+        _, codes, scales = cr.convrot_norm_residual_mx4(t, o, 256, SEED, post_norm=norm, norm=norm,
+                                                        eps=eps)
+        want = cr.convrot_quantize_mx4(h, 256, SEED)
+        assert torch.equal(codes, want[0]) and torch.equal(scales[:, :8], want[1][:, :8])
+
+
+def test_rows_of_zeros_without_eps():
+    """0 / sqrt(0): NaN, in the row of zeros alone."""
+    x = torch.ones((5, 64), dtype=torch.bfloat16, device=DEV)
+    x[2] = 0
+    h = cr.convrot_norm_residual(x, eps=0.0)[1]
+    assert torch.isnan(h[2]).all() and (h[[0, 1, 3, 4]] == 1).all()
