@@ -252,14 +252,18 @@ convrot_status convrot_norm_residual(const convrot_norm_args* args, void* stream
                         a.h, a.h_codes, a.h_scales};
   for (const void* p : wide)
     if (!aligned(p, 16)) return fail(CONVROT_E_MISALIGNED, "%s: misaligned pointer", fn);
-  const int64_t samples = mods ? (m + a.rows_per_mod - 1) / a.rows_per_mod : 1;
+  // modulation rows: rows_per_mod beyond m (any value) means one for all
+  const int64_t rows_per_mod = mods && a.rows_per_mod < m ? a.rows_per_mod : m;
+  const int64_t samples = (m - 1) / rows_per_mod + 1;
   const struct {
     const void* p;
     int64_t stride;
   } mod[] = {{a.gate, a.gate_stride}, {a.scale, a.scale_stride}, {a.shift, a.shift_stride}};
   for (const auto& t : mod) {
     if (!t.p) continue;
-    if (t.stride < 0 || t.stride > ((int64_t)1 << 40))
+    // no range of 2^62 bytes: byte counts below stay inside 64 bits
+    if (t.stride < 0 || t.stride > ((int64_t)1 << 40) ||
+        (samples > 1 && t.stride > ((int64_t)1 << 60) / (samples - 1)))
       return fail(CONVROT_E_INVALID_ARG, "%s: modulation stride %lld", fn, (long long)t.stride);
     if (t.stride % 8)
       return fail(CONVROT_E_MISALIGNED, "%s: modulation stride %lld is not a multiple of 8", fn,
@@ -300,7 +304,7 @@ convrot_status convrot_norm_residual(const convrot_norm_args* args, void* stream
   n.h_codes = a.h_codes;
   n.h_scales = a.h_scales;
   n.m = m;
-  n.rows_per_mod = mods && a.rows_per_mod < m ? a.rows_per_mod : m;
+  n.rows_per_mod = rows_per_mod;
   n.k = (int)k;
   n.post_norm = (NormKind)a.post_norm;
   n.norm = (NormKind)a.norm;

@@ -365,3 +365,22 @@ def test_rows_of_zeros_without_eps():
     x[2] = 0
     h = cr.convrot_norm_residual(x, eps=0.0)[1]
     assert torch.isnan(h[2]).all() and (h[[0, 1, 3, 4]] == 1).all()
+
+
+def test_rows_per_mod_beyond_the_rows():
+    """The C call: any rows_per_mod of at least m is one modulation row for all."""
+    import ctypes
+
+    from int8_gemm_amd import mx4
+    rng = np.random.default_rng(18)
+    m, k = 10, 264
+    x = dev(rng.standard_normal((m, k)), torch.bfloat16)
+    shift = dev(rng.standard_normal((3, k)), torch.bfloat16)
+    want = cr.convrot_norm_residual(x, shift=shift[0], eps=EPS)[1]
+    for rows in (m, m + 1, 2 ** 32 + 1, 2 ** 63 - 1):
+        h = torch.zeros_like(x)
+        a = mx4._NormArgs(x=x.data_ptr(), h=h.data_ptr(), m=m, k=k, rows_per_mod=rows, norm=1,
+                          eps=EPS, shift=shift.data_ptr(), shift_stride=k)
+        stream = torch.cuda.current_stream().cuda_stream
+        assert cr.load_library().convrot_norm_residual(ctypes.byref(a), stream) == 0
+        assert torch.equal(h, want), rows

@@ -267,3 +267,17 @@ def test_gemm_grids_of_many_tiles(lib):
         p = cr.convrot_plan_launch("gemm_mx4", m=2 * m - 64, n=n, k=32, compute_units=cus)
         assert p["grid"] * p["block"] < 1 << 32
         assert p["tile_m"] * p["tile_n"] > 64 * 64
+
+
+def test_norm_modulation_ranges_do_not_overflow(lib):
+    """rows_per_mod beyond m means one row for all, whose range is one row long; a
+    range that 64 bits do not hold is refused."""
+    def st(**kw):
+        return norm_status(lib, **kw)
+    for rows in (8, 9, 1 << 40, (1 << 63) - 1):
+        # D: the 8 rows of h; the modulation lies in its first row, or its last
+        assert st(gate=D + 16, gate_stride=512, rows_per_mod=rows) == 1, rows
+        assert st(scale=D + 4080, scale_stride=512, rows_per_mod=rows) == 1, rows
+    big = {"m": (1 << 25) - 8, "x": 1 << 52, "o": 1 << 53, "x_out": 1 << 54, "h": 1 << 50}
+    assert st(shift=(1 << 50) + 16, shift_stride=1 << 40, rows_per_mod=1, **big) == 1
+    assert st(shift=E, shift_stride=1 << 60, rows_per_mod=1) == 1
