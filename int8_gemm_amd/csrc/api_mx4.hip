@@ -17,6 +17,11 @@ size_t scales_bytes(int64_t rows, int64_t k) {
   return (size_t)((k + kMx4Tile - 1) / kMx4Tile * mx4_pad_rows(rows) * 8);
 }
 
+// dimensions that some call takes
+bool valid_size(int64_t rows, int64_t k) {
+  return rows > 0 && rows < kMaxDim && k > 0 && k % kMx4Block == 0 && k <= kMaxMx4K;
+}
+
 bool valid_mx4_group(int g) { return g == 1 || valid_group(g); }
 
 // rows x k quantized in groups of g (1: not rotated)
@@ -62,7 +67,7 @@ convrot_status check_mx4_gemm(const char* fn, int64_t m, int64_t n, int64_t k) {
 extern "C" {
 
 size_t convrot_mx4_scales_size(int64_t rows, int64_t k) {
-  if (rows <= 0 || k <= 0 || rows >= kMaxDim || k > kMaxMx4K) return 0;
+  if (!valid_size(rows, k)) return 0;
   return scales_bytes(rows, k);
 }
 
@@ -142,12 +147,12 @@ convrot_status convrot_gemm_mx4(const uint8_t* x_codes, const uint8_t* x_scales,
 }
 
 size_t convrot_linear_mx4_workspace_for_rows(int64_t rows, int64_t k) {
-  if (rows <= 0 || k <= 0 || rows >= kMaxDim || k > kMaxMx4K) return 0;
+  if (!valid_size(rows, k)) return 0;
   return align_up(codes_bytes(rows, k), 256) + scales_bytes(rows, k);
 }
 
 size_t convrot_linear_mx4_workspace_size(int64_t m, int64_t n, int64_t k) {
-  if (m < 0 || n <= 0 || k <= 0) return 0;
+  if (m < 0 || m >= kMaxDim || n % 16 || !valid_size(n, k)) return 0;
   // at least what 64 MiB hold: a narrow layer's short slices are bound by their
   // launches (5518 x 144 x 6080 in 13 slices of 432 rows 298 us, in one 30;
   // 21017 x 304 x 768 in 3 slices of 8192 rows 41 us, in one 23)

@@ -281,3 +281,16 @@ def test_norm_modulation_ranges_do_not_overflow(lib):
     big = {"m": (1 << 25) - 8, "x": 1 << 52, "o": 1 << 53, "x_out": 1 << 54, "h": 1 << 50}
     assert st(shift=(1 << 50) + 16, shift_stride=1 << 40, rows_per_mod=1, **big) == 1
     assert st(shift=E, shift_stride=1 << 60, rows_per_mod=1) == 1
+
+
+def test_sizes_of_invalid_dimensions_are_zero(lib):
+    rows, size = cr.convrot_linear_mx4_workspace_for_rows, cr.convrot_linear_mx4_workspace_size
+    far = 1 << 31
+    for k in (0, -32, 16, 100, 131104):
+        assert rows(8, k) == 0 and size(8, 16, k) == 0 and cr.convrot_mx4_scales_size(8, k) == 0, k
+    for m in (-1, far, 1 << 62):
+        assert rows(m, 256) == 0 and size(m, 16, 256) == 0
+        assert cr.convrot_mx4_scales_size(m, 256) == 0
+    for n in (0, -16, 24, far, (1 << 62) + 16, (1 << 63) - 16):
+        assert size(8, n, 256) == 0, n
+    assert size(8, 16, 131072) == rows(8, 131072) > 0
