@@ -467,3 +467,66 @@ def test_gemm_128_tiles_one_and_two_to_a_cu(m, n, k):
             check_gemm(m, n, k, torch.float16, True, 128, lo=121, hi=128)
     finally:
         cr.convrot_set_compute_units(0)
+
+
+# ---- offsets that pass 32 bits ------------------------------------------------
+# A tensor of 63 rows over and over: 63 and the powers of two that an offset could
+# wrap by have no common factor, so a wrapped row is another row.
+
+LONG = 131072                # the longest row
+FOLD = 63
+
+
+def folded(rows, times):
+    """A [63, ...] tensor `times` times over."""
+    return rows.repeat(times, *[1] * (rows.dim() - 1))
+
+
+def folded_scales(scales, times):
+    """Scales of 63 rows, likewise, in their own layout."""
+    held_rows = scales[:, :FOLD].repeat(1, times, 1)
+    pad = torch.zeros((scales.shape[0], -held_rows.shape[1] % 16, 8), dtype=torch.uint8, device=DEV)
+    return torch.cat([held_rows, pad], 1)
+
+
+def test_quantize_and_dequant_behind_4_gib():
+    """x and out of 8.7e9 elements, codes of 4.3 GB."""
+    rng = np.random.default_rng(51)
+    g, times = 256, 1050
+    base = dev(tokens(rng, FOLD, LONG), torch.bfloat16)
+    want_c, want_s = cr.convrot_quantize_mx4(base, g, SEED)
+    want = cr.convrot_dequant_mx4(want_c, want_s, g, SEED)
+    assert_quantized(want_c[:4], want_s, f64(base[:4]), g)
+    x = folded(base, times)
+    codes, scales = cr.convrot_quantize_mx4(x, g, SEED)
+    del x
+    assert codes.numel() > 1 << 32
+    assert (codes.view(times, FOLD, -1) == want_c).all()
+    assert torch.equal(scales[:, :FOLD * times], folded_scales(want_s, times)[:, :FOLD * times])
+    out = cr.convrot_dequant_mx4(codes, scales, g, SEED)
+    assert (out.view(times, FOLD, -1) == want).all()
+
+
+@pytest.mark.parametrize("side", ["x", "w"])
+def test_gemm_codes_behind_4_gib(side):
+    """Codes of 4.3 GB on either side, in the tiled kernel and the one for few
+    rows; one scale for all, so that y is the exact sum rounded once: multiples of
+    1/4 whose partial sums stay below 2^22."""
+    rng = np.random.default_rng(52)
+    times = 1056
+    bc, bs, bv = held(rng, FOLD, LONG, 127, 128)
+    big_c, big_s = folded(bc, times), folded_scales(bs, times)
+    assert big_c.numel() > 1 << 32
+    for rows in (16,) if side == "x" else (4, 80):
+        oc, os_, ov = held(rng, rows, LONG, 127, 128)
+        for tile in (0, 64, 256, 384) if side == "x" or rows > 64 else (0, 16):
+            if side == "x":
+                y = cr.convrot_gemm_mx4(big_c, big_s, oc, os_, tile=tile)
+                y = y.view(times, FOLD, rows)
+                want = bv @ ov.T
+            else:
+                y = cr.convrot_gemm_mx4(oc, os_, big_c, big_s, tile=tile)
+                y = y.view(rows, times, FOLD).transpose(0, 1)
+                want = ov @ bv.T
+            want = torch.from_numpy(want).to(torch.float32).to(torch.bfloat16).to(DEV)
+            assert (y == want).all(), (rows, tile)

@@ -384,3 +384,20 @@ def test_rows_per_mod_beyond_the_rows():
         stream = torch.cuda.current_stream().cuda_stream
         assert cr.load_library().convrot_norm_residual(ctypes.byref(a), stream) == 0
         assert torch.equal(h, want), rows
+
+
+def test_rows_behind_2_to_the_31_elements():
+    """63 rows over and over (a wrapped offset would meet another row); x' in place."""
+    rng = np.random.default_rng(21)
+    fold, times, k, g = 63, 2100, 16384, 64
+    x, o, kw = build(rng, fold, k, torch.bfloat16, 1, "rms", True, True)
+    want_x, want_c, want_s = cr.convrot_norm_residual_mx4(x, o, g, SEED, **kw)
+    want_h = cr.convrot_norm_residual(x, o, **kw)[1]
+    check(x, o, want_x, want_h, kw)
+    big, o = x.repeat(times, 1), o.repeat(times, 1)
+    assert big.numel() > 1 << 31
+    h = torch.empty_like(big)
+    out, codes, scales = cr.convrot_norm_residual_mx4(big, o, g, SEED, x_out=big, h=h, **kw)
+    for got, want in ((out, want_x), (h, want_h), (codes, want_c)):
+        assert (got.view(times, fold, -1) == want).all()
+    assert torch.equal(scales[:, :fold * times], want_s[:, :fold].repeat(1, times, 1))
