@@ -414,8 +414,9 @@ size_t convrot_linear_int8_workspace_size(int64_t m, int64_t n, int64_t k);
  *           32 (8t + j) .. + 31 of row r; 255 makes the block NaN. Bytes of
  *           padding rows are not written and bytes behind the last block of a
  *           row are written 0; neither is ever used. A row-major [rows, k/32]
- *           scale tensor (k % 256 == 0) is brought into this order by
- *           reshaping to [rows, k/256, 8] and swapping the first two axes.
+ *           scale tensor is brought into this order by padding it, with any
+ *           bytes, to multiples of 16 rows and 8 columns, reshaping to
+ *           [padded rows, ceil(k/256), 8] and swapping the first two axes.
  *
  * Numerics:
  *   quantize: x_r = each rotated element's sum in float64 rounded once to fp32
@@ -491,9 +492,9 @@ size_t convrot_linear_mx4_workspace_size(int64_t m, int64_t n, int64_t k);
  *   CONVROT_NORM_LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) [* weight]
  * (post_norm may be CONVROT_NORM_NONE). norm() reads x' as it was rounded; all
  * else is fp32, and a norm takes finite rows of any magnitude (a power of two is
- * taken out of a row whose squares fp32 does not hold). h goes out in 16 bits (h), rotated and quantized for
- * convrot_gemm_mx4 (h_codes, h_scales, g, rot_seed: bit for bit what
- * convrot_quantize_mx4 gives for the 16-bit h), or both.
+ * taken out of a row whose squares fp32 does not hold). h goes out in 16 bits (h),
+ * rotated and quantized for convrot_gemm_mx4 (h_codes, h_scales, g, rot_seed: bit
+ * for bit what convrot_quantize_mx4 gives for the 16-bit h), or both.
  *   x, o, x_out, h [m, k]; post_weight, weight [k]; all in dtype. Null: absent.
  *   x_out may be x itself (in place); otherwise no output may overlap an input.
  *   gate, scale, shift: one [k] row per sample; row r of x takes modulation

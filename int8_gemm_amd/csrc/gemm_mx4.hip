@@ -15,23 +15,28 @@
 // it), so a lane's four scales of a row are one 32-bit LDS read and the
 // instruction selects the slice's byte.
 //
-// Measured: 32760 x 13824 x 5120 1.18-1.24 ms, 3.7-3.9 PFLOP/s, under the
-// power limit: the clock falls to 1.64 GHz and the MFMA pipes are busy 0.54 of
-// it (with nearly no copies the same loop takes 0.95 ms, without its LDS reads
-// as well 0.90; reads from LDS alone cost 2-4%). So are grids of some 240 large
-// tiles: a K-step of a 384 x 192 tile takes 0.97 us without its copies and 1.16
-// with them when 20 CUs work, 1.69 and 1.99 when 240 do (4608 x 3840 x 3840 39-45
-// us). Smaller grids are bound by their operands' way into the XCDs' L2: copies
-// without any arithmetic take 0.46 us a K-step for 216 tiles of 128, with three
-// stages or four, the product 0.48 (lines that L2 holds already come at 52-62 bytes
-// per cycle and CU, these at 30). Up to 192 rows a tile, waves of their own do the
-// copies: issued between the MFMAs of the waves that compute, they cost 512 x 5120 x
-// 5120 17.8 instead of 13.3 us. The two large tiles' accumulators leave no registers
-// for that. Tried without gain: reading the fragments of a whole K-step ahead,
-// a fourth stage for the 128 tile, eight computing or eight copying waves, K-steps
-// of half the length with twice the stages (copies alone 17.3 -> 21.8 us at 4608 x
-// 3840 x 3840), a wave that touches the lines four stages ahead (512 x 5120 x 5120
-// 13.0 -> 16.4), starting the first blocks at different times.
+// Measured: 32760 x 13824 x 5120 1.17-1.18 ms in a steady row, 1.24 (1.18-1.30) as
+// the median of the first twelve launches, 3.7-4.0 PFLOP/s, under the power limit:
+// the clock falls to 1.63 GHz and the MFMA pipes are busy 0.55 of it (with nearly
+// no copies the same loop takes 0.95 ms, without its LDS reads as well 0.90; reads
+// from LDS alone cost 2-4%). So are grids of some 240 large tiles (at least 1.63
+// GHz, MFMA busy 0.52): a K-step of a 384 x 192 tile takes 0.97 us without its
+// copies and 1.16 with them when 20 CUs work, 1.69 and 1.99 when 240 do (4608 x 3840
+// x 3840 38-40 us). Smaller grids are bound by their operands' way into the XCDs'
+// L2 and by the launch's start and end: 333 x 9216 x K takes 6 us and 0.45 a K-step
+// (K = 2048 9.6, 3840 12.4, 5120 14.9 us). Copies without any arithmetic take 0.46 us
+// a K-step there, with three stages or four (lines that L2 holds already come at
+// 52-62 bytes per cycle and CU, these at 30). Where K / 2 is no multiple of 128 each
+// 128-byte piece of a row lies on two lines, which costs that grid 2.4 us more (K
+// = 3872 15.2 us against 12.8 at 4096, 4896 17.4 against 14.9 at 5120). Up to 192 rows
+// a tile, waves of their own do the copies: issued between the MFMAs of the waves
+// that compute, they cost 512 x 5120 x 5120 17.8 instead of 13.3 us. The two large
+// tiles' accumulators leave no registers for that. Tried without gain: reading the
+// fragments of a whole K-step ahead, a fourth stage for the 128 tile, eight
+// computing or eight copying waves, K-steps of half the length with twice the
+// stages (copies alone 17.3 -> 21.8 us at 4608 x 3840 x 3840), a wave that touches the
+// lines four stages ahead (512 x 5120 x 5120 13.0 -> 16.4), starting the first blocks
+// at different times.
 //
 // The end of K: what stands in the place of columns behind a row's end are
 // codes of the next row (the copies stop at the tensor's end) with both
@@ -561,10 +566,12 @@ int64_t rows_cost(int64_t m, int64_t n, int64_t cus, int* nf) {
   return best;
 }
 
-// The tiled kernel's tiles by the number that names them, and what a round of
-// them over the CUs (per_cu to a CU) takes in us: `start` (first copies,
-// epilogue) and `step` for each 256 of K; a last round that leaves one to a CU
-// is shorter (start1, step1).
+// The tiled kernel's tiles by the number that names them, and the cost of a round
+// of them over the CUs (per_cu to a CU): `start` (first copies, epilogue) and
+// `step` for each 256 of K; a last round that leaves one to a CU is cheaper (start1,
+// step1). The costs are weights, in us by their scale, fitted so that they rank the
+// tiles of a shape; a launch takes some us more than their sum (333 x 9216 x 4096:
+// 10.0 by the weights, 12.8 measured).
 struct Tile {
   int tile, bm, bn, waves, per_cu;
   double start, step, start1, step1;
@@ -575,7 +582,7 @@ constexpr Tile kTiles[] = {
     {128, 128, 128, 8, 2, 2.3, 0.85, 2.3, 0.48}, {96, 64, 128, 8, 2, 2.0, 0.57, 1.35, 0.38},
     {64, 64, 64, 8, 2, 4.1, 0.40, 1.0, 0.30},   {40, 64, 32, 4, 2, 2.0, 0.34, 1.0, 0.28}};
 
-// The tile of least estimated time, and that time in us. Measured on 620 shapes
+// The tile of least cost, and that cost. Measured on 620 shapes
 // with weights in the last-level cache (m 70 to 20000, n 512 to 14400, k 512 to
 // 14400): 0.3% behind each shape's best tile on average, 11% at most; with weights
 // from memory 0.4% and 34% (140 x 5504 x 12256, just more 64 tiles than CUs). The
@@ -604,7 +611,8 @@ double tile_us(int64_t m, int64_t n, int64_t k, int cus, int* tile) {
 }
 
 // Whether the few-rows kernel takes m rows: 3 us + 22 KB per us through a CU
-// against the tiles' time or, with long weights, 4.2 TB/s of their bytes.
+// against the tiles' cost and 4 us or, with long weights, 4.2 TB/s of their bytes
+// (fitted together: the 4 us stand for what the tiles' weights leave out).
 // Measured, few rows / tiles, weights from memory: 13824 x 5120 with 8, 16, 32, 64
 // rows 9.5, 10.0, 11.9, 22.5 / 9.6, 9.7, 10.2, 11.7 us; 5120 x 13824 11.6, 13.0, 17.5,
 // 24.7 / 15.8, 15.6, 15.6, 16.1; over 302 shapes of up to 256 rows 0.4% behind the best

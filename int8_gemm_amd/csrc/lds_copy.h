@@ -6,7 +6,6 @@
 namespace convrot {
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
-typedef const __attribute__((address_space(1))) void* gbl_ptr_t;
 
 // s_waitcnt on vmcnt only (expcnt, lgkmcnt left unconstrained); gfx9 encoding
 template <int V>

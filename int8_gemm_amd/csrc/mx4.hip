@@ -8,12 +8,14 @@
 //   dequant:  W_hat = (v 2^e) . blockdiag(R)^T = ((v 2^e) . D) . H / sqrt(g), sums
 //     in fp32, rounded once to bf16 / half.
 //
-// Both are bound by memory: 2 + 17/32 bytes per element, 83 us for 32760 x 5120
-// at the 5.12 TB/s of a large device copy. A wave takes 8 rows of one
-// 256-column tile: its loads and stores are 128-byte runs, and the scales of
-// its 8 rows are 64 consecutive bytes. Measured at that size in a steady state:
-// quantize 78 us (g = 1), 88 (64), 105 (256; 85 for a lone launch, whose clock
-// the power limit does not yet hold down), read-back 66-76 us.
+// Both move 2 + 17/32 bytes per element, 83 us for 32760 x 5120 at the 5.12 TB/s
+// of a large device copy. A wave takes 8 rows of one 256-column tile: its loads
+// and stores are 128-byte runs, and the scales of its 8 rows are 64 consecutive
+// bytes. Measured at that size in a steady state: quantize 78 us (g = 1), 88 (64),
+// 105 (256; 85-93 for a lone launch, whose clock the power limit does not yet hold
+// down), read-back 66-76 us. Memory bounds the read-back and g = 1; g = 256 is
+// bound by the issue of vector instructions: 22.7 an element are 6.0e7 a launch
+// and, at 4 cycles each on 1024 SIMDs, 100 of its 105 us at 2.33 GHz.
 // Tried: a grid that fills the card once and walks down the rows, which saves
 // the waves' set-up, was no faster (101-109 us at g = 256, 81-88 at g = 1).
 

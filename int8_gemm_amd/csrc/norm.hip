@@ -12,8 +12,9 @@
 // caller gets. Everything else is fp32.
 //
 // Bound by memory: x and o are read once, x' and h written once (32760 x 5120:
-// 1.34 GB, 234-244 us = 5.5-5.7 TB/s, a large device copy reaches 5.1; with h
-// quantized 258 us, 4.2 TB/s, the rotation's arithmetic on top); the row stays in
+// 1.34 GB, 234-244 us = 5.5-5.7 TB/s, a large device copy reaches 5.1); with h
+// quantized 258-263 us, 4.2 TB/s, vector instructions on top (53.9 an element, 0.7
+// of the issue slots of the 36 us that 4608 x 3840 take). The row stays in
 // registers between the norms (32 elements a lane, in the tile layout of
 // mx4.h). A row takes ceil(K / 2048) waves or, up to 1024 elements, 8, 16 or 32
 // lanes of one (32760 x 256: 14 us, with a wave per row 39); rows of up to one

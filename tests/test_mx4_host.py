@@ -294,3 +294,17 @@ def test_sizes_of_invalid_dimensions_are_zero(lib):
     for n in (0, -16, 24, far, (1 << 62) + 16, (1 << 63) - 16):
         assert size(8, n, 256) == 0, n
     assert size(8, 16, 131072) == rows(8, 131072) > 0
+
+
+@pytest.mark.parametrize("rows,k", [(16, 256), (5, 2880), (33, 288), (48, 512)])
+def test_row_major_scales_are_brought_into_the_held_order(rows, k):
+    """The header's recipe: pad to multiples of 16 rows and 8 columns, with any bytes,
+    reshape, swap the first two axes."""
+    rng = np.random.default_rng(rows)
+    exps = rng.integers(0, 256, (rows, k // 32)).astype(np.uint8)
+    padded = np.pad(exps, ((0, -rows % 16), (0, -(k // 32) % 8)), constant_values=7)
+    held = padded.reshape(padded.shape[0], -1, 8).swapaxes(0, 1)
+    codes, want = ref.pack(np.zeros((rows, k), np.uint8), exps)
+    assert held.shape == want.shape == mx4._scales_shape(rows, k)
+    assert np.array_equal(ref.unpack(codes, held)[1], exps)
+    assert held.size == cr.convrot_mx4_scales_size(rows, k)
