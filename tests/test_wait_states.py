@@ -101,7 +101,8 @@ def test_accesses_wait_for_sgprs_that_vector_instructions_write(kernels):
             seen += bool(read)
             for was, to in before(lines, i, 5) if read else ():
                 if was.startswith("s_"):
-                    read = read - sgprs(to[0])  # a scalar write since
+                    # a scalar write since, which waits for the vector one by itself
+                    read = read - sgprs(to[0])
                 # results: the first operand, or the first two (carries)
                 elif was.startswith("v_") and \
                         sgprs(to[0] + " " + (to[1] if "_co_" in was else "")) & read:
