@@ -529,6 +529,104 @@ typedef struct convrot_norm_args {
 } convrot_norm_args;
 convrot_status convrot_norm_residual(const convrot_norm_args* args, void* stream);
 
+/* ---- Attention -----------------------------------------------------------------
+ *
+ * What stands between a block's projection of q, k and v and its output
+ * projection: rotary tables, norms of q and k with the rotation, and attention.
+ * q, k, v and out are [tokens, heads, d] in dtype with any strides (elements, a
+ * multiple of 8; the d elements of a head are consecutive), so column ranges of
+ * one wider tensor or a cache's rows do. d % 8 == 0, d <= 256. Outputs may share
+ * a wider tensor with inputs (other columns, other heads), not elements.
+ *
+ * convrot_rope_table: angles of positions with several axes (time, height,
+ * width). Axis a owns dims[a] / 2 pairs of the table, in the axes' order, and
+ * turns its pair j by position * theta^(-2 j / n): j counts within the axis and n
+ * is dims[a], or, where the axes share one ladder (shared != 0), j counts over all
+ * pairs and n is the sum of dims. Angles are float64, cos and sin are rounded
+ * once to fp32.
+ *   positions [tokens, axes], integers or fp32, at any strides; dims [axes] (host
+ *     memory), even, their sum at most 256; axes <= 8
+ *   table [tokens, pairs, 2] fp32 (out): cos, sin; pairs = sum of dims / 2
+ *
+ * convrot_qk_norm_rope: for q and for k (k_heads 0: q alone)
+ *   v = norm(x) * weight over each head, weight [d], or (row != 0) over all heads
+ *       of a token at once, weight [heads, d]; CONVROT_NORM_NONE: v = x
+ *   pair i < pairs of a head's first 2 pairs elements, (2 i, 2 i + 1) or, halves
+ *       != 0, (i, i + pairs), turned by its table entry:
+ *       (a, b) -> (a cos - b sin, b cos + a sin); the elements behind stay
+ * in fp32, rounded once; norms take finite rows of any magnitude, as
+ * convrot_norm_residual does. Token t reads table row t % table_rows (a batch of
+ * equal sequences shares a table). pairs % 4 == 0, for halves pairs % 8 == 0; row
+ * norms take rows of up to 2048 * 16 elements. q_out may be q, and k_out k.
+ *
+ * convrot_attention: out = softmax(scale q k^T) v for every sequence and head;
+ * query head h reads key head h / (q_heads / k_heads).
+ *   Sequence b owns queries q_offsets[b] .. q_offsets[b + 1] and keys k_offsets[b]
+ *   .. k_offsets[b + 1] (int32 [batch + 1], device memory; null: equal
+ *   sequences); k_lens[b] (nullable), where smaller, is how many of its keys are
+ *   used: a padded cache has k_offsets null and k_lens. causal: query i of n sees
+ *   key j of l where j <= i + l - n. A query that sees no key gets 0 (lse
+ *   -infinity). Keys that a query does not see have no part in its result,
+ *   whatever they hold; rows of out and lse outside the sequences stay as they
+ *   were. Offsets that decrease or leave the tensors are held inside them: such a
+ *   call reads and writes nothing out of bounds, its results are not specified.
+ *   lse [q_heads, q_tokens] fp32 (nullable): log of the sum of exp of the scores.
+ *   Scores, sums and the output are fp32; softmax weights are rounded to dtype for
+ *   the product with v. Results are the same bits from run to run and on any
+ *   number of compute units.
+ *   workspace (256-byte aligned, convrot_attention_workspace_size bytes, nullable
+ *   where that is 0) holds the parts of calls with few queries, whose keys are
+ *   split over the card; with less, a call splits less, and sums in another order.
+ *   k and v tokens are at most 2^22 elements apart. scale > 0. */
+typedef enum convrot_position_type {
+  CONVROT_POSITION_I32 = 0,
+  CONVROT_POSITION_I64 = 1,
+  CONVROT_POSITION_F32 = 2
+} convrot_position_type;
+convrot_status convrot_rope_table(const void* positions, convrot_position_type type,
+                                  int64_t token_stride, int64_t axis_stride, int64_t tokens,
+                                  int axes, const int32_t* dims, double theta, int shared,
+                                  float* table, void* stream);
+typedef struct convrot_qk_args {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const void* q_weight;
+  const void* k_weight;
+  const float* table;
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride;
+  int64_t q_out_stride, q_out_head_stride, k_out_stride, k_out_head_stride;
+  int64_t tokens, table_rows;
+  int32_t q_heads, k_heads, d, pairs;
+  convrot_norm_kind norm;
+  int32_t row, halves;
+  convrot_dtype dtype;
+  float eps;
+} convrot_qk_args;
+convrot_status convrot_qk_norm_rope(const convrot_qk_args* args, void* stream);
+typedef struct convrot_attention_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  const int32_t* q_offsets;
+  const int32_t* k_offsets;
+  const int32_t* k_lens;
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride;
+  int64_t v_stride, v_head_stride, out_stride, out_head_stride;
+  int64_t q_tokens, k_tokens, batch;
+  int32_t q_heads, k_heads, d, causal;
+  convrot_dtype dtype;
+  float scale;
+} convrot_attention_args;
+/* Workspace bytes of a call of these sizes (its pointers are not read, but whether
+ * q_offsets is null counts); 0 where none is used, and for invalid sizes. */
+size_t convrot_attention_workspace_size(const convrot_attention_args* args);
+convrot_status convrot_attention(const convrot_attention_args* args, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 /* Host-only: the rotation signs d[0..g) for (g, rot_seed) as +1/-1 bytes into
  * host memory `d` (g bytes). Touches no GPU. */
 convrot_status convrot_rotation_signs(uint64_t rot_seed, int g, int8_t* d);

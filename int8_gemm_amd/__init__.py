@@ -34,6 +34,8 @@ __all__ = [
     "convrot_quantize_mx4", "convrot_dequant_mx4", "convrot_gemm_mx4", "convrot_linear_mx4",
     "convrot_linear_mx4_workspace_size", "convrot_linear_mx4_workspace_for_rows",
     "convrot_mx4_scales_size", "convrot_norm_residual", "convrot_norm_residual_mx4",
+    "convrot_rope_table", "convrot_qk_norm_rope", "convrot_attention",
+    "convrot_attention_workspace_size",
 ]
 
 ROT_SEED = 0xC0FFEE
@@ -62,6 +64,8 @@ EXPORTED_SYMBOLS = (
     "convrot_mx4_scales_size", "convrot_quantize_mx4", "convrot_dequant_mx4", "convrot_gemm_mx4",
     "convrot_linear_mx4", "convrot_linear_mx4_workspace_for_rows",
     "convrot_linear_mx4_workspace_size", "convrot_norm_residual",
+    "convrot_rope_table", "convrot_qk_norm_rope", "convrot_attention",
+    "convrot_attention_workspace_size",
 )
 
 # bytes of the per-device scratch array behind convrot_linear_int8_noalloc
@@ -156,6 +160,9 @@ def load_library():
             "convrot_gemm_mx4": [P, P, P, P, P, I64, I64, I64, P, I, I, P],
             "convrot_linear_mx4": [P, P, P, P, I64, I64, I64, I, U64, P, I, P, SZ, P],
             "convrot_norm_residual": [P, P],
+            "convrot_rope_table": [P, I, I64, I64, I64, I, P, ctypes.c_double, I, P, P],
+            "convrot_qk_norm_rope": [P, P],
+            "convrot_attention": [P, P, SZ, P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -171,6 +178,8 @@ def load_library():
         lib.convrot_linear_mx4_workspace_for_rows.restype = SZ
         lib.convrot_linear_mx4_workspace_size.argtypes = [I64, I64, I64]
         lib.convrot_linear_mx4_workspace_size.restype = SZ
+        lib.convrot_attention_workspace_size.argtypes = [P]
+        lib.convrot_attention_workspace_size.restype = SZ
         lib.convrot_status_string.argtypes = [I]
         lib.convrot_status_string.restype = ctypes.c_char_p
         lib.convrot_last_error_string.argtypes = []
@@ -780,3 +789,5 @@ from .mx4 import (convrot_dequant_mx4, convrot_gemm_mx4, convrot_linear_mx4,  # 
                   convrot_linear_mx4_workspace_for_rows, convrot_linear_mx4_workspace_size,
                   convrot_mx4_scales_size, convrot_norm_residual, convrot_norm_residual_mx4,
                   convrot_quantize_mx4)
+from .attention import (convrot_attention, convrot_attention_workspace_size,  # noqa: E402
+                        convrot_qk_norm_rope, convrot_rope_table)

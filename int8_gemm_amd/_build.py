@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libconvrot.so")
 SOURCES = ("api.hip", "rotate.hip", "dequant.hip", "gemm.hip", "check.hip",
-           "api_mx4.hip", "mx4.hip", "gemm_mx4.hip", "norm.hip")
+           "api_mx4.hip", "mx4.hip", "gemm_mx4.hip", "norm.hip",
+           "api_attention.hip", "rope.hip", "attention.hip")
 
 # -ffp-contract=off: the numerics contract spells out every fp32 rounding; a
 # fused multiply-add would skip one. The packed-fp32 feature is turned off for

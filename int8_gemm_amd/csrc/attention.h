@@ -1,0 +1,77 @@
+// Arguments and launchers of the attention half of a block (rope.hip, attention.hip).
+#pragma once
+
+#include "internal.h"
+
+namespace convrot {
+
+// ---- rotary table ----
+constexpr int kMaxRopePairs = 128;
+constexpr int kMaxRopeAxes = 8;
+enum class PosType { kI32 = 0, kI64 = 1, kF32 = 2 };
+struct RopeTableArgs {
+  const void* positions;
+  int64_t token_stride, axis_stride;  // elements
+  int64_t tokens;
+  int pairs;
+  double log2_theta;
+  int axes;
+  int first[kMaxRopeAxes + 1];  // first pair of each axis
+  int shared;
+  float* table;
+};
+hipError_t launch_rope_table(const RopeTableArgs& a, PosType type, hipStream_t st);
+
+// ---- norms of q and k with the rotation ----
+struct HeadsTensor {
+  const uint16_t* in;
+  uint16_t* out;
+  const uint16_t* weight;
+  int64_t in_stride, in_head_stride, out_stride, out_head_stride;
+  int heads;
+};
+struct HeadsArgs {
+  HeadsTensor t[2];  // q, k (heads 0: absent)
+  const float* table;
+  int64_t tokens, table_rows;
+  int d, pairs;
+  NormKind norm;
+  bool row;  // norms over all heads of a token
+  float eps;
+};
+// Whether a token's heads fit the lanes of a block (norms over rows).
+bool heads_row_fits(int64_t heads, int d);
+bool heads_grid_fits(const HeadsArgs& a);  // tokens < 2^31
+hipError_t launch_qk_norm_rope(const HeadsArgs& a, bool halves, DType dt, hipStream_t st);
+
+// ---- attention ----
+struct AttentionArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t* out;
+  float* lse;
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride, out_stride,
+      out_head_stride;
+  const int32_t *q_offsets, *k_offsets, *k_lens;
+  int64_t q_tokens, k_tokens;
+  int batch, q_heads, k_heads, d;
+  bool causal;
+  float scale;
+  // splits > 1: each split's normalised rows and their log2 sums, joined by a second launch
+  int splits;
+  float* part;      // [splits][q_tokens * q_heads][d]
+  float* part_lse;  // [splits][q_tokens * q_heads]
+};
+// How a call is cut: the kernel's rows per block, its slots per key head, key splits.
+struct AttentionPlan {
+  int rows = 0;        // rows (query, head of the group) of a block's tile
+  int64_t slots = 0;   // tiles per key head, at most
+  int splits = 1;
+  int64_t grid = 0;
+};
+// By sizes alone, so that results do not depend on the device.
+AttentionPlan plan_attention(const AttentionArgs& a, int max_splits);
+size_t attention_part_bytes(const AttentionArgs& a, int splits);
+hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& p, DType dt,
+                            hipStream_t st);
+
+}  // namespace convrot

@@ -1,0 +1,544 @@
+// Attention over packed sequences (gfx950): out = softmax(scale q k^T) v for each
+// sequence and head, query heads in groups that share a key head.
+//
+// One pass over the keys with a running maximum m and sum l of each row's
+// softmax: a tile of scores s raises m to m', and l and the accumulated output
+// are scaled by 2^(c (m - m')) before the tile's p = 2^(c (s - m')) are added
+// (c = scale log2 e). A row is a (query, head of the group) pair, so that a
+// group's heads read their keys together.
+//
+// Scores are formed transposed, S^T = K Q^T, 32 keys x 32 rows an MFMA tile: a
+// lane then holds 16 keys of one row, so that maxima and sums are its own but
+// for one exchange with the lane 32 away, and P^T, rounded to 16 bits, is in
+// the layout of the second product's operand as it is: O^T += V^T P^T, whose
+// contraction takes keys in the order in which the first product's result has
+// them. V^T comes from LDS through the transposing reads.
+
+#include "attention.h"
+#include "lds_copy.h"
+
+namespace convrot {
+
+namespace {
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef _Float16 hf8 __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+constexpr int kTileKeys = 64;   // keys of a copied tile
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLowest = -3.402823466e38f;
+
+template <bool F16>
+__device__ __forceinline__ v16f mfma(const u4& a, const u4& b, const v16f& c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(hf8, a),
+                                                  __builtin_bit_cast(hf8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a),
+                                                   __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+}
+
+// A head of DP elements (padded) in LDS: rows of DP / 8 chunks of 16 bytes, a row's
+// chunks permuted so that neither kind of read meets a bank twice: rows of K are
+// read 16 lanes to one chunk of 16 rows, rows of V four lanes to 32 bytes of a row.
+template <int DP>
+__device__ __forceinline__ int k_slot(int row, int chunk) {
+  return DP == 64 ? chunk ^ ((row >> 1) & 7) : chunk ^ (row & 15);
+}
+template <int DP>
+__device__ __forceinline__ int v_slot(int row, int chunk) {
+  return DP == 64 ? chunk ^ (((row >> 1) & 1) << 2) : chunk ^ ((row & 3) << 2);
+}
+
+__device__ __forceinline__ float other_half(float v) {
+  typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+  const uint32_t a = __float_as_uint(v);
+  const u2v r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+  return __uint_as_float((threadIdx.x & 32) ? r.x : r.y);
+}
+
+// Where a block works: a sequence's rows and keys.
+struct Where {
+  int64_t q0, k0;  // first query and key
+  int lq, lk;
+  int tile;        // tile of the sequence's rows
+};
+
+__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) {
+  return v < lo ? lo : v > hi ? hi : v;
+}
+
+// Sequence b of the call. Offsets are held inside the tensors whatever they are.
+__device__ __forceinline__ Where sequence(const AttentionArgs& a, int b) {
+  Where w;
+  int64_t q1, k1;
+  if (a.q_offsets) {
+    w.q0 = clamp64(a.q_offsets[b], 0, a.q_tokens);
+    q1 = clamp64(a.q_offsets[b + 1], w.q0, a.q_tokens);
+  } else {
+    const int64_t n = a.q_tokens / a.batch;
+    w.q0 = b * n;
+    q1 = w.q0 + n;
+  }
+  if (a.k_offsets) {
+    w.k0 = clamp64(a.k_offsets[b], 0, a.k_tokens);
+    k1 = clamp64(a.k_offsets[b + 1], w.k0, a.k_tokens);
+  } else {
+    const int64_t n = a.k_tokens / a.batch;
+    w.k0 = b * n;
+    k1 = w.k0 + n;
+  }
+  w.lq = (int)(q1 - w.q0);
+  w.lk = (int)(k1 - w.k0);
+  if (a.k_lens) w.lk = (int)clamp64(a.k_lens[b], 0, w.lk);
+  return w;
+}
+
+// The sequence and tile of a slot: tiles of `rows` rows counted through the
+// sequences, 64 of them at a time. False behind the last.
+template <int ROWS>
+__device__ bool find(const AttentionArgs& a, int64_t slot, Where* w) {
+  const int group = a.q_heads / a.k_heads;
+  if (!a.q_offsets) {
+    const int tiles = (int)((a.q_tokens / a.batch * group + ROWS - 1) / ROWS);
+    const int b = (int)(slot / max(tiles, 1));
+    if (b >= a.batch || tiles == 0) return false;
+    *w = sequence(a, b);
+    w->tile = (int)(slot - (int64_t)b * tiles);
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;
+  for (int base = 0; base < a.batch; base += 64) {
+    const int b = base + lane;
+    int tiles = 0;
+    if (b < a.batch) {
+      const int64_t lo = clamp64(a.q_offsets[b], 0, a.q_tokens);
+      const int64_t hi = clamp64(a.q_offsets[b + 1], lo, a.q_tokens);
+      tiles = (int)(((hi - lo) * group + ROWS - 1) / ROWS);  // < 2^26
+    }
+    int upto = min(tiles, 1 << 24);
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int below = __shfl_up(upto, s);
+      if (lane >= s) upto += below;
+    }
+    const uint64_t past = __ballot(before + upto > slot);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      const int first = at ? __builtin_amdgcn_readlane(upto, at - 1) : 0;
+      *w = sequence(a, base + at);
+      w->tile = (int)(slot - before) - first;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
+template <int DP, int QT, int NW, bool F16>
+struct Kernel {
+  static constexpr int kRows = 32 * QT * NW;         // rows of a block
+  static constexpr int kRowBytes = DP * 2;
+  static constexpr int kChunks = DP / 8;
+  static constexpr int kTileBytes = kTileKeys * kRowBytes;
+  static constexpr int kStages = 2;
+  static constexpr int kLds = 2 * kStages * kTileBytes + 16;  // and a flag
+  static constexpr int kCopies = kTileBytes / 1024 / NW;  // of a wave, per tile and operand
+  static constexpr int kSteps = DP / 16;
+  static constexpr int kDTiles = DP / 32;
+};
+
+// Values of keys that only some rows of a tile see. A weight of 0 does not cancel an
+// infinity or a NaN in the product, so a tile in which some row's mask ends is looked
+// through, infinities and NaN in it are replaced by 0 (by every wave that finds one,
+// before its own reads; they all write the same), and at the end each row adds
+// those of the keys that it sees.
+template <bool F16>
+constexpr uint32_t kExp16 = F16 ? 0x7C007C00u : 0x7F807F80u;
+template <bool F16>
+constexpr uint32_t kExpUnit16 = F16 ? 0x04000400u : 0x00800080u;  // its last bits
+
+template <bool F16>
+__device__ __forceinline__ bool nonfinite16(uint32_t h) {
+  return (h & kExp16<F16> & 0xFFFFu) == (kExp16<F16> & 0xFFFFu);
+}
+
+// True if the tile holds an infinity or a NaN; none is left then.
+template <bool F16, int DP>
+__device__ __forceinline__ bool clear_nonfinite(uint8_t* vt) {
+  const int lane = threadIdx.x & 63;
+  uint32_t found = 0;
+#pragma unroll 1
+  for (int i = lane; i < kTileKeys * DP / 8; i += 64) {
+    const u4 w = *reinterpret_cast<const u4*>(vt + i * 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      found |= ((w[e] & kExp16<F16>) + kExpUnit16<F16>) & 0x80008000u;
+  }
+  if (__builtin_expect(!__any(found != 0), 1)) return false;
+#pragma unroll 1
+  for (int i = lane; i < kTileKeys * DP / 2; i += 64) {
+    uint32_t* at = reinterpret_cast<uint32_t*>(vt + i * 4);
+    const uint32_t w = *at;
+    const uint32_t keep = (nonfinite16<F16>(w & 0xFFFFu) ? 0u : 0xFFFFu) |
+                          (nonfinite16<F16>(w >> 16) ? 0u : 0xFFFF0000u);
+    if (keep != ~0u) *at = w & keep;
+  }
+  wait_lgkm0();
+  return true;
+}
+
+template <int DP, int QT, int NW, bool F16, bool CAUSAL>
+__global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, int64_t slots,
+                                                               int xcds) {
+  using T = Kernel<DP, QT, NW, F16>;
+  extern __shared__ __align__(1024) uint8_t lds[];
+  volatile int* cleared = reinterpret_cast<int*>(lds + 2 * T::kStages * T::kTileBytes);
+  if (CAUSAL && threadIdx.x == 0) *cleared = 0;  // a barrier follows in every tile
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, col = lane & 31;
+  const int group = a.q_heads / a.k_heads;
+
+  // blocks of an XCD (they are dealt in turn) take neighbouring tiles of the same
+  // heads, whose keys then meet in its L2
+  int64_t id = blockIdx.x;
+  {
+    const int64_t total = gridDim.x, full = total / xcds, rest = total % xcds;
+    const int64_t x = id % xcds, i = id / xcds;
+    id = x * full + (x < rest ? x : rest) + i;
+  }
+  const int split = (int)(id % a.splits);
+  id /= a.splits;
+  int64_t slot = id % slots;
+  const int hk = (int)(id / slots);
+  Where w;
+  if (CAUSAL) slot = slots - 1 - slot;  // long tiles first
+  if (!find<T::kRows>(a, slot, &w)) return;
+
+  const int rows = w.lq * group;  // < 2^31 checked
+  const int row0 = w.tile * T::kRows;
+  // keys that the tile's last and first query see
+  const int shift = w.lk - w.lq + 1;
+  int end = w.lk, full = w.lk;
+  if (CAUSAL) {
+    const int last = min(rows - 1, row0 + T::kRows - 1) / group, first = row0 / group;
+    end = min(w.lk, max(0, last + shift));
+    full = min(w.lk, max(0, first + shift));
+  }
+  int tiles = (end + kTileKeys - 1) / kTileKeys;
+  int t0 = 0;
+  if (a.splits > 1) {
+    const int per = (tiles + a.splits - 1) / a.splits;
+    t0 = min(tiles, split * per);
+    tiles = min(tiles, t0 + per);
+  }
+
+  // this lane's rows
+  int row[QT], seen[QT];
+  u4 qf[QT][T::kSteps];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    row[t] = row0 + (wave * QT + t) * 32 + col;
+    const int r = min(row[t], rows - 1);
+    const int token = r / group, head = hk * group + r % group;
+    seen[t] = CAUSAL ? min(w.lk, token + shift) : w.lk;
+    const uint16_t* q = a.q + (w.q0 + token) * a.q_stride + head * a.q_head_stride;
+#pragma unroll
+    for (int s = 0; s < T::kSteps; ++s) {
+      const int c = 2 * s + half;
+      const u4 zero = {0, 0, 0, 0};
+      qf[t][s] = c * 8 < a.d ? *reinterpret_cast<const u4*>(q + c * 8) : zero;
+    }
+  }
+
+  // copies: lane i of a copy fills the 16 bytes behind 16 i
+  const int8_t* kbase =
+      reinterpret_cast<const int8_t*>(a.k + w.k0 * a.k_stride + hk * a.k_head_stride);
+  const int8_t* vbase =
+      reinterpret_cast<const int8_t*>(a.v + w.k0 * a.v_stride + hk * a.v_head_stride);
+  const uint32_t kstride = (uint32_t)a.k_stride * 2, vstride = (uint32_t)a.v_stride * 2;
+  auto issue = [&](int t, int stage) {
+    const int last = w.lk - 1 - t * kTileKeys;  // rows behind it repeat it
+    const int8_t* kp = kbase + (int64_t)t * kTileKeys * a.k_stride * 2;
+    const int8_t* vp = vbase + (int64_t)t * kTileKeys * a.v_stride * 2;
+#pragma unroll
+    for (int i = 0; i < T::kCopies; ++i) {
+      const int at = (wave * T::kCopies + i) * 64;
+      const int r = (at + lane) / T::kChunks, c = (at + lane) % T::kChunks;
+      const int from = min(r, last);
+      const int kc = min(k_slot<DP>(r, c), a.d / 8 - 1), vc = min(v_slot<DP>(r, c), a.d / 8 - 1);
+      dma16(kp, from * kstride + kc * 16, stage * T::kTileBytes + at * 16);
+      dma16(vp, from * vstride + vc * 16,
+            (T::kStages + stage) * T::kTileBytes + at * 16);
+    }
+  };
+
+  v16f o[T::kDTiles][QT];
+  float m[QT], l[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    m[t] = kLowest;
+    l[t] = 0.f;
+#pragma unroll
+    for (int d = 0; d < T::kDTiles; ++d) o[d][t] = (v16f){0};
+  }
+  const float c = a.scale * kLog2e;
+
+  if (t0 < tiles) issue(t0, 0);
+  for (int t = t0; t < tiles; ++t) {
+    const int stage = (t - t0) & 1;
+    wait_vmcnt<0>();
+    wait_lgkm0();
+    lds_barrier();
+    if (t + 1 < tiles) issue(t + 1, stage ^ 1);
+    const uint8_t* kt = lds + stage * T::kTileBytes;
+    uint8_t* vt = lds + (T::kStages + stage) * T::kTileBytes;
+    v16f s[2][QT];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int q = 0; q < QT; ++q) s[u][q] = (v16f){0};
+#pragma unroll
+      for (int st = 0; st < T::kSteps; ++st) {
+        const int r = u * 32 + col;
+        const u4 kf = *reinterpret_cast<const u4*>(kt + r * T::kRowBytes +
+                                                   k_slot<DP>(r, 2 * st + half) * 16);
+#pragma unroll
+        for (int q = 0; q < QT; ++q) s[u][q] = mfma<F16>(kf, qf[q][st], s[u][q]);
+      }
+    }
+    const int key0 = t * kTileKeys;
+    if (key0 + kTileKeys > full) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < QT; ++q)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int key = key0 + u * 32 + 8 * (i >> 2) + 4 * half + (i & 3);
+            if (key >= seen[q]) s[u][q][i] = -__builtin_inff();
+          }
+    }
+    u4 p[2][QT][2];
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+      float top = s[0][q][0];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][q][i]);
+      top = fmaxf(top, other_half(top));
+      top = fmaxf(top, m[q]);
+      const float alpha = __builtin_amdgcn_exp2f((m[q] - top) * c);
+      m[q] = top;
+      l[q] *= alpha;
+#pragma unroll
+      for (int d = 0; d < T::kDTiles; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][q][i] *= alpha;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[u][q][i] = __builtin_amdgcn_exp2f((s[u][q][i] - top) * c);
+          l[q] += s[u][q][i];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            p[u][q][h][e] = pack16x2<F16>(s[u][q][8 * h + 2 * e], s[u][q][8 * h + 2 * e + 1]);
+      }
+    }
+    // V^T: 32 elements of the head, keys 16 h + 4 half + .. of a unit and those 8 further
+    auto values = [&](int u, int h, int d) {
+      const int r = u * 32 + h * 16 + half * 4 + ((lane & 15) >> 2);
+      const int chunk = d * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+      const int at = v_slot<DP>(r, chunk) * 16 + (lane & 1) * 8;
+      typedef __attribute__((address_space(3))) s4* lp;
+      const u2 w0 = __builtin_bit_cast(
+          u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vt + r * T::kRowBytes + at)));
+      const u2 w1 = __builtin_bit_cast(
+          u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vt + (r + 8) * T::kRowBytes + at)));
+      return (u4){w0.x, w0.y, w1.x, w1.y};
+    };
+    if (CAUSAL && key0 + kTileKeys > full && clear_nonfinite<F16, DP>(vt)) *cleared = 1;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int d = 0; d < T::kDTiles; ++d) {
+          const u4 vf = values(u, h, d);
+#pragma unroll
+          for (int q = 0; q < QT; ++q) o[d][q] = mfma<F16>(vf, p[u][q][h], o[d][q]);
+        }
+  }
+
+  if (CAUSAL) {
+    wait_lgkm0();
+    lds_barrier();
+    if (__builtin_expect(*cleared, 0)) {
+      const int to = min(end, tiles * kTileKeys);
+#pragma unroll 1
+      for (int key = max(full / kTileKeys, t0) * kTileKeys; key < to; ++key) {
+        const uint16_t* vr = a.v + (w.k0 + key) * a.v_stride + hk * a.v_head_stride;
+#pragma unroll
+        for (int d = 0; d < T::kDTiles; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int e = d * 32 + 8 * (i >> 2) + 4 * half + (i & 3);
+            const uint32_t h = e < a.d ? vr[e] : 0;
+            const float f = lo16<F16>(h);
+#pragma unroll
+            for (int q = 0; q < QT; ++q)
+              if (nonfinite16<F16>(h) && key < seen[q]) o[d][q][i] += f;
+          }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int q = 0; q < QT; ++q) {
+    const float sum = l[q] + other_half(l[q]);
+    const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
+    const float lse2 = sum > 0.f || sum != sum ? m[q] * c + log2f(sum) : -__builtin_inff();
+    if (row[q] >= rows) continue;
+    const int token = row[q] / group, head = hk * group + row[q] % group;
+    if (a.splits > 1) {
+      const int64_t at = ((int64_t)split * a.q_tokens + w.q0 + token) * a.q_heads + head;
+      if (half == 0) a.part_lse[at] = lse2;
+      if (lse2 == -__builtin_inff()) continue;
+      float* to = a.part + at * a.d;
+#pragma unroll
+      for (int d = 0; d < T::kDTiles; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = d * 32 + i * 8 + half * 4;
+          typedef float v4f __attribute__((ext_vector_type(4)));
+          const v4f f = {o[d][q][4 * i] * inv, o[d][q][4 * i + 1] * inv, o[d][q][4 * i + 2] * inv,
+                         o[d][q][4 * i + 3] * inv};
+          if (e < a.d) *reinterpret_cast<v4f*>(to + e) = f;
+        }
+      continue;
+    }
+    if (a.lse && half == 0) a.lse[(int64_t)head * a.q_tokens + w.q0 + token] = lse2 * kLn2;
+    uint16_t* to = a.out + (w.q0 + token) * a.out_stride + head * a.out_head_stride;
+#pragma unroll
+    for (int d = 0; d < T::kDTiles; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = d * 32 + i * 8 + half * 4;
+        const u2 f = {pack16x2<F16>(o[d][q][4 * i] * inv, o[d][q][4 * i + 1] * inv),
+                      pack16x2<F16>(o[d][q][4 * i + 2] * inv, o[d][q][4 * i + 3] * inv)};
+        if (e < a.d) *reinterpret_cast<u2*>(to + e) = f;
+      }
+  }
+}
+
+// Joins the splits of a row: out = sum_s 2^(lse_s - lse) out_s. A wave takes a
+// row, lanes 4 elements each.
+template <bool F16>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t all = a.q_tokens * a.q_heads;
+  if (r >= all) return;
+  const int64_t token = r / a.q_heads;
+  const int head = (int)(r % a.q_heads);
+  if (a.q_offsets && (token < a.q_offsets[0] || token >= a.q_offsets[a.batch])) return;
+  float top = kLowest;
+  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * all + r]);
+  float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < a.splits; ++s) {
+    const float x = a.part_lse[s * all + r];
+    if (x == -__builtin_inff()) continue;
+    const float f = __builtin_amdgcn_exp2f(x - top);
+    sum += f;
+    if (lane * 4 < a.d) {
+      typedef float v4f __attribute__((ext_vector_type(4)));
+      const v4f v = *reinterpret_cast<const v4f*>(a.part + (s * all + r) * a.d + lane * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
+    }
+  }
+  const bool none = sum == 0.f;
+  const float inv = none ? 0.f : 1.0f / sum;
+  if (a.lse && lane == 0)
+    a.lse[head * a.q_tokens + token] = none ? -__builtin_inff() : (top + log2f(sum)) * kLn2;
+  if (lane * 4 < a.d) {
+    const u2 f = {pack16x2<F16>(acc[0] * inv, acc[1] * inv),
+                  pack16x2<F16>(acc[2] * inv, acc[3] * inv)};
+    *reinterpret_cast<u2*>(a.out + token * a.out_stride + head * a.out_head_stride + lane * 4) = f;
+  }
+}
+
+template <int DP, int QT, int NW, bool F16>
+hipError_t launch_tile(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
+  using T = Kernel<DP, QT, NW, F16>;
+  auto kern = a.causal ? attention_kernel<DP, QT, NW, F16, true>
+                       : attention_kernel<DP, QT, NW, F16, false>;
+  if (T::kLds > 65536) {
+    // per device: the attribute is set on every call (a host-side table write)
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+    if (e != hipSuccess) return e;
+  }
+  kern<<<dim3((uint32_t)p.grid), dim3(64 * NW), T::kLds, st>>>(a, p.slots,
+                                                               xcd_count(compute_units()));
+  return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t launch_dtype(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
+  hipError_t e;
+  if (a.d <= 64)
+    e = launch_tile<64, 1, 4, F16>(a, p, st);
+  else if (a.d <= 128)
+    e = launch_tile<128, 1, 4, F16>(a, p, st);
+  else
+    e = launch_tile<256, 1, 4, F16>(a, p, st);
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t rows = a.q_tokens * a.q_heads;
+  attention_join_kernel<F16><<<dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+AttentionPlan plan_attention(const AttentionArgs& a, int max_splits) {
+  AttentionPlan p;
+  const int64_t group = a.q_heads / a.k_heads;
+  p.rows = 128;
+  if (a.q_offsets)
+    p.slots = (a.q_tokens * group + p.rows - 1) / p.rows + a.batch;
+  else
+    p.slots = a.batch * ((a.q_tokens / a.batch * group + p.rows - 1) / p.rows);
+  const int64_t blocks = p.slots * a.k_heads;
+  // fewer tiles than the card has compute units: split the keys
+  const int64_t tiles = (a.k_tokens / a.batch + kTileKeys - 1) / kTileKeys;
+  int64_t splits = blocks ? 512 / blocks : 1;
+  if (splits > tiles / 4) splits = tiles / 4;
+  if (splits > max_splits) splits = max_splits;
+  p.splits = splits < 1 ? 1 : (int)splits;
+  p.grid = blocks * p.splits;
+  return p;
+}
+
+size_t attention_part_bytes(const AttentionArgs& a, int splits) {
+  if (splits <= 1) return 0;
+  return (size_t)splits * (size_t)(a.q_tokens * a.q_heads) * (size_t)(a.d + 1) * 4;
+}
+
+hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& p, DType dt,
+                            hipStream_t st) {
+  if (p.grid == 0) return hipSuccess;
+  return dt == DType::kF16 ? launch_dtype<true>(a, p, st) : launch_dtype<false>(a, p, st);
+}
+
+}  // namespace convrot

@@ -23,6 +23,7 @@
 
 #include "internal.h"
 #include "mx4.h"
+#include "wave_sum.h"
 
 namespace convrot {
 
@@ -37,27 +38,6 @@ constexpr int kMaxWaves = 8;                    // K <= 16384
 struct RowShape {
   int waves, shift;
 };
-
-// Sum over 2^shift lanes, the same bits in each: DPP exchanges within 16 lanes,
-// then swaps of 16-lane rows and of the wave's halves.
-__device__ __forceinline__ float lanes_sum(float v, int shift) {
-  typedef uint32_t u2v __attribute__((ext_vector_type(2)));
-  v += mx4_dpp<kDppXor1>(v);
-  v += mx4_dpp<kDppXor2>(v);
-  v += mx4_dpp<kDppMirror8>(v);
-  if (shift > 3) v += mx4_dpp<kDppMirror16>(v);
-  if (shift > 4) {
-    const uint32_t a = __float_as_uint(v);
-    const u2v r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-    v = __uint_as_float(r.x) + __uint_as_float(r.y);
-  }
-  if (shift > 5) {
-    const uint32_t a = __float_as_uint(v);
-    const u2v r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
-    v = __uint_as_float(r.x) + __uint_as_float(r.y);
-  }
-  return v;
-}
 
 // Sum over the row; `part` holds one slot per wave. Two calls in a row use
 // different slots, so one barrier each is enough.

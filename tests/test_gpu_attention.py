@@ -1,0 +1,407 @@
+"""GPU: attention over packed sequences against a float64 oracle.
+
+Bounds (u = 2^-24, A = the mean of |v| under a row's softmax weights, S = sum |q k| of a
+score, N keys): a score is off by (d + 8) 2 u S scale; the exponent's argument and its
+multiply-adds by 4 u of the largest |scaled score|, the power of two by 4 u, the running
+maximum's factors by 4 u a tile. Relative errors e of the weights move the output by at
+most 2 e A. The weights' rounding to 16 bits adds h A (h = 2^-8 bf16, 2^-11 half; half
+weights below 2^-14 of the largest are off by 2^-25 of it, N times that against a sum of
+at least 1), the sums of N terms 2 N u A. Then one rounding of the output."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import int8_gemm_amd as cr
+from oracle import attention_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+U = 2.0 ** -24
+H16 = {torch.bfloat16: (2.0 ** -8, 2.0 ** -134), torch.float16: (2.0 ** -11, 2.0 ** -25)}
+DTYPES = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    cr.load_library()
+
+
+def dev(a, dtype):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(dtype).to(DEV)
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+def offsets(lens):
+    return torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32, device=DEV)
+
+
+def close(q, k, v, out, lse, scale, causal):
+    """One sequence's results against the oracle's."""
+    dtype = out.dtype
+    half, tiny = H16[dtype]
+    q, k, v = f64(q), f64(k), f64(v)
+    n, hq, d = q.shape
+    length, hk, _ = k.shape
+    want, want_lse, spread = ref.attention(q, k, v, scale, causal)
+    kk = np.repeat(k, hq // hk, 1)
+    # the largest sum of |q k| and the largest score of a row
+    size = np.abs(q).max(-1) * np.abs(kk).sum(-1).max(0, initial=0.0)[None]
+    if length:
+        size = np.minimum(size, np.sqrt((q ** 2).sum(-1) * (kk ** 2).sum(-1).max(0)[None]))
+    e = (d + 8) * 2 * U * size * scale + 4 * U * size * scale + 4 * U + 4 * U * (length / 32 + 2)
+    top = np.abs(v).max() if v.size else 0.0
+    tol = (2 * e[..., None] + half + 4 * length * U) * spread
+    if dtype == torch.float16:
+        tol = tol + length * 2.0 ** -25 * top
+    tol = tol * 1.01 + (half + 2 * U) * np.abs(want) + tiny
+    bad = ~(np.abs(f64(out) - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[0].tolist())
+    if lse is not None:
+        got = f64(lse)
+        none = want_lse == -np.inf
+        assert (got[none] == -np.inf).all()
+        got, want_lse = np.where(none, 0, got), np.where(none, 0, want_lse)
+        err = (e.T + (length + 8) * U + 4 * U * np.abs(want_lse))
+        assert (np.abs(got - want_lse) <= err).all()
+
+
+def make(rng, q_lens, k_lens, hq, hk, d, dtype, heat=1.0):
+    q = dev(rng.standard_normal((sum(q_lens), hq, d)) * heat, dtype)
+    k = dev(rng.standard_normal((sum(k_lens), hk, d)), dtype)
+    v = dev(rng.standard_normal((sum(k_lens), hk, d)), dtype)
+    return q, k, v
+
+
+def run_packed(q, k, v, q_lens, k_lens, causal, **kw):
+    out, lse = cr.convrot_attention(q, k, v, q_offsets=offsets(q_lens),
+                                    k_offsets=offsets(k_lens), causal=causal, return_lse=True, **kw)
+    return out, lse
+
+
+def check_packed(q, k, v, out, lse, q_lens, k_lens, causal, scale=None):
+    scale = scale or 1 / math.sqrt(q.shape[-1])
+    qo, ko = np.cumsum([0, *q_lens]), np.cumsum([0, *k_lens])
+    for b in range(len(q_lens)):
+        qs, ks = slice(qo[b], qo[b + 1]), slice(ko[b], ko[b + 1])
+        close(q[qs], k[ks], v[ks], out[qs], lse[:, qs], scale, causal)
+
+
+LENS = [
+    ([1], [1]), ([1], [63]), ([1], [64]), ([5], [65]), ([33], [33]), ([129], [200]),
+    ([200], [129]), ([1, 0, 7, 130, 64], [1, 5, 0, 130, 31]), ([257, 3], [300, 1000]),
+    ([0, 0], [4, 0]), ([1, 1, 1], [700, 1, 4097]), ([513], [513])]
+
+
+@DTYPES
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("q_lens,k_lens", LENS)
+@pytest.mark.parametrize("hq,hk,d", [(2, 2, 128), (6, 2, 64), (8, 1, 128)])
+def test_lengths(q_lens, k_lens, hq, hk, d, causal, dtype):
+    rng = np.random.default_rng(sum(q_lens) + 7 * sum(k_lens))
+    q, k, v = make(rng, q_lens, k_lens, hq, hk, d, dtype, 3.0)
+    out, lse = run_packed(q, k, v, q_lens, k_lens, causal)
+    check_packed(q, k, v, out, lse, q_lens, k_lens, causal)
+
+
+@DTYPES
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("hq,hk,d", [(1, 1, 8), (3, 3, 16), (4, 2, 40), (5, 1, 64), (2, 1, 72),
+                                     (4, 4, 80), (3, 1, 96), (2, 2, 112), (7, 1, 128),
+                                     (2, 1, 136), (3, 3, 192), (4, 2, 256)])
+def test_heads(hq, hk, d, causal, dtype):
+    rng = np.random.default_rng(d)
+    q_lens, k_lens = [37, 150, 1], [37, 211, 90]
+    q, k, v = make(rng, q_lens, k_lens, hq, hk, d, dtype, 2.0)
+    out, lse = run_packed(q, k, v, q_lens, k_lens, causal)
+    check_packed(q, k, v, out, lse, q_lens, k_lens, causal)
+
+
+@DTYPES
+@pytest.mark.parametrize("hq,hk,d,n,length", [(3, 3, 128, 1100, 1300), (2, 1, 64, 2100, 900),
+                                              (2, 2, 256, 300, 700), (24, 8, 128, 9, 20000),
+                                              (4, 4, 96, 77, 5000)])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+def test_larger(hq, hk, d, n, length, causal, dtype):
+    rng = np.random.default_rng(n)
+    q, k, v = make(rng, [n], [length], hq, hk, d, dtype, 4.0)
+    out, lse = cr.convrot_attention(q, k, v, causal=causal, return_lse=True)
+    close(q, k, v, out, lse, 1 / math.sqrt(d), causal)
+
+
+@DTYPES
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("hq,hk,d,lens", [(4, 4, 128, [700, 65]), (8, 2, 64, [1, 300, 33]),
+                                          (2, 1, 256, [200, 5]), (4, 1, 72, [130, 64])])
+def test_each_query_finds_its_key(hq, hk, d, lens, causal, dtype):
+    """Scores that leave one key: the output is that key's value, to the bit."""
+    rng = np.random.default_rng(d)
+    q, k, v = make(rng, lens, lens, hq, hk, d, dtype)
+    k = torch.sign(k) * 2                        # any two differ in many signs
+    at = np.concatenate([rng.integers(0, np.arange(1, n + 1) if causal else n, n)
+                         + sum(lens[:i]) for i, n in enumerate(lens)])
+    at = torch.from_numpy(at).to(DEV)
+    q = (torch.sign(k)[at] * 4).repeat_interleave(hq // hk, 1)
+    out, _ = run_packed(q, k, v, lens, lens, causal, scale=8.0)
+    # equal keys share the weight: drop queries whose key comes again
+    for h in range(hq):
+        kh = k[:, h // (hq // hk)].float()
+        sc = q[:, h].float() @ kh.t()
+        seq = torch.repeat_interleave(torch.arange(len(lens)), torch.tensor(lens)).to(DEV)
+        sc[seq[:, None] != seq[None]] = -math.inf
+        best = sc.topk(min(2, sc.shape[1]), 1).values
+        alone = best[:, 0] - best[:, -1] >= 16       # 16 * 8 in the exponent: e^-128
+        assert alone.float().mean() > 0.5
+        assert torch.equal(out[alone, h], v[at[alone], h // (hq // hk)])
+
+
+@DTYPES
+def test_a_padded_cache_and_what_it_holds_behind_its_use(dtype):
+    rng = np.random.default_rng(3)
+    batch, room, hq, hk, d = 5, 300, 8, 2, 128
+    lens = [300, 1, 0, 131, 64]
+    q = dev(rng.standard_normal((batch, 2, hq, d)) * 2, dtype)
+    k = dev(rng.standard_normal((batch, room, hk, d)), dtype)
+    v = dev(rng.standard_normal((batch, room, hk, d)), dtype)
+    k[2, :] = math.nan
+    for b, n in enumerate(lens):
+        k[b, n:] = math.nan
+        v[b, n:] = math.inf
+    used = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for causal in (False, True):
+        out, lse = cr.convrot_attention(q, k, v, k_lens=used, causal=causal, return_lse=True)
+        assert out.shape == q.shape
+        for b, n in enumerate(lens):
+            close(q[b], k[b, :n], v[b, :n], out[b], lse[:, 2 * b:2 * b + 2], 1 / math.sqrt(d),
+                  causal)
+    # more than there is room for, and less than nothing
+    wild = torch.tensor([1 << 30, -5, 0, 131, 64], dtype=torch.int32, device=DEV)
+    k, v = torch.nan_to_num(k, 0.0), torch.nan_to_num(v, 0.0, 0.0, 0.0)
+    out = cr.convrot_attention(q, k, v, k_lens=wild)
+    close(q[0], k[0], v[0], out[0], None, 1 / math.sqrt(d), False)
+    assert (out[1] == 0).all() and (out[2] == 0).all()
+
+
+@DTYPES
+@pytest.mark.parametrize("hq,hk,d,n,length", [(2, 2, 128, 200, 200), (4, 1, 64, 90, 300),
+                                              (2, 1, 256, 70, 70), (8, 1, 128, 2, 3000),
+                                              (3, 3, 40, 300, 100)])
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+def test_keys_that_the_mask_hides_have_no_part(hq, hk, d, n, length, what, dtype):
+    """Non-finite keys and values: queries that do not see them are what they are
+    without them, the others get what they get from them."""
+    rng = np.random.default_rng(n)
+    q, k, v = make(rng, [n], [length], hq, hk, d, dtype)
+    clean = cr.convrot_attention(q, k, v, causal=True)
+    at = length - 1 - min(length, n) // 2      # seen by the later queries only
+    col = d - 3
+    v[at, :, col] = what
+    got = cr.convrot_attention(q, k, v, causal=True)
+    sees = torch.arange(n, device=DEV) + length - n >= at
+    assert torch.equal(got[~sees], clean[~sees])
+    hit = got[sees][:, :, col]
+    assert (torch.isnan(hit) if math.isnan(what) else hit == what).all()
+    rest = [c for c in range(d) if c != col]
+    assert torch.equal(got[sees][:, :, rest], clean[sees][:, :, rest])
+    # two of opposite sign meet
+    if math.isinf(what) and at + 1 < length:
+        v[at + 1, :, col] = -what
+        got = cr.convrot_attention(q, k, v, causal=True)
+        both = torch.arange(n, device=DEV) + length - n >= at + 1
+        assert torch.isnan(got[both][:, :, col]).all()
+        assert (got[sees & ~both][:, :, col] == what).all()
+    # a key: its scores are hidden as well
+    v[:, :, col] = 0
+    clean = cr.convrot_attention(q, k, v, causal=True)
+    k[at] = what
+    got = cr.convrot_attention(q, k, v, causal=True)
+    assert torch.equal(got[~sees], clean[~sees])
+
+
+def test_rows_outside_the_sequences_stay():
+    rng = np.random.default_rng(4)
+    hq, hk, d = 4, 2, 64
+    for splits_len in (40, 5000):            # the second is split over the keys
+        q, k, v = make(rng, [50], [splits_len], hq, hk, d, torch.bfloat16)
+        out = torch.full_like(q, 7.0)
+        lse = torch.full((hq, 50), 7.0, device=DEV)
+        qo = torch.tensor([3, 13, 40], dtype=torch.int32, device=DEV)
+        ko = torch.tensor([0, 9, splits_len], dtype=torch.int32, device=DEV)
+        cr.convrot_attention(q, k, v, q_offsets=qo, k_offsets=ko, out=out, lse=lse)
+        inside = torch.zeros(50, dtype=torch.bool, device=DEV)
+        inside[3:40] = True
+        assert (out[~inside] == 7).all() and (lse[:, ~inside] == 7).all()
+        close(q[3:13], k[:9], v[:9], out[3:13], lse[:, 3:13], 1 / 8, False)
+        close(q[13:40], k[9:], v[9:], out[13:40], lse[:, 13:40], 1 / 8, False)
+
+
+def test_offsets_that_leave_the_tensors_stay_inside():
+    """Nothing is read or written out of bounds; sequences that are as they should be
+    come out right."""
+    rng = np.random.default_rng(5)
+    q, k, v = make(rng, [100], [200], 4, 2, 64, torch.bfloat16)
+    guard = torch.full((300, 4, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    for qo, ko in (([0, 20, 1 << 30], [0, 50, 1 << 30]), ([0, 20, 10], [0, 50, 40]),
+                   ([0, 20, 100], [0, 50, -7]), ([0, 20, -(1 << 31)], [0, 50, 200])):
+        out = guard[100:200]
+        cr.convrot_attention(q, k, v, q_offsets=torch.tensor(qo, dtype=torch.int32, device=DEV),
+                             k_offsets=torch.tensor(ko, dtype=torch.int32, device=DEV), out=out)
+        torch.cuda.synchronize()
+        close(q[:10], k[:50], v[:50], out[:10], None, 1 / 8, False)
+        assert (guard[:100] == 7).all() and (guard[200:] == 7).all()
+
+
+@DTYPES
+def test_many_sequences(dtype):
+    """More than a wave's worth of sequences, some empty."""
+    rng = np.random.default_rng(6)
+    lens = rng.integers(0, 40, 200).tolist()
+    lens[3] = 300
+    q, k, v = make(rng, lens, lens, 2, 1, 64, dtype, 2.0)
+    for causal in (False, True):
+        out, lse = run_packed(q, k, v, lens, lens, causal)
+        check_packed(q, k, v, out, lse, lens, lens, causal)
+
+
+def test_layouts():
+    rng = np.random.default_rng(7)
+    dt, n, h, d = torch.bfloat16, 150, 4, 64
+    mix = dev(rng.standard_normal((2, n, h, 3, d)), dt)
+    q, k, v = (mix[:, :, :, i] for i in range(3))
+    want = cr.convrot_attention(q.contiguous(), k.contiguous(), v.contiguous())
+    assert torch.equal(cr.convrot_attention(q, k, v), want)
+    # into columns of a wider tensor that holds the inputs
+    wide = torch.cat([t.reshape(2 * n, h * d) for t in (q, k, v)], 1)
+    wide = torch.cat([wide, torch.zeros_like(wide[:, :h * d])], 1)
+    col = [wide[:, i * h * d:(i + 1) * h * d].view(2, n, h, d) for i in range(4)]
+    assert torch.equal(cr.convrot_attention(*col[:3], out=col[3]), want)
+    # heads outermost
+    hm = [t[0].transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v)]
+    assert torch.equal(cr.convrot_attention(*hm), want[0])
+    for b in range(2):
+        close(q[b], k[b], v[b], want[b], None, 1 / 8, False)
+
+
+def test_scale_and_large_scores():
+    rng = np.random.default_rng(8)
+    q, k, v = make(rng, [64], [100], 2, 2, 64, torch.bfloat16)
+    for scale in (1e-3, 0.7, 3.0):
+        out, lse = cr.convrot_attention(q, k, v, scale=scale, return_lse=True)
+        close(q, k, v, out, lse, scale, False)
+    # scores of 10^30, all negative, and equal
+    big = torch.full_like(q, 1e15)
+    out, lse = cr.convrot_attention(big, -big[:1].expand(100, 2, 64), v, return_lse=True)
+    want = v.double().mean(0)
+    assert ((out.double() - want).abs().max() <= 2.0 ** -7 * v.abs().max()).item()
+    assert (lse < -1e28).all().item()
+
+
+@pytest.mark.parametrize("n,length,hq,hk", [(1, 9000, 8, 2), (3, 700, 4, 4), (100, 3000, 2, 1)])
+def test_workspaces(n, length, hq, hk):
+    rng = np.random.default_rng(9)
+    q, k, v = make(rng, [n], [length], hq, hk, 128, torch.float16, 2.0)
+    size = cr.convrot_attention_workspace_size(q, k, v)
+    assert size > 0
+    want, lse = cr.convrot_attention(q, k, v, return_lse=True)
+    close(q, k, v, want, lse, 128 ** -0.5, False)
+    guard = torch.full((size + 1024,), 77, dtype=torch.uint8, device=DEV)
+    got = cr.convrot_attention(q, k, v, workspace=guard[256:256 + size])
+    assert torch.equal(got, want)
+    assert (guard[:256] == 77).all() and (guard[256 + size:] == 77).all()
+    for part in (0, 256, size // 2, size - 256):
+        got, lse = cr.convrot_attention(q, k, v, workspace=guard[:part], return_lse=True)
+        close(q, k, v, got, lse, 128 ** -0.5, False)
+        assert (guard[256 + size:] == 77).all()
+
+
+def test_results_repeat_and_do_not_depend_on_the_device():
+    rng = np.random.default_rng(10)
+    for n, length, hq, hk in ((300, 900, 4, 2), (1, 5000, 8, 1)):
+        q, k, v = make(rng, [n], [length], hq, hk, 128, torch.bfloat16)
+        want = cr.convrot_attention(q, k, v, causal=True)
+        for cus in (3, 64):
+            cr.convrot_set_compute_units(cus)
+            try:
+                assert torch.equal(cr.convrot_attention(q, k, v, causal=True), want)
+            finally:
+                cr.convrot_set_compute_units(0)
+
+
+def test_streams_and_graphs():
+    rng = np.random.default_rng(11)
+    calls = []
+    for n, length, hq, hk in ((200, 300, 4, 2), (2, 6000, 8, 2), (1, 9000, 4, 1)):
+        q, k, v = make(rng, [n], [length], hq, hk, 64, torch.bfloat16)
+        calls.append((q, k, v, cr.convrot_attention(q, k, v, causal=True)))
+    streams = [torch.cuda.Stream() for _ in calls]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        for s, (q, k, v, _) in zip(streams, calls):
+            with torch.cuda.stream(s):
+                got.append(cr.convrot_attention(q, k, v, causal=True))
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, calls[i % 3][3])
+    out = [torch.zeros_like(c[3]) for c in calls]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for (q, k, v, _), o in zip(calls, out):
+            cr.convrot_attention(q, k, v, causal=True, out=o)
+    for _ in range(3):
+        for o in out:
+            o.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, c[3]) for o, c in zip(out, calls))
+        torch.ones(1000, device=DEV).sum().item()
+    # other lengths in the same buffers are read at each replay
+    used = torch.tensor([9000], dtype=torch.int32, device=DEV)
+    q, k, v, _ = calls[2]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cr.convrot_attention(q, k, v, k_lens=used, out=out[2])
+    for n in (9000, 1, 4321, 0):
+        used.fill_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        close(q, k[:n], v[:n], out[2], None, 1 / 8, False)
+
+
+def test_a_block():
+    """Projection, norms and rotation in place, attention, output projection: the
+    attention half of a block as a model runs it, over two packed sequences."""
+    rng = np.random.default_rng(12)
+    lens, heads, d = [150, 70], 4, 64
+    t, width = sum(lens), heads * d
+    x = dev(rng.standard_normal((t, width)), torch.bfloat16)
+    w_in = cr.convrot_quantize_mx4(dev(rng.standard_normal((3 * width, width)) * 0.06,
+                                       torch.bfloat16), 256)
+    w_out = cr.convrot_quantize_mx4(dev(rng.standard_normal((width, width)) * 0.06,
+                                        torch.bfloat16), 256)
+    weight = dev(1 + 0.1 * rng.standard_normal(d), torch.bfloat16)
+    pos = np.stack([np.zeros(t), np.arange(t) // 10, np.arange(t) % 10], 1).astype(np.int64)
+    table = cr.convrot_rope_table(dev(pos, torch.int64), (16, 24, 24))
+    qkv = cr.convrot_linear_mx4(x, *w_in, 256)
+    q, k, v = qkv.view(t, 3, heads, d).unbind(1)
+    raw = [f64(y) for y in (q, k, v)]
+    q, k = cr.convrot_qk_norm_rope(q, k, table, q_weight=weight, k_weight=weight, q_out=q, k_out=k)
+    for y, r in zip((q, k), raw):
+        ms = np.sqrt((r ** 2).mean(-1, keepdims=True) + 1e-6)
+        want = ref.rotate(r / ms * f64(weight), f64(table), False)
+        mag = np.abs(r / ms * f64(weight)).max(-1, keepdims=True)
+        assert (np.abs(f64(y) - want) <= 2.0 ** -8 * np.abs(want) + 200 * U * mag).all()
+    at = offsets(lens)
+    o, lse = cr.convrot_attention(q, k, v, q_offsets=at, k_offsets=at, return_lse=True)
+    check_packed(q, k, v, o, lse, lens, lens, False)
+    y = cr.convrot_linear_mx4(o.reshape(t, width), *w_out, 256)
+    codes, scales = cr.convrot_quantize_mx4(o.reshape(t, width), 256)
+    assert torch.equal(y, cr.convrot_gemm_mx4(codes, scales, *w_out))
