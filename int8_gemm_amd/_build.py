@@ -37,7 +37,7 @@ def hipcc() -> str:
 # that they fit); otherwise the allocator shuffles accumulator blocks between
 # AGPR ranges every K-step
 _VGPR_FORM = ["-mllvm", "--amdgpu-mfma-vgpr-form"]
-EXTRA_FLAGS = {"gemm.hip": _VGPR_FORM, "gemm_mx4.hip": _VGPR_FORM}
+EXTRA_FLAGS = {"gemm.hip": _VGPR_FORM, "gemm_mx4.hip": _VGPR_FORM, "attention.hip": _VGPR_FORM}
 
 
 def _compile(src: str) -> str:

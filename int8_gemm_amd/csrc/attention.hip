@@ -29,6 +29,12 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 constexpr int kTileKeys = 64;   // keys of a copied tile
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
+// A row's reference m is a largest score of it: it is raised when a score passes it by
+// kRoom / c, so weights stay below 2^(kRoom + kLift). Half weights are lifted so that
+// those of 2^-20 of the largest are normal numbers; the sum is lifted with them.
+constexpr float kRoom = 8.f;
+template <bool F16>
+constexpr float kLift = F16 ? 6.f : 0.f;
 constexpr float kLowest = -3.402823466e38f;
 
 template <bool F16>
@@ -279,15 +285,18 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
   };
 
   v16f o[T::kDTiles][QT];
-  float m[QT], l[QT];
+  v16f below[QT];           // -m in every place: the first product starts from it
+  float l[QT], raise_at[QT];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    m[t] = kLowest;
+    below[t] = (v16f){0};
+    raise_at[t] = -__builtin_inff();  // no m yet
     l[t] = 0.f;
 #pragma unroll
     for (int d = 0; d < T::kDTiles; ++d) o[d][t] = (v16f){0};
   }
   const float c = a.scale * kLog2e;
+  const float room = kRoom / c;
 
   if (t0 < tiles) issue(t0, 0);
   for (int t = t0; t < tiles; ++t) {
@@ -302,14 +311,13 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
-      for (int q = 0; q < QT; ++q) s[u][q] = (v16f){0};
-#pragma unroll
       for (int st = 0; st < T::kSteps; ++st) {
         const int r = u * 32 + col;
         const u4 kf = *reinterpret_cast<const u4*>(kt + r * T::kRowBytes +
                                                    k_slot<DP>(r, 2 * st + half) * 16);
 #pragma unroll
-        for (int q = 0; q < QT; ++q) s[u][q] = mfma<F16>(kf, qf[q][st], s[u][q]);
+        for (int q = 0; q < QT; ++q)
+          s[u][q] = mfma<F16>(kf, qf[q][st], st == 0 ? below[q] : s[u][q]);
       }
     }
     const int key0 = t * kTileKeys;
@@ -324,28 +332,49 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
             if (key >= seen[q]) s[u][q][i] = -__builtin_inff();
           }
     }
-    u4 p[2][QT][2];
+    float top[QT];
+    bool raise = false;
 #pragma unroll
     for (int q = 0; q < QT; ++q) {
-      float top = s[0][q][0];
+      top[q] = s[0][q][0];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][q][i]);
-      top = fmaxf(top, other_half(top));
-      top = fmaxf(top, m[q]);
-      const float alpha = __builtin_amdgcn_exp2f((m[q] - top) * c);
-      m[q] = top;
-      l[q] *= alpha;
+        for (int i = 0; i < 16; ++i) top[q] = fmaxf(top[q], s[u][q][i]);
+      top[q] = fmaxf(top[q], other_half(top[q]));
+      raise |= top[q] > raise_at[q];
+    }
+    if (__any(raise)) {
 #pragma unroll
-      for (int d = 0; d < T::kDTiles; ++d)
+      for (int q = 0; q < QT; ++q) {
+        const bool up = top[q] > raise_at[q];
+        const float by = up ? top[q] : 0.f;
+        // a row without an m has nothing to scale yet (or NaN, which stays)
+        const float alpha =
+            up && raise_at[q] > kLowest ? __builtin_amdgcn_exp2f(-by * c) : 1.f;
+        raise_at[q] = up ? room : raise_at[q];
+        l[q] *= alpha;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][q][i] *= alpha;
+        for (int i = 0; i < 16; ++i) below[q][i] -= by;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[u][q][i] -= by;
+#pragma unroll
+        for (int d = 0; d < T::kDTiles; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[d][q][i] *= alpha;
+      }
+    }
+    u4 p[2][QT][2];
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[u][q][i] = __builtin_amdgcn_exp2f((s[u][q][i] - top) * c);
+          s[u][q][i] = __builtin_amdgcn_exp2f(
+              F16 ? __builtin_fmaf(s[u][q][i], c, kLift<F16>) : s[u][q][i] * c);
           l[q] += s[u][q][i];
         }
 #pragma unroll
@@ -407,7 +436,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
   for (int q = 0; q < QT; ++q) {
     const float sum = l[q] + other_half(l[q]);
     const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
-    const float lse2 = sum > 0.f || sum != sum ? m[q] * c + log2f(sum) : -__builtin_inff();
+    const float lse2 = sum > 0.f || sum != sum ? log2f(sum) - kLift<F16> - below[q][0] * c : -__builtin_inff();
     if (row[q] >= rows) continue;
     const int token = row[q] / group, head = hk * group + row[q] % group;
     if (a.splits > 1) {
