@@ -63,9 +63,10 @@ struct AttentionArgs {
 };
 // How a call is cut: the kernel's rows per block, its slots per key head, key splits.
 struct AttentionPlan {
-  int rows = 0;        // rows (query, head of the group) of a block's tile
+  int rows = 0;        // rows (query, head of the group) of a block's tile; 32: few rows
   int64_t slots = 0;   // tiles per key head, at most
   int splits = 1;
+  int chunk = 0;  // few rows: units of 32 keys of a split
   int64_t grid = 0;
 };
 // By sizes alone, so that results do not depend on the device.

@@ -24,6 +24,7 @@ namespace {
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef _Float16 hf8 __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileKeys = 64;   // keys of a copied tile
@@ -145,6 +146,22 @@ __device__ bool find(const AttentionArgs& a, int64_t slot, Where* w) {
   return false;
 }
 
+// V^T of 16 keys for the second product, 32 elements of the head: keys 4 half + .. and
+// those 8 further, the order in which the first product leaves a row's keys.
+template <int DP>
+__device__ __forceinline__ u4 values(const uint8_t* vt, int key, int dtile) {
+  typedef __attribute__((address_space(3))) s4* lp;
+  const int lane = threadIdx.x & 63;
+  const int r = key + (lane >> 5) * 4 + ((lane & 15) >> 2);
+  const int chunk = dtile * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+  const int at = r * DP * 2 + v_slot<DP>(r, chunk) * 16 + (lane & 1) * 8;
+  uint8_t* p = const_cast<uint8_t*>(vt) + at;
+  const u2 w0 = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)p));
+  const u2 w1 =
+      __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p + 8 * DP * 2)));
+  return (u4){w0.x, w0.y, w1.x, w1.y};
+}
+
 template <int DP, int QT, int NW, bool F16>
 struct Kernel {
   static constexpr int kRows = 32 * QT * NW;         // rows of a block
@@ -174,12 +191,12 @@ __device__ __forceinline__ bool nonfinite16(uint32_t h) {
 }
 
 // True if the tile holds an infinity or a NaN; none is left then.
-template <bool F16, int DP>
+template <bool F16, int DP, int KEYS>
 __device__ __forceinline__ bool clear_nonfinite(uint8_t* vt) {
   const int lane = threadIdx.x & 63;
   uint32_t found = 0;
 #pragma unroll 1
-  for (int i = lane; i < kTileKeys * DP / 8; i += 64) {
+  for (int i = lane; i < KEYS * DP / 8; i += 64) {
     const u4 w = *reinterpret_cast<const u4*>(vt + i * 16);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -187,7 +204,7 @@ __device__ __forceinline__ bool clear_nonfinite(uint8_t* vt) {
   }
   if (__builtin_expect(!__any(found != 0), 1)) return false;
 #pragma unroll 1
-  for (int i = lane; i < kTileKeys * DP / 2; i += 64) {
+  for (int i = lane; i < KEYS * DP / 2; i += 64) {
     uint32_t* at = reinterpret_cast<uint32_t*>(vt + i * 4);
     const uint32_t w = *at;
     const uint32_t keep = (nonfinite16<F16>(w & 0xFFFFu) ? 0u : 0xFFFFu) |
@@ -198,9 +215,27 @@ __device__ __forceinline__ bool clear_nonfinite(uint8_t* vt) {
   return true;
 }
 
+// What key `key` of the tensor has of them, added to a row that sees it.
+template <int DTILES, bool F16>
+__device__ __forceinline__ void add_nonfinite(const AttentionArgs& a, int64_t key, int hk,
+                                              bool sees, v16f (&o)[DTILES]) {
+  const int half = (threadIdx.x >> 5) & 1;
+  const uint16_t* vr = a.v + key * a.v_stride + hk * a.v_head_stride;
+#pragma unroll
+  for (int d = 0; d < DTILES; ++d) {
+    asm volatile("" ::: "memory");  // one tile's loads at a time
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int e = d * 32 + 8 * (i >> 2) + 4 * half + (i & 3);
+      const uint32_t h = e < a.d ? vr[e] : 0;
+      if (sees && nonfinite16<F16>(h)) o[d][i] += lo16<F16>(h);
+    }
+  }
+}
+
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, int64_t slots,
-                                                               int xcds) {
+__global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, uint32_t slots,
+                                                               uint32_t xcds) {
   using T = Kernel<DP, QT, NW, F16>;
   extern __shared__ __align__(1024) uint8_t lds[];
   volatile int* cleared = reinterpret_cast<int*>(lds + 2 * T::kStages * T::kTileBytes);
@@ -212,15 +247,15 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
 
   // blocks of an XCD (they are dealt in turn) take neighbouring tiles of the same
   // heads, whose keys then meet in its L2
-  int64_t id = blockIdx.x;
+  uint32_t id = blockIdx.x;
   {
-    const int64_t total = gridDim.x, full = total / xcds, rest = total % xcds;
-    const int64_t x = id % xcds, i = id / xcds;
-    id = x * full + (x < rest ? x : rest) + i;
+    const uint32_t total = gridDim.x, full = total / xcds, rest = total % xcds;
+    const uint32_t x = id % xcds, i = id / xcds;
+    id = x * full + min(x, rest) + i;
   }
-  const int split = (int)(id % a.splits);
-  id /= a.splits;
-  int64_t slot = id % slots;
+  const int split = (int)(id % (uint32_t)a.splits);
+  id /= (uint32_t)a.splits;
+  uint32_t slot = id % slots;
   const int hk = (int)(id / slots);
   Where w;
   if (CAUSAL) slot = slots - 1 - slot;  // long tiles first
@@ -284,7 +319,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
     }
   };
 
-  v16f o[T::kDTiles][QT];
+  v16f o[QT][T::kDTiles];
   v16f below[QT];           // -m in every place: the first product starts from it
   float l[QT], raise_at[QT];
 #pragma unroll
@@ -293,7 +328,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
     raise_at[t] = -__builtin_inff();  // no m yet
     l[t] = 0.f;
 #pragma unroll
-    for (int d = 0; d < T::kDTiles; ++d) o[d][t] = (v16f){0};
+    for (int d = 0; d < T::kDTiles; ++d) o[t][d] = (v16f){0};
   }
   const float c = a.scale * kLog2e;
   const float room = kRoom / c;
@@ -363,7 +398,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
 #pragma unroll
         for (int d = 0; d < T::kDTiles; ++d)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[d][q][i] *= alpha;
+          for (int i = 0; i < 16; ++i) o[q][d][i] *= alpha;
       }
     }
     u4 p[2][QT][2];
@@ -384,28 +419,16 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
             p[u][q][h][e] = pack16x2<F16>(s[u][q][8 * h + 2 * e], s[u][q][8 * h + 2 * e + 1]);
       }
     }
-    // V^T: 32 elements of the head, keys 16 h + 4 half + .. of a unit and those 8 further
-    auto values = [&](int u, int h, int d) {
-      const int r = u * 32 + h * 16 + half * 4 + ((lane & 15) >> 2);
-      const int chunk = d * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-      const int at = v_slot<DP>(r, chunk) * 16 + (lane & 1) * 8;
-      typedef __attribute__((address_space(3))) s4* lp;
-      const u2 w0 = __builtin_bit_cast(
-          u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vt + r * T::kRowBytes + at)));
-      const u2 w1 = __builtin_bit_cast(
-          u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vt + (r + 8) * T::kRowBytes + at)));
-      return (u4){w0.x, w0.y, w1.x, w1.y};
-    };
-    if (CAUSAL && key0 + kTileKeys > full && clear_nonfinite<F16, DP>(vt)) *cleared = 1;
+    if (CAUSAL && key0 + kTileKeys > full && clear_nonfinite<F16, DP, kTileKeys>(vt)) *cleared = 1;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int d = 0; d < T::kDTiles; ++d) {
-          const u4 vf = values(u, h, d);
+          const u4 vf = values<DP>(vt, u * 32 + h * 16, d);
 #pragma unroll
-          for (int q = 0; q < QT; ++q) o[d][q] = mfma<F16>(vf, p[u][q][h], o[d][q]);
+          for (int q = 0; q < QT; ++q) o[q][d] = mfma<F16>(vf, p[u][q][h], o[q][d]);
         }
   }
 
@@ -415,20 +438,10 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
     if (__builtin_expect(*cleared, 0)) {
       const int to = min(end, tiles * kTileKeys);
 #pragma unroll 1
-      for (int key = max(full / kTileKeys, t0) * kTileKeys; key < to; ++key) {
-        const uint16_t* vr = a.v + (w.k0 + key) * a.v_stride + hk * a.v_head_stride;
+      for (int key = max(full / kTileKeys, t0) * kTileKeys; key < to; ++key)
 #pragma unroll
-        for (int d = 0; d < T::kDTiles; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int e = d * 32 + 8 * (i >> 2) + 4 * half + (i & 3);
-            const uint32_t h = e < a.d ? vr[e] : 0;
-            const float f = lo16<F16>(h);
-#pragma unroll
-            for (int q = 0; q < QT; ++q)
-              if (nonfinite16<F16>(h) && key < seen[q]) o[d][q][i] += f;
-          }
-      }
+        for (int q = 0; q < QT; ++q)
+          add_nonfinite<T::kDTiles, F16>(a, w.k0 + key, hk, key < seen[q], o[q]);
     }
   }
 
@@ -449,9 +462,8 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = d * 32 + i * 8 + half * 4;
-          typedef float v4f __attribute__((ext_vector_type(4)));
-          const v4f f = {o[d][q][4 * i] * inv, o[d][q][4 * i + 1] * inv, o[d][q][4 * i + 2] * inv,
-                         o[d][q][4 * i + 3] * inv};
+              const v4f f = {o[q][d][4 * i] * inv, o[q][d][4 * i + 1] * inv, o[q][d][4 * i + 2] * inv,
+                         o[q][d][4 * i + 3] * inv};
           if (e < a.d) *reinterpret_cast<v4f*>(to + e) = f;
         }
       continue;
@@ -463,10 +475,252 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int e = d * 32 + i * 8 + half * 4;
-        const u2 f = {pack16x2<F16>(o[d][q][4 * i] * inv, o[d][q][4 * i + 1] * inv),
-                      pack16x2<F16>(o[d][q][4 * i + 2] * inv, o[d][q][4 * i + 3] * inv)};
+        const u2 f = {pack16x2<F16>(o[q][d][4 * i] * inv, o[q][d][4 * i + 1] * inv),
+                      pack16x2<F16>(o[q][d][4 * i + 2] * inv, o[q][d][4 * i + 3] * inv)};
         if (e < a.d) *reinterpret_cast<u2*>(to + e) = f;
       }
+  }
+}
+
+// ---- few rows: single tokens against a long cache ----------------------------
+//
+// Up to 32 rows a tile, bound by the bytes of the keys: every wave of a block
+// streams its own units of 32 keys, copied two ahead into its own part of LDS, and
+// waits for no other wave until the end, where the waves' sums are joined. Weights
+// go into the second product in two 16-bit parts, which costs nothing here.
+template <int DP>
+struct Few {
+  static constexpr int kWaves = DP == 256 ? 2 : 4;
+  static constexpr int kUnit = 32;
+  static constexpr int kRowBytes = DP * 2;
+  static constexpr int kChunks = DP / 8;
+  static constexpr int kUnitBytes = kUnit * kRowBytes;
+  static constexpr int kRing = 2;
+  static constexpr int kWaveBytes = 2 * kRing * kUnitBytes;  // K and V
+  static constexpr int kCopies = kUnitBytes / 1024;
+  static constexpr int kJoinRow = DP + 4;  // floats of a row of partial sums
+  static constexpr int kLds = kWaves * kWaveBytes;
+  static_assert(kWaves * (32 * kJoinRow + 64) * 4 <= kLds, "sums fit the ring");
+};
+
+template <int DP, bool F16>
+__global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(AttentionArgs a,
+                                                                                int chunk) {
+  using T = Few<DP>;
+  constexpr int kSteps = DP / 16, kDTiles = DP / 32;
+  extern __shared__ __align__(1024) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, col = lane & 31;
+  const int group = a.q_heads / a.k_heads;
+  const uint32_t id = blockIdx.x;
+  const int split = (int)(id % (uint32_t)a.splits);
+  const uint32_t rest = id / (uint32_t)a.splits;
+  const int hk = (int)(rest % (uint32_t)a.k_heads);
+  Where w;
+  if (!find<32>(a, rest / (uint32_t)a.k_heads, &w)) return;
+
+  const int rows = w.lq * group, row0 = w.tile * 32;
+  const int shift = w.lk - w.lq + 1;
+  int end = w.lk, full = w.lk;
+  if (a.causal) {
+    end = min(w.lk, max(0, min(rows - 1, row0 + 31) / group + shift));
+    full = min(w.lk, max(0, row0 / group + shift));
+  }
+  // units of this split, dealt to the waves: `chunk`, or more where the sequence is longer
+  const int units = (end + T::kUnit - 1) / T::kUnit;
+  const int per = max(chunk, (units + a.splits - 1) / a.splits);
+  const int first = min(units, split * per), last = min(units, first + per);
+
+  const int row = row0 + col;
+  const int r = min(row, rows - 1);
+  const int token = r / group, head = hk * group + r % group;
+  const int seen = a.causal ? min(w.lk, token + shift) : w.lk;
+  u4 qf[kSteps];
+  {
+    const uint16_t* q = a.q + (w.q0 + token) * a.q_stride + head * a.q_head_stride;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int e = (2 * s + half) * 8;
+      const u4 zero = {0, 0, 0, 0};
+      qf[s] = e < a.d ? *reinterpret_cast<const u4*>(q + e) : zero;
+    }
+  }
+
+  const int8_t* kbase =
+      reinterpret_cast<const int8_t*>(a.k + w.k0 * a.k_stride + hk * a.k_head_stride);
+  const int8_t* vbase =
+      reinterpret_cast<const int8_t*>(a.v + w.k0 * a.v_stride + hk * a.v_head_stride);
+  const uint32_t kstride = (uint32_t)a.k_stride * 2, vstride = (uint32_t)a.v_stride * 2;
+  const int ring = wave * T::kWaveBytes;
+  auto issue = [&](int u, int stage) {
+    const int top = w.lk - 1 - u * T::kUnit;  // rows behind it repeat it
+    const int8_t* kp = kbase + (int64_t)u * T::kUnit * a.k_stride * 2;
+    const int8_t* vp = vbase + (int64_t)u * T::kUnit * a.v_stride * 2;
+    const int to = ring + stage * 2 * T::kUnitBytes;
+#pragma unroll
+    for (int i = 0; i < T::kCopies; ++i) {
+      const int n = i * 64 + lane, from = min(n / T::kChunks, top);
+      const int c = min(k_slot<DP>(n / T::kChunks, n % T::kChunks), a.d / 8 - 1);
+      dma16(kp, from * kstride + c * 16, to + i * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < T::kCopies; ++i) {
+      const int n = i * 64 + lane, from = min(n / T::kChunks, top);
+      const int c = min(v_slot<DP>(n / T::kChunks, n % T::kChunks), a.d / 8 - 1);
+      dma16(vp, from * vstride + c * 16, to + T::kUnitBytes + i * 1024);
+    }
+  };
+
+  v16f o[kDTiles], below = (v16f){0};
+#pragma unroll
+  for (int d = 0; d < kDTiles; ++d) o[d] = (v16f){0};
+  float l = 0.f, raise_at = -__builtin_inff();
+  const float c = a.scale * kLog2e, room = kRoom / c;
+
+  int u = first + wave, stage = 0;
+  if (u < last) issue(u, 0);
+  for (; u < last; u += T::kWaves, stage ^= 1) {
+    const bool more = u + T::kWaves < last;
+    wait_lgkm0();  // the other stage's last reads
+    asm volatile("" ::: "memory");
+    if (more) {
+      issue(u + T::kWaves, stage ^ 1);
+      wait_vmcnt<3 * T::kCopies>();
+    } else {
+      wait_vmcnt<T::kCopies>();
+    }
+    asm volatile("" ::: "memory");
+    const uint8_t* kt = lds + ring + stage * 2 * T::kUnitBytes;
+    uint8_t* vt = lds + ring + stage * 2 * T::kUnitBytes + T::kUnitBytes;
+    v16f s = below;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      const u4 kf = *reinterpret_cast<const u4*>(kt + col * T::kRowBytes +
+                                                 k_slot<DP>(col, 2 * st + half) * 16);
+      s = mfma<F16>(kf, qf[st], s);
+    }
+    const int key0 = u * T::kUnit;
+    if (key0 + T::kUnit > full) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (key0 + 8 * (i >> 2) + 4 * half + (i & 3) >= seen) s[i] = -__builtin_inff();
+    }
+    float top = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    top = fmaxf(top, other_half(top));
+    if (__any(top > raise_at)) {
+      const bool up = top > raise_at;
+      const float by = up ? top : 0.f;
+      const float alpha = up && raise_at > kLowest ? __builtin_amdgcn_exp2f(-by * c) : 1.f;
+      raise_at = up ? room : raise_at;
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        below[i] -= by;
+        s[i] -= by;
+      }
+#pragma unroll
+      for (int d = 0; d < kDTiles; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
+    }
+    u4 hi[2], lo[2];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[i] = __builtin_amdgcn_exp2f(F16 ? __builtin_fmaf(s[i], c, kLift<F16>) : s[i] * c);
+      l += s[i];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p0 = s[8 * h + 2 * e], p1 = s[8 * h + 2 * e + 1];
+        const uint32_t p = pack16x2<F16>(p0, p1);
+        hi[h][e] = p;
+        lo[h][e] = pack16x2<F16>(p0 - lo16<F16>(p), p1 - hi16<F16>(p));
+      }
+    if (more)
+      wait_vmcnt<2 * T::kCopies>();
+    else
+      wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+    const bool cleared =
+        a.causal && key0 + T::kUnit > full && clear_nonfinite<F16, DP, T::kUnit>(vt);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int d = 0; d < kDTiles; ++d) {
+        const u4 vf = values<DP>(vt, h * 16, d);
+        o[d] = mfma<F16>(vf, hi[h], o[d]);
+        o[d] = mfma<F16>(vf, lo[h], o[d]);
+      }
+    if (__builtin_expect(cleared, 0)) {
+      const int to = min(end, key0 + T::kUnit);
+      for (int key = key0; key < to; ++key)
+        add_nonfinite<kDTiles, F16>(a, w.k0 + key, hk, key < seen, o);
+    }
+  }
+
+  // ---- join the waves: sums of each go to LDS, [row][element], with their m and l ----
+  const float sum = l + other_half(l);
+  wait_lgkm0();
+  lds_barrier();
+  constexpr int kPart = 32 * T::kJoinRow;
+  float* part = reinterpret_cast<float*>(lds);
+  float* stat = part + T::kWaves * kPart;  // [wave][m, l][32]
+#pragma unroll
+  for (int d = 0; d < kDTiles; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const v4f f = {o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+      *reinterpret_cast<v4f*>(part + wave * kPart + col * T::kJoinRow + d * 32 + i * 8 +
+                              half * 4) = f;
+    }
+  if (half == 0) {
+    // a row without an m has seen nothing, or only NaN
+    stat[wave * 64 + col] = raise_at > kLowest ? -below[0] : kLowest;
+    stat[wave * 64 + 32 + col] = sum;
+  }
+  wait_lgkm0();
+  lds_barrier();
+  const int here = min(32, rows - row0);
+  constexpr int kQuads = DP / 4;
+  for (int i = threadIdx.x; i < here * kQuads; i += 64 * T::kWaves) {
+    const int jr = i / kQuads, e = i % kQuads * 4;
+    if (e >= a.d) continue;
+    float m = kLowest;
+#pragma unroll
+    for (int v = 0; v < T::kWaves; ++v) m = fmaxf(m, stat[v * 64 + jr]);
+    float total = 0.f;
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < T::kWaves; ++v) {
+      const float lv = stat[v * 64 + 32 + jr];
+      if (lv == 0.f) continue;  // saw nothing
+      const float f = __builtin_amdgcn_exp2f((stat[v * 64 + jr] - m) * c);
+      const v4f x = *reinterpret_cast<const v4f*>(part + v * kPart + jr * T::kJoinRow + e);
+      total += f * lv;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[q] = __builtin_fmaf(f, x[q], acc[q]);
+    }
+    const bool some = total > 0.f || total != total;
+    const float inv = some ? 1.0f / total : 0.f;
+    const float lse2 = some ? log2f(total) - kLift<F16> + m * c : -__builtin_inff();
+    const int jtoken = (row0 + jr) / group, jhead = hk * group + (row0 + jr) % group;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] *= inv;
+    if (a.splits > 1) {
+      const int64_t at = ((int64_t)split * a.q_tokens + w.q0 + jtoken) * a.q_heads + jhead;
+      if (e == 0) a.part_lse[at] = lse2;
+      if (some) *reinterpret_cast<v4f*>(a.part + at * a.d + e) = acc;
+      continue;
+    }
+    if (a.lse && e == 0) a.lse[(int64_t)jhead * a.q_tokens + w.q0 + jtoken] = lse2 * kLn2;
+    const u2 f = {pack16x2<F16>(acc[0], acc[1]), pack16x2<F16>(acc[2], acc[3])};
+    *reinterpret_cast<u2*>(a.out + (w.q0 + jtoken) * a.out_stride + jhead * a.out_head_stride + e) =
+        f;
   }
 }
 
@@ -490,7 +744,6 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
     const float f = __builtin_amdgcn_exp2f(x - top);
     sum += f;
     if (lane * 4 < a.d) {
-      typedef float v4f __attribute__((ext_vector_type(4)));
       const v4f v = *reinterpret_cast<const v4f*>(a.part + (s * all + r) * a.d + lane * 4);
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
@@ -518,15 +771,32 @@ hipError_t launch_tile(const AttentionArgs& a, const AttentionPlan& p, hipStream
                                              hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
     if (e != hipSuccess) return e;
   }
-  kern<<<dim3((uint32_t)p.grid), dim3(64 * NW), T::kLds, st>>>(a, p.slots,
+  kern<<<dim3((uint32_t)p.grid), dim3(64 * NW), T::kLds, st>>>(a, (uint32_t)p.slots,
                                                                xcd_count(compute_units()));
+  return hipGetLastError();
+}
+
+template <int DP, bool F16>
+hipError_t launch_few(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
+  using T = Few<DP>;
+  auto kern = attention_few_kernel<DP, F16>;
+  if (T::kLds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+    if (e != hipSuccess) return e;
+  }
+  kern<<<dim3((uint32_t)p.grid), dim3(64 * T::kWaves), T::kLds, st>>>(a, p.chunk);
   return hipGetLastError();
 }
 
 template <bool F16>
 hipError_t launch_dtype(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
   hipError_t e;
-  if (a.d <= 64)
+  if (p.rows == 32)
+    e = a.d <= 64    ? launch_few<64, F16>(a, p, st)
+        : a.d <= 128 ? launch_few<128, F16>(a, p, st)
+                     : launch_few<256, F16>(a, p, st);
+  else if (a.d <= 64)
     e = launch_tile<64, 1, 4, F16>(a, p, st);
   else if (a.d <= 128)
     e = launch_tile<128, 1, 4, F16>(a, p, st);
@@ -543,17 +813,34 @@ hipError_t launch_dtype(const AttentionArgs& a, const AttentionPlan& p, hipStrea
 AttentionPlan plan_attention(const AttentionArgs& a, int max_splits) {
   AttentionPlan p;
   const int64_t group = a.q_heads / a.k_heads;
-  p.rows = 128;
+  const int64_t rows = a.q_tokens * group;  // of a key head
+  const int64_t keys = a.k_tokens / a.batch;
+  p.rows = rows <= 32 * (int64_t)a.batch ? 32 : 128;
   if (a.q_offsets)
-    p.slots = (a.q_tokens * group + p.rows - 1) / p.rows + a.batch;
+    p.slots = (rows + p.rows - 1) / p.rows + a.batch;
   else
-    p.slots = a.batch * ((a.q_tokens / a.batch * group + p.rows - 1) / p.rows);
+    p.slots = a.batch * ((rows / a.batch + p.rows - 1) / p.rows);
   const int64_t blocks = p.slots * a.k_heads;
-  // fewer tiles than the card has compute units: split the keys
-  const int64_t tiles = (a.k_tokens / a.batch + kTileKeys - 1) / kTileKeys;
-  int64_t splits = blocks ? 512 / blocks : 1;
-  if (splits > tiles / 4) splits = tiles / 4;
-  if (splits > max_splits) splits = max_splits;
+  int64_t splits = 1;
+  if (p.rows == 32) {
+    // sequences may use less of their keys than there is room for: splits of a fixed
+    // length, about two rounds of a block per compute unit if all is used
+    const int64_t units = (keys + 31) / 32;
+    int64_t tiles = (rows + 31) / 32;
+    tiles = (tiles > a.batch ? tiles : a.batch) * a.k_heads;
+    int64_t chunk = (units * tiles + 511) / 512;
+    if (chunk < 8) chunk = 8;
+    splits = (units + chunk - 1) / chunk;
+    if (splits > max_splits) splits = max_splits;
+    if (splits < 1) splits = 1;
+    p.chunk = (int)((units + splits - 1) / splits);
+  } else {
+    // fewer tiles than the card has compute units: split the keys
+    const int64_t tiles = (keys + kTileKeys - 1) / kTileKeys;
+    splits = blocks ? 512 / blocks : 1;
+    if (splits > tiles / 4) splits = tiles / 4;
+    if (splits > max_splits) splits = max_splits;
+  }
   p.splits = splits < 1 ? 1 : (int)splits;
   p.grid = blocks * p.splits;
   return p;
