@@ -28,6 +28,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileKeys = 64;   // keys of a copied tile
+constexpr int kMaxSplits = 512;  // two rounds of a block per compute unit
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 // A row's reference m is a largest score of it: it is raised when a score passes it by
@@ -724,39 +725,79 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
   }
 }
 
-// Joins the splits of a row: out = sum_s 2^(lse_s - lse) out_s. A wave takes a
-// row, lanes 4 elements each.
+// Joins the splits of a row: out = sum_s 2^(lse_s - lse) out_s. A block takes a row: a
+// thread a split's factor, then groups of lanes, four elements each, the splits in turn,
+// all of whose loads are under way together.
+constexpr int kJoinThreads = 256;
+
 template <bool F16>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionArgs a, int lanes) {
+  __shared__ float factor[kMaxSplits];
+  __shared__ float red[2][kJoinThreads / 64];
+  __shared__ __align__(16) float acc[kJoinThreads * 4];
+  const int64_t r = blockIdx.x;
   const int64_t all = a.q_tokens * a.q_heads;
-  if (r >= all) return;
   const int64_t token = r / a.q_heads;
   const int head = (int)(r % a.q_heads);
   if (a.q_offsets && (token < a.q_offsets[0] || token >= a.q_offsets[a.batch])) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int group = tid / lanes, groups = kJoinThreads / lanes, e = tid % lanes * 4;
+
+  float x[kMaxSplits / kJoinThreads];
   float top = kLowest;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * all + r]);
-  float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float x = a.part_lse[s * all + r];
-    if (x == -__builtin_inff()) continue;
-    const float f = __builtin_amdgcn_exp2f(x - top);
-    sum += f;
-    if (lane * 4 < a.d) {
-      const v4f v = *reinterpret_cast<const v4f*>(a.part + (s * all + r) * a.d + lane * 4);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
+  for (int i = 0; i < kMaxSplits / kJoinThreads; ++i) {
+    const int s = tid + i * kJoinThreads;
+    x[i] = s < a.splits ? a.part_lse[s * all + r] : -__builtin_inff();
+    top = fmaxf(top, x[i]);
+  }
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
+  if (lane == 0) red[0][wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoinThreads / 64; ++i) top = fmaxf(top, red[0][i]);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / kJoinThreads; ++i) {
+    const float f = __builtin_amdgcn_exp2f(x[i] - top);  // 0 for a split that saw nothing
+    if (tid + i * kJoinThreads < a.splits) factor[tid + i * kJoinThreads] = f;
+    sum += f;
+  }
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
+  if (lane == 0) red[1][wave] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinThreads / 64; ++i) sum += red[1][i];
+
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+  if (e < a.d) {
+    const float* from = a.part + r * a.d + e;
+#pragma unroll 8
+    for (int s = group; s < a.splits; s += groups) {
+      const float f = factor[s];
+      const v4f p = *reinterpret_cast<const v4f*>(from + (int64_t)s * all * a.d);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)  // what a split that saw nothing holds is not its result
+        v[q] = f != 0.f ? __builtin_fmaf(f, p[q], v[q]) : v[q];
     }
   }
+  *reinterpret_cast<v4f*>(acc + tid * 4) = v;
+  __syncthreads();
   const bool none = sum == 0.f;
-  const float inv = none ? 0.f : 1.0f / sum;
-  if (a.lse && lane == 0)
+  if (a.lse && tid == 0)
     a.lse[head * a.q_tokens + token] = none ? -__builtin_inff() : (top + log2f(sum)) * kLn2;
-  if (lane * 4 < a.d) {
-    const u2 f = {pack16x2<F16>(acc[0] * inv, acc[1] * inv),
-                  pack16x2<F16>(acc[2] * inv, acc[3] * inv)};
-    *reinterpret_cast<u2*>(a.out + token * a.out_stride + head * a.out_head_stride + lane * 4) = f;
+  if (group == 0 && e < a.d) {
+    for (int g = 1; g < groups; ++g) {
+      const v4f p = *reinterpret_cast<const v4f*>(acc + (g * lanes) * 4 + e);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] += p[q];
+    }
+    const float inv = none ? 0.f : 1.0f / sum;
+    const u2 f = {pack16x2<F16>(v[0] * inv, v[1] * inv), pack16x2<F16>(v[2] * inv, v[3] * inv)};
+    *reinterpret_cast<u2*>(a.out + token * a.out_stride + head * a.out_head_stride + e) = f;
   }
 }
 
@@ -803,8 +844,10 @@ hipError_t launch_dtype(const AttentionArgs& a, const AttentionPlan& p, hipStrea
   else
     e = launch_tile<256, 1, 4, F16>(a, p, st);
   if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t rows = a.q_tokens * a.q_heads;
-  attention_join_kernel<F16><<<dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, st>>>(a);
+  int lanes = 1;
+  while (lanes * 4 < a.d) lanes *= 2;
+  attention_join_kernel<F16>
+      <<<dim3((uint32_t)(a.q_tokens * a.q_heads)), dim3(kJoinThreads), 0, st>>>(a, lanes);
   return hipGetLastError();
 }
 
@@ -828,16 +871,17 @@ AttentionPlan plan_attention(const AttentionArgs& a, int max_splits) {
     const int64_t units = (keys + 31) / 32;
     int64_t tiles = (rows + 31) / 32;
     tiles = (tiles > a.batch ? tiles : a.batch) * a.k_heads;
-    int64_t chunk = (units * tiles + 511) / 512;
+    int64_t chunk = (units * tiles + kMaxSplits - 1) / kMaxSplits;
     if (chunk < 8) chunk = 8;
     splits = (units + chunk - 1) / chunk;
     if (splits > max_splits) splits = max_splits;
+    if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;
     p.chunk = (int)((units + splits - 1) / splits);
   } else {
     // fewer tiles than the card has compute units: split the keys
     const int64_t tiles = (keys + kTileKeys - 1) / kTileKeys;
-    splits = blocks ? 512 / blocks : 1;
+    splits = blocks ? kMaxSplits / blocks : 1;
     if (splits > tiles / 4) splits = tiles / 4;
     if (splits > max_splits) splits = max_splits;
   }
