@@ -6,7 +6,6 @@ the rest of the binding."""
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
@@ -43,14 +42,21 @@ class _AttentionArgs(ctypes.Structure):
                 + [("dtype", ctypes.c_int), ("scale", ctypes.c_float)])
 
 
+# As in mx4.py: one expression on the good path, what is wrong is worked out behind it.
+
 def _heads(t, name: str, dtype, dev: int):
     """Check a [tokens, heads, d] or [batch, length, heads, d] tensor; (address,
     tokens, heads, d, token stride, head stride, batch)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev:
+        shape, strides = t.shape, t.stride()
+        if len(shape) == 3 and strides[2] == 1:
+            tokens, heads, d = shape
+            if tokens > 1 and heads > 1:
+                return t.data_ptr(), tokens, heads, d, strides[0], strides[1], 1
+    elif not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.get_device() != dev:
+    else:
         raise ValueError(f"{name} is on {t.device}, expected device {dev}")
-    shape, strides = t.shape, t.stride()
     batch = 1
     if len(shape) == 4:
         batch, length, heads, d = shape
@@ -73,6 +79,14 @@ def _heads(t, name: str, dtype, dev: int):
         stride = (heads * d + 7) // 8 * 8
     return (t.data_ptr(), tokens, heads, d, stride, strides[-2] if heads > 1 else (d + 7) // 8 * 8,
             batch)
+
+
+def _like(x: torch.Tensor, tokens: int, heads: int, d: int):
+    """A new contiguous tensor of x's shape; with its address and strides as _heads'."""
+    out = torch.empty_strided(x.shape, (heads * d, d, 1) if x.dim() == 3 else
+                              (tokens // x.shape[0] * heads * d if x.shape[0] else 1, heads * d,
+                               d, 1), dtype=x.dtype, device=x.device)
+    return out, out.data_ptr(), heads * d, d
 
 
 def _first(t, name: str) -> int:
@@ -127,39 +141,51 @@ def convrot_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None,
     works in place."""
     if norm not in _NORMS or span not in ("head", "row"):
         raise ValueError(f"norm={norm!r}, span={span!r}: 'rms', 'layer' or None; 'head' or 'row'")
-    dev, dtype = _first(q, "q"), q.dtype
-    a = _QkArgs(norm=_NORMS[norm], row=span == "row", halves=halves, dtype=_DTYPES[dtype], eps=eps)
-    a.q, tokens, heads, d, a.q_stride, a.q_head_stride, _ = _heads(q, "q", dtype, dev)
-    a.tokens, a.q_heads, a.d = tokens, heads, d
+    dev, dtype, row = _first(q, "q"), q.dtype, span == "row"
+    pq, tokens, heads, d, qs, qh, _ = _heads(q, "q", dtype, dev)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
-    elif q_out.shape != q.shape:
-        raise ValueError(f"q_out must have shape {tuple(q.shape)} (got {tuple(q_out.shape)})")
-    a.q_out, _, _, _, a.q_out_stride, a.q_out_head_stride, _ = _heads(q_out, "q_out", dtype, dev)
-    if q_weight is not None:
-        a.q_weight = _weight(q_weight, "q_weight", dtype, dev, d, heads if span == "row" else 1)
+        q_out, pqo, qos, qoh = _like(q, tokens, heads, d)
+    elif q_out is q:
+        pqo, qos, qoh = pq, qs, qh
+    else:
+        pqo, qos, qoh = _output(q_out, "q_out", q, dev)
+    pqw = None if q_weight is None else _weight(q_weight, "q_weight", dtype, dev, d,
+                                                heads if row else 1)
+    pk = pko = pkw = None
+    k_heads = ks = kh = kos = koh = 0
     if k is not None:
-        a.k, k_tokens, a.k_heads, k_d, a.k_stride, a.k_head_stride, _ = _heads(k, "k", dtype, dev)
+        pk, k_tokens, k_heads, k_d, ks, kh, _ = _heads(k, "k", dtype, dev)
         if k_tokens != tokens or k_d != d:
             raise ValueError(f"k {tuple(k.shape)} does not fit q {tuple(q.shape)}")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=dtype, device=k.device)
-        elif k_out.shape != k.shape:
-            raise ValueError(f"k_out must have shape {tuple(k.shape)} (got {tuple(k_out.shape)})")
-        a.k_out, _, _, _, a.k_out_stride, a.k_out_head_stride, _ = _heads(k_out, "k_out", dtype,
-                                                                         dev)
+            k_out, pko, kos, koh = _like(k, tokens, k_heads, d)
+        elif k_out is k:
+            pko, kos, koh = pk, ks, kh
+        else:
+            pko, kos, koh = _output(k_out, "k_out", k, dev)
         if k_weight is not None:
-            a.k_weight = _weight(k_weight, "k_weight", dtype, dev, d,
-                                 a.k_heads if span == "row" else 1)
+            pkw = _weight(k_weight, "k_weight", dtype, dev, d, k_heads if row else 1)
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
+    pt, rows, pairs = None, 0, 0
     if table is not None:
-        if table.dim() != 3 or table.shape[2] != 2:
-            raise ValueError(f"table must be [rows, pairs, 2] (got shape {tuple(table.shape)})")
-        a.table = _tensor(table, "table", torch.float32, tuple(table.shape), dev)
-        a.table_rows, a.pairs = table.shape[0], table.shape[1]
+        shape = table.shape
+        if len(shape) != 3 or shape[2] != 2:
+            raise ValueError(f"table must be [rows, pairs, 2] (got shape {tuple(shape)})")
+        pt = _tensor(table, "table", torch.float32, shape, dev)
+        rows, pairs, _ = shape
+    a = _QkArgs(pq, pk, pqo, pko, pqw, pkw, pt, qs, qh, ks, kh, qos, qoh, kos, koh, tokens, rows,
+                heads, k_heads, d, pairs, _NORMS[norm], row, halves, _DTYPES[dtype], eps)
     _launch("convrot_qk_norm_rope", dev, ctypes.byref(a))
     return q_out, k_out
+
+
+def _output(out, name: str, like: torch.Tensor, dev: int):
+    """Check an output of another tensor's shape; (address, token and head stride)."""
+    p, _, _, _, stride, head_stride, _ = _heads(out, name, like.dtype, dev)
+    if out.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)} (got {tuple(out.shape)})")
+    return p, stride, head_stride
 
 
 def _weight(t, name: str, dtype, dev: int, d: int, heads: int) -> int:
@@ -167,34 +193,36 @@ def _weight(t, name: str, dtype, dev: int, d: int, heads: int) -> int:
     return _tensor(t, name, dtype, shape, dev)
 
 
+def _sequences(offsets, name: str, of: torch.Tensor, batch: int, dev: int):
+    """Check offsets into `of`, whose own batch counts without them; (address, sequences)."""
+    if offsets is None:
+        return None, batch
+    n = offsets.numel() - 1 if isinstance(offsets, torch.Tensor) else 0
+    p = _tensor(offsets, name, _I32, (n + 1,), dev)
+    if of.dim() == 4:
+        raise ValueError(f"{name} need a packed [tokens, heads, d] tensor")
+    if n < 1:
+        raise ValueError(f"{name} have one entry more than there are sequences")
+    return p, n
+
+
 def _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale):
+    """The arguments of a call but its outputs, and the device index."""
     dev, dtype = _first(q, "q"), q.dtype
-    a = _AttentionArgs(causal=causal, dtype=_DTYPES[dtype])
-    a.q, a.q_tokens, a.q_heads, d, a.q_stride, a.q_head_stride, q_batch = _heads(q, "q", dtype, dev)
-    a.k, k_tokens, k_heads, k_d, a.k_stride, a.k_head_stride, k_batch = _heads(k, "k", dtype, dev)
-    a.v, v_tokens, v_heads, v_d, a.v_stride, a.v_head_stride, _ = _heads(v, "v", dtype, dev)
-    if (k_tokens, k_heads, k_d) != (v_tokens, v_heads, v_d) or k_d != d:
+    pq, tokens, heads, d, qs, qh, batch = _heads(q, "q", dtype, dev)
+    pk, k_tokens, k_heads, k_d, ks, kh, k_batch = _heads(k, "k", dtype, dev)
+    pv, v_tokens, v_heads, v_d, vs, vh, _ = _heads(v, "v", dtype, dev)
+    if k_tokens != v_tokens or k_heads != v_heads or k_d != d or v_d != d:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not "
                          "fit")
-    a.k_tokens, a.k_heads, a.d = k_tokens, k_heads, d
-    batch = None
-    for t, name, of, n in ((q_offsets, "q_offsets", q, q_batch), (k_offsets, "k_offsets", k,
-                                                                  k_batch)):
-        if t is not None:
-            n = t.numel() - 1
-            setattr(a, name, _tensor(t, name, _I32, (n + 1,), dev))
-            if of.dim() == 4:
-                raise ValueError(f"{name} need a packed [tokens, heads, d] tensor")
-        if batch is not None and n != batch:
-            raise ValueError(f"{batch} sequences of queries, {n} of keys")
-        batch = n
-    if batch < 1:
-        raise ValueError("offsets have one entry more than there are sequences")
-    a.batch = batch
-    if k_lens is not None:
-        a.k_lens = _tensor(k_lens, "k_lens", _I32, (batch,), dev)
-    a.scale = 1.0 / math.sqrt(d) if scale is None else scale
-    return a, dev
+    pqo, batch = _sequences(q_offsets, "q_offsets", q, batch, dev)
+    pko, k_batch = _sequences(k_offsets, "k_offsets", k, k_batch, dev)
+    if batch != k_batch:
+        raise ValueError(f"{batch} sequences of queries, {k_batch} of keys")
+    pkl = None if k_lens is None else _tensor(k_lens, "k_lens", _I32, (batch,), dev)
+    return _AttentionArgs(pq, pk, pv, None, None, pqo, pko, pkl, qs, qh, ks, kh, vs, vh, 0, 0,
+                          tokens, k_tokens, batch, heads, k_heads, d, causal, _DTYPES[dtype],
+                          d ** -0.5 if scale is None else scale), dev
 
 
 def convrot_attention_workspace_size(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
@@ -218,28 +246,27 @@ def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     q [tokens, q_heads, d], k, v [tokens, k_heads, d] bf16 or fp16 packed by
     `q_offsets` and `k_offsets` (int32 [batch + 1]; none: one sequence), or
     [batch, length, heads, d]; k_lens (int32 [batch]): the keys in use of each
-    sequence. `causal` masks lower right. Rows that no sequence owns are not
-    written. `workspace` (uint8 on the device) defaults to what the call asks for."""
+    sequence. `causal` masks lower right; `scale` defaults to d^-1/2. Rows that no
+    sequence owns are not written. `workspace` (uint8 on the device) defaults to what
+    the call asks for."""
     a, dev = _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError(f"out must have shape {tuple(q.shape)} (got {tuple(out.shape)})")
-    a.out, _, _, _, a.out_stride, a.out_head_stride, _ = _heads(out, "out", q.dtype, dev)
+        out, a.out, a.out_stride, a.out_head_stride = _like(q, a.q_tokens, a.q_heads, a.d)
+    else:
+        a.out, a.out_stride, a.out_head_stride = _output(out, "out", q, dev)
     if lse is not None:
         a.lse = _tensor(lse, "lse", torch.float32, (a.q_heads, a.q_tokens), dev)
     elif return_lse:
         lse = torch.empty((a.q_heads, a.q_tokens), dtype=torch.float32, device=q.device)
         a.lse = lse.data_ptr()
-    if workspace is None:
+    pw, size = None, 0
+    if workspace is not None:
+        size = workspace.numel()
+        pw = _tensor(workspace, "workspace", _U8, (size,), dev)
+    else:
         size = load_library().convrot_attention_workspace_size(ctypes.byref(a))
         if size:
             workspace = torch.empty_strided((size,), (1,), dtype=_U8, device=q.device)
             pw = workspace.data_ptr()
-        else:
-            pw = None
-    else:
-        pw = _tensor(workspace, "workspace", _U8, (workspace.numel(),), dev)
-        size = workspace.numel()
     _launch("convrot_attention", dev, ctypes.byref(a), pw, size)
     return out if lse is None else (out, lse)

@@ -140,8 +140,6 @@ AttentionArgs attention_args(const convrot_attention_args& a) {
   return n;
 }
 
-constexpr int kMaxSplits = 1 << 20;
-
 }  // namespace
 
 extern "C" {
@@ -295,7 +293,7 @@ size_t convrot_attention_workspace_size(const convrot_attention_args* args) {
   DType dt;
   if (!args || check_attention("convrot_attention_workspace_size", *args, &dt)) return 0;
   const AttentionArgs n = attention_args(*args);
-  return attention_part_bytes(n, plan_attention(n, kMaxSplits).splits);
+  return attention_workspace(n, plan_attention(n, SIZE_MAX));
 }
 
 convrot_status convrot_attention(const convrot_attention_args* args, void* workspace,
@@ -318,8 +316,7 @@ convrot_status convrot_attention(const convrot_attention_args* args, void* works
                                        a.q_heads, kMaxStride))
     return s;
   AttentionArgs n = attention_args(a);
-  AttentionPlan p = plan_attention(n, kMaxSplits);
-  if (p.grid >= ((int64_t)1 << 23))
+  if (plan_attention(n, SIZE_MAX).grid >= ((int64_t)1 << 23))
     return fail(CONVROT_E_UNSUPPORTED_SHAPE, "%s: too many tiles (q_tokens=%lld heads=%d)", fn,
                 (long long)a.q_tokens, a.q_heads);
   if (a.q_tokens == 0) return ok();
@@ -354,14 +351,8 @@ convrot_status convrot_attention(const convrot_attention_args* args, void* works
   }
   bad |= overlap(a.lse, nlse, workspace, workspace_bytes);
   if (bad) return fail(CONVROT_E_INVALID_ARG, "%s: overlapping buffers", fn);
-  // as many splits as the workspace holds
-  if (attention_part_bytes(n, p.splits) > workspace_bytes) {
-    const size_t held = workspace_bytes / (attention_part_bytes(n, 2) / 2);
-    p = plan_attention(n, held < kMaxSplits ? (int)held : kMaxSplits);
-  }
-  n.splits = p.splits;
-  n.part = static_cast<float*>(workspace);
-  n.part_lse = n.part + (size_t)p.splits * (size_t)(a.q_tokens * a.q_heads) * a.d;
+  const AttentionPlan p = plan_attention(n, workspace_bytes);
+  attention_use(&n, p, workspace);
   return hip_status(launch_attention(n, p, dt, (hipStream_t)stream), fn);
 }
 

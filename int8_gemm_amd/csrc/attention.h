@@ -56,22 +56,29 @@ struct AttentionArgs {
   int batch, q_heads, k_heads, d;
   bool causal;
   float scale;
-  // splits > 1: each split's normalised rows and their log2 sums, joined by a second launch
+  // splits > 1: the tiles from `whole` on (few rows: all) go by parts, each split's
+  // normalised rows and their log2 sums, joined by a second launch
   int splits;
-  float* part;      // [splits][q_tokens * q_heads][d]
-  float* part_lse;  // [splits][q_tokens * q_heads]
+  uint32_t whole;
+  float* part;        // few rows: [split][q_tokens * q_heads][d]; else [tile][split][row][d]
+  float* part_lse;    // the same without d
+  int64_t* part_map;  // [tile][row]: row of the output, -1 for none; null for few rows
 };
-// How a call is cut: the kernel's rows per block, its slots per key head, key splits.
+// How a call is cut.
 struct AttentionPlan {
   int rows = 0;        // rows (query, head of the group) of a block's tile; 32: few rows
   int64_t slots = 0;   // tiles per key head, at most
-  int splits = 1;
-  int chunk = 0;  // few rows: units of 32 keys of a split
+  int64_t whole = 0;   // tiles of a block each
+  int splits = 1;      // parts of each of the others
+  int64_t part_rows = 0;
+  int chunk = 0;       // few rows: units of 32 keys of a split
   int64_t grid = 0;
 };
-// By sizes alone, so that results do not depend on the device.
-AttentionPlan plan_attention(const AttentionArgs& a, int max_splits);
-size_t attention_part_bytes(const AttentionArgs& a, int splits);
+// By sizes and the workspace's bytes alone, so that results do not depend on the device.
+AttentionPlan plan_attention(const AttentionArgs& a, size_t workspace);
+size_t attention_workspace(const AttentionArgs& a, const AttentionPlan& p);
+// Fill in the plan and the workspace's parts.
+void attention_use(AttentionArgs* a, const AttentionPlan& p, void* workspace);
 hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& p, DType dt,
                             hipStream_t st);
 

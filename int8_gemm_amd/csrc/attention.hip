@@ -28,6 +28,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileKeys = 64;   // keys of a copied tile
+constexpr int kRowsOfTile = 128;
 constexpr int kMaxSplits = 512;  // two rounds of a block per compute unit
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -117,6 +118,11 @@ __device__ bool find(const AttentionArgs& a, int64_t slot, Where* w) {
     *w = sequence(a, b);
     w->tile = (int)(slot - (int64_t)b * tiles);
     return true;
+  }
+  if (a.batch == 1) {  // no counting
+    *w = sequence(a, 0);
+    w->tile = (int)slot;
+    return slot * ROWS < (int64_t)w->lq * group;
   }
   const int lane = threadIdx.x & 63;
   int64_t before = 0;
@@ -235,7 +241,7 @@ __device__ __forceinline__ void add_nonfinite(const AttentionArgs& a, int64_t ke
 }
 
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, uint32_t slots,
+__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(AttentionArgs a, uint32_t slots,
                                                                uint32_t xcds) {
   using T = Kernel<DP, QT, NW, F16>;
   extern __shared__ __align__(1024) uint8_t lds[];
@@ -248,19 +254,33 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
 
   // blocks of an XCD (they are dealt in turn) take neighbouring tiles of the same
   // heads, whose keys then meet in its L2
-  uint32_t id = blockIdx.x;
+  // the first a.whole tiles are a block's each, the last ones are split
+  const bool tail = blockIdx.x >= a.whole;
+  uint32_t id = tail ? blockIdx.x - a.whole : blockIdx.x;
   {
-    const uint32_t total = gridDim.x, full = total / xcds, rest = total % xcds;
+    const uint32_t total = tail ? gridDim.x - a.whole : a.whole;
+    const uint32_t full = total / xcds, rest = total % xcds;
     const uint32_t x = id % xcds, i = id / xcds;
     id = x * full + min(x, rest) + i;
   }
-  const int split = (int)(id % (uint32_t)a.splits);
-  id /= (uint32_t)a.splits;
+  const int splits = tail ? a.splits : 1;
+  const int split = tail ? (int)(id % (uint32_t)splits) : 0;
+  const uint32_t piece = id;  // of the tail
+  if (tail) id = a.whole + id / (uint32_t)splits;
   uint32_t slot = id % slots;
   const int hk = (int)(id / slots);
-  Where w;
   if (CAUSAL) slot = slots - 1 - slot;  // long tiles first
-  if (!find<T::kRows>(a, slot, &w)) return;
+  Where w;
+  const bool found = find<T::kRows>(a, slot, &w);
+  if (tail && split == 0 && threadIdx.x < T::kRows) {
+    // which row of the output each of the tile's is
+    const int64_t r = (int64_t)w.tile * T::kRows + threadIdx.x;
+    int64_t to = -1;
+    if (found && r < (int64_t)w.lq * group)
+      to = (w.q0 + r / group) * a.q_heads + hk * group + r % group;
+    a.part_map[(int64_t)(id - a.whole) * T::kRows + threadIdx.x] = to;
+  }
+  if (!found) return;
 
   const int rows = w.lq * group;  // < 2^31 checked
   const int row0 = w.tile * T::kRows;
@@ -274,8 +294,8 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
   }
   int tiles = (end + kTileKeys - 1) / kTileKeys;
   int t0 = 0;
-  if (a.splits > 1) {
-    const int per = (tiles + a.splits - 1) / a.splits;
+  if (splits > 1) {
+    const int per = (tiles + splits - 1) / splits;
     t0 = min(tiles, split * per);
     tiles = min(tiles, t0 + per);
   }
@@ -452,9 +472,8 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
     const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
     const float lse2 = sum > 0.f || sum != sum ? log2f(sum) - kLift<F16> - below[q][0] * c : -__builtin_inff();
     if (row[q] >= rows) continue;
-    const int token = row[q] / group, head = hk * group + row[q] % group;
-    if (a.splits > 1) {
-      const int64_t at = ((int64_t)split * a.q_tokens + w.q0 + token) * a.q_heads + head;
+    if (tail) {
+      const int64_t at = (int64_t)piece * T::kRows + row[q] - row0;
       if (half == 0) a.part_lse[at] = lse2;
       if (lse2 == -__builtin_inff()) continue;
       float* to = a.part + at * a.d;
@@ -463,22 +482,34 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_kernel(AttentionArgs a, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = d * 32 + i * 8 + half * 4;
-              const v4f f = {o[q][d][4 * i] * inv, o[q][d][4 * i + 1] * inv, o[q][d][4 * i + 2] * inv,
+          const v4f f = {o[q][d][4 * i] * inv, o[q][d][4 * i + 1] * inv, o[q][d][4 * i + 2] * inv,
                          o[q][d][4 * i + 3] * inv};
           if (e < a.d) *reinterpret_cast<v4f*>(to + e) = f;
         }
       continue;
     }
+    const int token = row[q] / group, head = hk * group + row[q] % group;
     if (a.lse && half == 0) a.lse[(int64_t)head * a.q_tokens + w.q0 + token] = lse2 * kLn2;
     uint16_t* to = a.out + (w.q0 + token) * a.out_stride + head * a.out_head_stride;
+    // the two lanes of a row hold four elements of each eight: they swap, so that each
+    // has every other eight
 #pragma unroll
     for (int d = 0; d < T::kDTiles; ++d)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = d * 32 + i * 8 + half * 4;
-        const u2 f = {pack16x2<F16>(o[q][d][4 * i] * inv, o[q][d][4 * i + 1] * inv),
-                      pack16x2<F16>(o[q][d][4 * i + 2] * inv, o[q][d][4 * i + 3] * inv)};
-        if (e < a.d) *reinterpret_cast<u2*>(to + e) = f;
+      for (int i = 0; i < 4; i += 2) {
+        u4 f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+          const int n = 4 * i + 2 * j;
+          const u2v x = __builtin_amdgcn_permlane32_swap(
+              pack16x2<F16>(o[q][d][n] * inv, o[q][d][n + 1] * inv),
+              pack16x2<F16>(o[q][d][n + 4] * inv, o[q][d][n + 5] * inv), false, false);
+          f[j] = x.x;
+          f[2 + j] = x.y;
+        }
+        const int e = d * 32 + (i + half) * 8;
+        if (e < a.d) *reinterpret_cast<u4*>(to + e) = f;
       }
   }
 }
@@ -735,11 +766,18 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
   __shared__ float factor[kMaxSplits];
   __shared__ float red[2][kJoinThreads / 64];
   __shared__ __align__(16) float acc[kJoinThreads * 4];
-  const int64_t r = blockIdx.x;
-  const int64_t all = a.q_tokens * a.q_heads;
+  // few rows: parts [split][row of the output]; tiles: [tile][split][row of the tile]
+  int64_t r = blockIdx.x, at = r, step = a.q_tokens * a.q_heads;
+  if (a.part_map) {
+    step = kRowsOfTile;
+    at = r / step * step * a.splits + r % step;
+    r = a.part_map[r];
+    if (r < 0) return;
+  }
   const int64_t token = r / a.q_heads;
   const int head = (int)(r % a.q_heads);
-  if (a.q_offsets && (token < a.q_offsets[0] || token >= a.q_offsets[a.batch])) return;
+  if (!a.part_map && a.q_offsets && (token < a.q_offsets[0] || token >= a.q_offsets[a.batch]))
+    return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int group = tid / lanes, groups = kJoinThreads / lanes, e = tid % lanes * 4;
 
@@ -748,7 +786,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
 #pragma unroll
   for (int i = 0; i < kMaxSplits / kJoinThreads; ++i) {
     const int s = tid + i * kJoinThreads;
-    x[i] = s < a.splits ? a.part_lse[s * all + r] : -__builtin_inff();
+    x[i] = s < a.splits ? a.part_lse[at + s * step] : -__builtin_inff();
     top = fmaxf(top, x[i]);
   }
 #pragma unroll
@@ -774,11 +812,11 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
 
   v4f v = {0.f, 0.f, 0.f, 0.f};
   if (e < a.d) {
-    const float* from = a.part + r * a.d + e;
+    const float* from = a.part + at * a.d + e;
 #pragma unroll 8
     for (int s = group; s < a.splits; s += groups) {
       const float f = factor[s];
-      const v4f p = *reinterpret_cast<const v4f*>(from + (int64_t)s * all * a.d);
+      const v4f p = *reinterpret_cast<const v4f*>(from + s * step * a.d);
 #pragma unroll
       for (int q = 0; q < 4; ++q)  // what a split that saw nothing holds is not its result
         v[q] = f != 0.f ? __builtin_fmaf(f, p[q], v[q]) : v[q];
@@ -846,25 +884,28 @@ hipError_t launch_dtype(const AttentionArgs& a, const AttentionPlan& p, hipStrea
   if (e != hipSuccess || a.splits == 1) return e;
   int lanes = 1;
   while (lanes * 4 < a.d) lanes *= 2;
-  attention_join_kernel<F16>
-      <<<dim3((uint32_t)(a.q_tokens * a.q_heads)), dim3(kJoinThreads), 0, st>>>(a, lanes);
+  attention_join_kernel<F16><<<dim3((uint32_t)p.part_rows), dim3(kJoinThreads), 0, st>>>(a, lanes);
   return hipGetLastError();
+}
+
+size_t workspace_bytes(const AttentionPlan& p, int d) {
+  if (p.splits <= 1) return 0;
+  return (size_t)p.part_rows * ((size_t)p.splits * (d + 1) * 4 + (p.rows == 32 ? 0 : 8));
 }
 
 }  // namespace
 
-AttentionPlan plan_attention(const AttentionArgs& a, int max_splits) {
+AttentionPlan plan_attention(const AttentionArgs& a, size_t workspace) {
   AttentionPlan p;
   const int64_t group = a.q_heads / a.k_heads;
   const int64_t rows = a.q_tokens * group;  // of a key head
   const int64_t keys = a.k_tokens / a.batch;
-  p.rows = rows <= 32 * (int64_t)a.batch ? 32 : 128;
+  p.rows = rows <= 32 * (int64_t)a.batch ? 32 : kRowsOfTile;
   if (a.q_offsets)
     p.slots = (rows + p.rows - 1) / p.rows + a.batch;
   else
     p.slots = a.batch * ((rows / a.batch + p.rows - 1) / p.rows);
   const int64_t blocks = p.slots * a.k_heads;
-  int64_t splits = 1;
   if (p.rows == 32) {
     // sequences may use less of their keys than there is room for: splits of a fixed
     // length, about two rounds of a block per compute unit if all is used
@@ -873,26 +914,65 @@ AttentionPlan plan_attention(const AttentionArgs& a, int max_splits) {
     tiles = (tiles > a.batch ? tiles : a.batch) * a.k_heads;
     int64_t chunk = (units * tiles + kMaxSplits - 1) / kMaxSplits;
     if (chunk < 8) chunk = 8;
-    splits = (units + chunk - 1) / chunk;
-    if (splits > max_splits) splits = max_splits;
+    int64_t splits = (units + chunk - 1) / chunk;
     if (splits > kMaxSplits) splits = kMaxSplits;
-    if (splits < 1) splits = 1;
-    p.chunk = (int)((units + splits - 1) / splits);
-  } else {
-    // fewer tiles than the card has compute units: split the keys
-    const int64_t tiles = (keys + kTileKeys - 1) / kTileKeys;
-    splits = blocks ? kMaxSplits / blocks : 1;
-    if (splits > tiles / 4) splits = tiles / 4;
-    if (splits > max_splits) splits = max_splits;
+    p.part_rows = a.q_tokens * a.q_heads;
+    p.splits = splits < 1 ? 1 : (int)splits;
+    while (workspace_bytes(p, a.d) > workspace) --p.splits;
+    if (p.splits == 1) p.part_rows = 0;
+    p.chunk = (int)((units + p.splits - 1) / p.splits);
+    p.grid = blocks * p.splits;
+    return p;
   }
-  p.splits = splits < 1 ? 1 : (int)splits;
-  p.grid = blocks * p.splits;
+  // Blocks run `room` at a time. The tiles behind the last whole round (all, if there
+  // are not that many) are split over their keys into as many parts as cost least:
+  // rounds of the parts, each with its start and end (about 2.5 key tiles' time), and
+  // the join. In a round of at most half its blocks these have a compute unit to
+  // themselves and take 0.62 of the time. Causal tiles come longest first and even
+  // out by themselves if there is more than one round.
+  const int64_t room = a.d > 128 ? kMaxSplits / 2 : kMaxSplits;
+  const int64_t tiles = (keys + kTileKeys - 1) / kTileKeys;
+  const int64_t whole = blocks / room * room, rest = blocks - whole;
+  p.whole = blocks;
+  p.grid = blocks;
+  if (rest == 0 || (a.causal && whole > 0)) return p;
+  double least = 0;
+  auto consider = [&](int64_t n) {
+    if (n > tiles / 4) n = tiles / 4;
+    if (n < 1) return;
+    AttentionPlan t = p;
+    t.whole = whole;
+    t.splits = (int)n;
+    t.part_rows = rest * p.rows;
+    t.grid = whole + rest * n;
+    const int64_t full = rest * n / room, last = rest * n % room;
+    const double rounds = full + (last == 0 ? 0 : 2 * last <= room ? 0.62 : 1.0);
+    const double cost = rounds * (1.0 / n + 2.5 / tiles) + (n > 1 ? 5.0 / tiles : 0);
+    if (least != 0 && (cost >= least || workspace_bytes(t, a.d) > workspace)) return;
+    least = cost;
+    if (n > 1) p = t;
+  };
+  for (int64_t n = 1; n <= 8; ++n) consider(n);
+  // half a round, one, two
+  for (int64_t of = room / 2; of <= 2 * room; of *= 2) consider(of / rest);
   return p;
 }
 
-size_t attention_part_bytes(const AttentionArgs& a, int splits) {
-  if (splits <= 1) return 0;
-  return (size_t)splits * (size_t)(a.q_tokens * a.q_heads) * (size_t)(a.d + 1) * 4;
+size_t attention_workspace(const AttentionArgs& a, const AttentionPlan& p) {
+  return workspace_bytes(p, a.d);
+}
+
+void attention_use(AttentionArgs* a, const AttentionPlan& p, void* workspace) {
+  a->splits = p.splits;
+  a->whole = (uint32_t)p.whole;
+  if (p.splits == 1) return;
+  char* at = static_cast<char*>(workspace);
+  if (p.rows != 32) {
+    a->part_map = reinterpret_cast<int64_t*>(at);
+    at += p.part_rows * 8;
+  }
+  a->part = reinterpret_cast<float*>(at);
+  a->part_lse = a->part + (size_t)p.splits * (size_t)p.part_rows * a->d;
 }
 
 hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& p, DType dt,
