@@ -56,6 +56,7 @@ struct AttentionArgs {
   int batch, q_heads, k_heads, d;
   bool causal;
   float scale;
+  int group, q_each, k_each;  // query heads of a key head; tokens of equal sequences
   // splits > 1: the tiles from `whole` on (few rows: all) go by parts, each split's
   // normalised rows and their log2 sums, joined by a second launch
   int splits;
@@ -77,7 +78,7 @@ struct AttentionPlan {
 // By sizes and the workspace's bytes alone, so that results do not depend on the device.
 AttentionPlan plan_attention(const AttentionArgs& a, size_t workspace);
 size_t attention_workspace(const AttentionArgs& a, const AttentionPlan& p);
-// Fill in the plan and the workspace's parts.
+// Fill in the plan, the workspace's parts and what the kernels need of the sizes.
 void attention_use(AttentionArgs* a, const AttentionPlan& p, void* workspace);
 hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& p, DType dt,
                             hipStream_t st);

@@ -71,81 +71,70 @@ __device__ __forceinline__ float other_half(float v) {
 
 // Where a block works: a sequence's rows and keys.
 struct Where {
-  int64_t q0, k0;  // first query and key
+  int q0, k0;  // first query and key
   int lq, lk;
-  int tile;        // tile of the sequence's rows
+  int tile;    // tile of the sequence's rows
 };
-
-__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) {
-  return v < lo ? lo : v > hi ? hi : v;
-}
 
 // Sequence b of the call. Offsets are held inside the tensors whatever they are.
 __device__ __forceinline__ Where sequence(const AttentionArgs& a, int b) {
   Where w;
-  int64_t q1, k1;
+  int q1, k1;
   if (a.q_offsets) {
-    w.q0 = clamp64(a.q_offsets[b], 0, a.q_tokens);
-    q1 = clamp64(a.q_offsets[b + 1], w.q0, a.q_tokens);
+    w.q0 = min(max(a.q_offsets[b], 0), (int)a.q_tokens);
+    q1 = min(max(a.q_offsets[b + 1], w.q0), (int)a.q_tokens);
   } else {
-    const int64_t n = a.q_tokens / a.batch;
-    w.q0 = b * n;
-    q1 = w.q0 + n;
+    w.q0 = b * a.q_each;
+    q1 = w.q0 + a.q_each;
   }
   if (a.k_offsets) {
-    w.k0 = clamp64(a.k_offsets[b], 0, a.k_tokens);
-    k1 = clamp64(a.k_offsets[b + 1], w.k0, a.k_tokens);
+    w.k0 = min(max(a.k_offsets[b], 0), (int)a.k_tokens);
+    k1 = min(max(a.k_offsets[b + 1], w.k0), (int)a.k_tokens);
   } else {
-    const int64_t n = a.k_tokens / a.batch;
-    w.k0 = b * n;
-    k1 = w.k0 + n;
+    w.k0 = b * a.k_each;
+    k1 = w.k0 + a.k_each;
   }
-  w.lq = (int)(q1 - w.q0);
-  w.lk = (int)(k1 - w.k0);
-  if (a.k_lens) w.lk = (int)clamp64(a.k_lens[b], 0, w.lk);
+  w.lq = q1 - w.q0;
+  w.lk = k1 - w.k0;
+  if (a.k_lens) w.lk = min(max(a.k_lens[b], 0), w.lk);
   return w;
 }
 
-// The sequence and tile of a slot: tiles of `rows` rows counted through the
-// sequences, 64 of them at a time. False behind the last.
+// The sequence and tile of a slot: tiles of ROWS rows counted through the
+// sequences, 64 of them at a time. False behind the last. A slot is below 2^23
+// (a grid's blocks), rows (query, head of the group) of all sequences below 2^31.
 template <int ROWS>
-__device__ bool find(const AttentionArgs& a, int64_t slot, Where* w) {
-  const int group = a.q_heads / a.k_heads;
-  if (!a.q_offsets) {
-    const int tiles = (int)((a.q_tokens / a.batch * group + ROWS - 1) / ROWS);
-    const int b = (int)(slot / max(tiles, 1));
-    if (b >= a.batch || tiles == 0) return false;
+__device__ bool find(const AttentionArgs& a, uint32_t slot, Where* w) {
+  if (!a.q_offsets || a.batch == 1) {  // no counting
+    const uint32_t tiles = (uint32_t)(a.q_each * a.group + ROWS - 1) / ROWS;
+    const uint32_t b = a.batch == 1 ? 0 : slot / max(tiles, 1u);
+    if (b >= (uint32_t)a.batch) return false;
     *w = sequence(a, b);
-    w->tile = (int)(slot - (int64_t)b * tiles);
-    return true;
-  }
-  if (a.batch == 1) {  // no counting
-    *w = sequence(a, 0);
-    w->tile = (int)slot;
-    return slot * ROWS < (int64_t)w->lq * group;
+    w->tile = (int)(slot - b * tiles);
+    return w->tile * ROWS < w->lq * a.group;
   }
   const int lane = threadIdx.x & 63;
-  int64_t before = 0;
+  uint32_t before = 0;
   for (int base = 0; base < a.batch; base += 64) {
     const int b = base + lane;
-    int tiles = 0;
+    uint32_t upto = 0;
     if (b < a.batch) {
-      const int64_t lo = clamp64(a.q_offsets[b], 0, a.q_tokens);
-      const int64_t hi = clamp64(a.q_offsets[b + 1], lo, a.q_tokens);
-      tiles = (int)(((hi - lo) * group + ROWS - 1) / ROWS);  // < 2^26
+      const int lo = min(max(a.q_offsets[b], 0), (int)a.q_tokens);
+      const int hi = min(max(a.q_offsets[b + 1], lo), (int)a.q_tokens);
+      upto = (uint32_t)((hi - lo) * a.group + ROWS - 1) / ROWS;  // < 2^26: 64 of them < 2^32
     }
-    int upto = min(tiles, 1 << 24);
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
-      const int below = __shfl_up(upto, s);
+      const uint32_t below = __shfl_up(upto, s);
       if (lane >= s) upto += below;
     }
-    const uint64_t past = __ballot(before + upto > slot);
+    // before <= slot here, so the difference is below 2^23
+    const uint64_t past = __ballot(upto > slot - before);
     if (past) {
       const int at = __builtin_ctzll(past);
-      const int first = at ? __builtin_amdgcn_readlane(upto, at - 1) : 0;
+      const uint32_t first = at ? __builtin_amdgcn_readlane(upto, at - 1) : 0;
       *w = sequence(a, base + at);
-      w->tile = (int)(slot - before) - first;
+      w->tile = (int)(slot - before - first);
       return true;
     }
     before += __builtin_amdgcn_readlane(upto, 63);
@@ -227,7 +216,7 @@ template <int DTILES, bool F16>
 __device__ __forceinline__ void add_nonfinite(const AttentionArgs& a, int64_t key, int hk,
                                               bool sees, v16f (&o)[DTILES]) {
   const int half = (threadIdx.x >> 5) & 1;
-  const uint16_t* vr = a.v + key * a.v_stride + hk * a.v_head_stride;
+  const uint16_t* vr = a.v + key * a.v_stride + (int64_t)hk * a.v_head_stride;
 #pragma unroll
   for (int d = 0; d < DTILES; ++d) {
     asm volatile("" ::: "memory");  // one tile's loads at a time
@@ -250,7 +239,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
-  const int group = a.q_heads / a.k_heads;
+  const int group = a.group;
 
   // blocks of an XCD (they are dealt in turn) take neighbouring tiles of the same
   // heads, whose keys then meet in its L2
@@ -274,10 +263,10 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
   const bool found = find<T::kRows>(a, slot, &w);
   if (tail && split == 0 && threadIdx.x < T::kRows) {
     // which row of the output each of the tile's is
-    const int64_t r = (int64_t)w.tile * T::kRows + threadIdx.x;
+    const int r = w.tile * T::kRows + (int)threadIdx.x;
     int64_t to = -1;
-    if (found && r < (int64_t)w.lq * group)
-      to = (w.q0 + r / group) * a.q_heads + hk * group + r % group;
+    if (found && r < w.lq * group)
+      to = (int64_t)(w.q0 + r / group) * a.q_heads + hk * group + r % group;
     a.part_map[(int64_t)(id - a.whole) * T::kRows + threadIdx.x] = to;
   }
   if (!found) return;
@@ -309,7 +298,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
     const int r = min(row[t], rows - 1);
     const int token = r / group, head = hk * group + r % group;
     seen[t] = CAUSAL ? min(w.lk, token + shift) : w.lk;
-    const uint16_t* q = a.q + (w.q0 + token) * a.q_stride + head * a.q_head_stride;
+    const uint16_t* q = a.q + (int64_t)(w.q0 + token) * a.q_stride + (int64_t)head * a.q_head_stride;
 #pragma unroll
     for (int s = 0; s < T::kSteps; ++s) {
       const int c = 2 * s + half;
@@ -320,9 +309,9 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
 
   // copies: lane i of a copy fills the 16 bytes behind 16 i
   const int8_t* kbase =
-      reinterpret_cast<const int8_t*>(a.k + w.k0 * a.k_stride + hk * a.k_head_stride);
+      reinterpret_cast<const int8_t*>(a.k + (int64_t)w.k0 * a.k_stride + (int64_t)hk * a.k_head_stride);
   const int8_t* vbase =
-      reinterpret_cast<const int8_t*>(a.v + w.k0 * a.v_stride + hk * a.v_head_stride);
+      reinterpret_cast<const int8_t*>(a.v + (int64_t)w.k0 * a.v_stride + (int64_t)hk * a.v_head_stride);
   const uint32_t kstride = (uint32_t)a.k_stride * 2, vstride = (uint32_t)a.v_stride * 2;
   auto issue = [&](int t, int stage) {
     const int last = w.lk - 1 - t * kTileKeys;  // rows behind it repeat it
@@ -490,7 +479,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
     }
     const int token = row[q] / group, head = hk * group + row[q] % group;
     if (a.lse && half == 0) a.lse[(int64_t)head * a.q_tokens + w.q0 + token] = lse2 * kLn2;
-    uint16_t* to = a.out + (w.q0 + token) * a.out_stride + head * a.out_head_stride;
+    uint16_t* to = a.out + (int64_t)(w.q0 + token) * a.out_stride + (int64_t)head * a.out_head_stride;
     // the two lanes of a row hold four elements of each eight: they swap, so that each
     // has every other eight
 #pragma unroll
@@ -544,7 +533,7 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
-  const int group = a.q_heads / a.k_heads;
+  const int group = a.group;
   const uint32_t id = blockIdx.x;
   const int split = (int)(id % (uint32_t)a.splits);
   const uint32_t rest = id / (uint32_t)a.splits;
@@ -570,7 +559,7 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
   const int seen = a.causal ? min(w.lk, token + shift) : w.lk;
   u4 qf[kSteps];
   {
-    const uint16_t* q = a.q + (w.q0 + token) * a.q_stride + head * a.q_head_stride;
+    const uint16_t* q = a.q + (int64_t)(w.q0 + token) * a.q_stride + (int64_t)head * a.q_head_stride;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int e = (2 * s + half) * 8;
@@ -580,9 +569,9 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
   }
 
   const int8_t* kbase =
-      reinterpret_cast<const int8_t*>(a.k + w.k0 * a.k_stride + hk * a.k_head_stride);
+      reinterpret_cast<const int8_t*>(a.k + (int64_t)w.k0 * a.k_stride + (int64_t)hk * a.k_head_stride);
   const int8_t* vbase =
-      reinterpret_cast<const int8_t*>(a.v + w.k0 * a.v_stride + hk * a.v_head_stride);
+      reinterpret_cast<const int8_t*>(a.v + (int64_t)w.k0 * a.v_stride + (int64_t)hk * a.v_head_stride);
   const uint32_t kstride = (uint32_t)a.k_stride * 2, vstride = (uint32_t)a.v_stride * 2;
   const int ring = wave * T::kWaveBytes;
   auto issue = [&](int u, int stage) {
@@ -751,7 +740,7 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
     }
     if (a.lse && e == 0) a.lse[(int64_t)jhead * a.q_tokens + w.q0 + jtoken] = lse2 * kLn2;
     const u2 f = {pack16x2<F16>(acc[0], acc[1]), pack16x2<F16>(acc[2], acc[3])};
-    *reinterpret_cast<u2*>(a.out + (w.q0 + jtoken) * a.out_stride + jhead * a.out_head_stride + e) =
+    *reinterpret_cast<u2*>(a.out + (int64_t)(w.q0 + jtoken) * a.out_stride + (int64_t)jhead * a.out_head_stride + e) =
         f;
   }
 }
@@ -835,7 +824,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
     }
     const float inv = none ? 0.f : 1.0f / sum;
     const u2 f = {pack16x2<F16>(v[0] * inv, v[1] * inv), pack16x2<F16>(v[2] * inv, v[3] * inv)};
-    *reinterpret_cast<u2*>(a.out + token * a.out_stride + head * a.out_head_stride + e) = f;
+    *reinterpret_cast<u2*>(a.out + token * a.out_stride + (int64_t)head * a.out_head_stride + e) = f;
   }
 }
 
@@ -963,6 +952,9 @@ size_t attention_workspace(const AttentionArgs& a, const AttentionPlan& p) {
 }
 
 void attention_use(AttentionArgs* a, const AttentionPlan& p, void* workspace) {
+  a->group = a->q_heads / a->k_heads;
+  a->q_each = (int)(a->q_tokens / a->batch);
+  a->k_each = (int)(a->k_tokens / a->batch);
   a->splits = p.splits;
   a->whole = (uint32_t)p.whole;
   if (p.splits == 1) return;
