@@ -9,9 +9,10 @@
 // over a head, or over all heads of a token, then (a, b) -> (a cos - b sin,
 // b cos + a sin) per pair; fp32 between the 16-bit ends. Bound by memory: q and
 // k are read once and written once. A lane holds two chunks of eight elements
-// of a head so placed that both elements of a pair are its own: chunks 2 t and
-// 2 t + 1 for pairs (2 i, 2 i + 1), chunks t and t + pairs / 8 for pairs
-// (i, i + pairs).
+// of a head so placed that both elements of a pair are its own and neighbouring
+// lanes read neighbouring chunks, of up to five heads of a token at once: that many
+// loads are under way before the first sum, and its cos and sin serve them all. Values
+// stay packed; each pass over them unpacks anew.
 
 #include "attention.h"
 #include "mx4.h"
@@ -56,52 +57,61 @@ __global__ __launch_bounds__(kTableThreads) void rope_table_kernel(RopeTableArgs
 // ---- norms and rotation ----------------------------------------------------
 
 constexpr int kHeadThreads = 256;
+constexpr int kMaxRowWaves = 8;
+constexpr int kMaxHeadsOfLane = 5;
 
-// A lane's place in a head: its chunks, and the pairs behind its entries.
+// A lane's place in a head of `chunks` chunks, and the pairs behind its entries.
 template <bool HALVES>
 struct Place {
-  int c0, c1;        // chunks of 8 elements
-  bool in0, in1;     // ... inside the head
-  bool turn0, turn1; // ... rotated
+  int c0, c1;         // chunks of 8 elements
+  bool in0, in1;      // ... inside the head
+  bool turn0, turn1;  // ... rotated
+  int p0, p1;         // first of the four pairs of (HALVES: either half of) them
   __device__ Place(int t, int d, int pairs) {
-    const int chunks = d / 8, p8 = pairs / 8;
+    const int chunks = d / 8;
     if (HALVES) {
+      const int p8 = pairs / 8;
       const bool turned = t < p8;
       c0 = turned ? t : 2 * p8 + 2 * (t - p8);
       c1 = turned ? t + p8 : c0 + 1;
       turn0 = turn1 = turned;
+      p0 = 8 * t;
+      p1 = p0 + 4;
     } else {
-      c0 = 2 * t;
-      c1 = c0 + 1;
-      turn0 = c0 * 4 < pairs;
-      turn1 = c1 * 4 < pairs;
+      c0 = t;
+      c1 = t + (chunks + 1) / 2;
+      p0 = 4 * c0;
+      p1 = 4 * c1;
+      turn0 = p0 < pairs;
+      turn1 = p1 < pairs;
+      if (t >= (chunks + 1) / 2) c0 = chunks;  // a lane without a chunk
     }
     in0 = c0 < chunks;
     in1 = c1 < chunks;
+    turn0 &= in0;
+    turn1 &= in1;
   }
 };
 
 // The lane's 8 (cos, sin), (1, 0) where it turns nothing.
 template <bool HALVES>
-__device__ __forceinline__ void load_turns(const HeadsArgs& a, const Place<HALVES>& pl, int t,
+__device__ __forceinline__ void load_turns(const HeadsArgs& a, const Place<HALVES>& pl,
                                            int64_t token, float (&cs)[8], float (&sn)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
   if (!a.table) return;
-  const int64_t row = a.table_rows == a.tokens ? token : token % a.table_rows;
-  const float4* from = reinterpret_cast<const float4*>(a.table + row * a.pairs * 2 + t * 16);
-  if (pl.turn0) {
+  const uint32_t row =
+      a.table_rows == a.tokens ? (uint32_t)token : (uint32_t)token % (uint32_t)a.table_rows;
+  const float* from = a.table + (int64_t)row * a.pairs * 2;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if (!(half ? pl.turn1 : pl.turn0)) continue;
+    const float4* f = reinterpret_cast<const float4*>(from + (half ? pl.p1 : pl.p0) * 2);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 f = from[i];
-      cs[2 * i] = f.x, sn[2 * i] = f.y, cs[2 * i + 1] = f.z, sn[2 * i + 1] = f.w;
-    }
-  }
-  if (pl.turn1) {
-#pragma unroll
-    for (int i = 2; i < 4; ++i) {
-      const float4 f = from[i];
-      cs[2 * i] = f.x, sn[2 * i] = f.y, cs[2 * i + 1] = f.z, sn[2 * i + 1] = f.w;
+      const int at = 4 * half + 2 * i;
+      const float4 v = f[i];
+      cs[at] = v.x, sn[at] = v.y, cs[at + 1] = v.z, sn[at + 1] = v.w;
     }
   }
 }
@@ -125,8 +135,8 @@ __device__ __forceinline__ u4 pack8(const float (&f)[8]) {
               pack16x2<F16>(f[6], f[7])};
 }
 
-// Sum over a head's lanes (SHIFT bits), or over all of a row's: `waves` waves of
-// the block with one slot each in `part`, or 2^shift lanes of one wave.
+// A norm's span: 2^shift lanes of a wave, or `waves` waves of the block, one slot
+// each in `part`.
 struct Span {
   int shift, waves;
 };
@@ -155,198 +165,190 @@ __device__ __forceinline__ uint32_t span_max(uint32_t v, const Span& sp, float* 
   for (int w = 1; w < sp.waves; ++w) m = max(m, __float_as_uint(part[w]));
   return m;
 }
+constexpr int kPartSlots = 5 * kMaxRowWaves;
 
-constexpr int kMaxSpanWaves = 16;
-constexpr int kPartSlots = 6 * kMaxSpanWaves;
+// What a norm does to its span: v = (x 2^-by - mean) r.
+struct Norm {
+  float mean, r;
+  int by;
+};
 
-// Normalise the span's values; absent chunks hold 0 in xw. Squares leave fp32's
-// range where bf16 values do not, so a span whose mean square is not in
-// [2^-100, inf) is taken again with a power of two out of it and of eps, exactly
-// (spans that share a wave repeat theirs with 2^0, to the same bits).
-template <int NI, bool F16>
-__device__ __forceinline__ void normalise(float (&v)[NI][2][8], const u4 (&xw)[NI][2],
-                                          const bool (&in)[NI][2], NormKind kind, float count,
-                                          float eps, const Span& sp, float* part) {
-  if (kind == NormKind::kNone) return;
+// Of N heads' packed values (absent chunks hold 0). Squares leave fp32's range where
+// bf16 values do not, so a span whose mean square is not in [2^-100, inf) is taken
+// again with a power of two out of it and of eps, exactly (`scaled` is set for the
+// wave; spans that share it repeat theirs with 2^0, to the same bits).
+template <int N, bool F16>
+__device__ __forceinline__ Norm norm_of(u4 (*xw)[2], const bool (*in)[2], NormKind kind,
+                                        float count, float eps, const Span& sp, float* part,
+                                        bool* scaled) {
+  Norm n = {0.f, 1.f, 0};
+  if (kind == NormKind::kNone) return n;
   const bool layer = kind == NormKind::kLayer;
-  auto each = [&](auto f) {
+  // f over the values, chunk by chunk
+  auto sum_of = [&](auto f) {
+    float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f(v[i][j][e]);
-  };
-  auto squares = [&] {
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float c = 0.f;
+        float v[8], c = 0.f;
+        mx4_unpack8<F16>(xw[i][j], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c = __builtin_fmaf(v[i][j][e], v[i][j][e], c);
-        q += in[i][j] ? c : 0.f;
+        for (int e = 0; e < 8; ++e) c = f(v[e], c);
+        s += in[i][j] ? c : 0.f;
+        // the next pass unpacks again: unpacked values are not held over
+        asm volatile("" : "+v"(xw[i][j]));
       }
-    return q;
+    return s;
   };
-  if (layer) {
-    float s = 0.f;
-    each([&](float& x) { s += x; });
-    const float mean = span_sum(s, sp, part) / count;
-    each([&](float& x) { x -= mean; });
-  }
-  float ms = span_sum(squares(), sp, part + kMaxSpanWaves) / count + eps;
+  if (layer)
+    n.mean = span_sum(sum_of([](float x, float c) { return c + x; }), sp, part) / count;
+  const float mean = n.mean;
+  float q = layer ? sum_of([=](float x, float c) {
+    return __builtin_fmaf(x - mean, x - mean, c);
+  })
+                  : sum_of([](float x, float c) { return __builtin_fmaf(x, x, c); });
+  float ms = span_sum(q, sp, part + kMaxRowWaves) / count + eps;
   const bool again = !(ms >= 0x1p-100f && ms < __builtin_inff());
   if (__builtin_expect(__any(again), 0)) {
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) mx4_unpack8<F16>(xw[i][j], v[i][j]);
-    each([&](float& x) { top = max(top, __float_as_uint(x) & 0x7FFFFFFFu); });
-    top = span_max(top, sp, part + 2 * kMaxSpanWaves) >> 23;
+      for (int j = 0; j < 2; ++j) {
+        float v[8];
+        mx4_unpack8<F16>(xw[i][j], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+      }
+    top = span_max(top, sp, part + 2 * kMaxRowWaves) >> 23;
     int by = max((int)top - 127, ((int)(__float_as_uint(eps) >> 23) - 127) >> 1) - 40;
     if (!again || top == 255) by = 0;  // an infinity or a NaN gives what it gave
-    each([&](float& x) { x = __builtin_ldexpf(x, -by); });
-    if (layer) {
-      float s = 0.f;
-      each([&](float& x) { s += x; });
-      const float mean = span_sum(s, sp, part + 3 * kMaxSpanWaves) / count;
-      each([&](float& x) { x -= mean; });
-    }
-    ms = span_sum(squares(), sp, part + 4 * kMaxSpanWaves) / count + __builtin_ldexpf(eps, -2 * by);
+    if (layer)
+      n.mean = span_sum(sum_of([=](float x, float c) { return c + __builtin_ldexpf(x, -by); }),
+                        sp, part + 3 * kMaxRowWaves) /
+               count;
+    const float m = n.mean;
+    q = sum_of([=](float x, float c) {
+      const float v = __builtin_ldexpf(x, -by) - m;
+      return __builtin_fmaf(v, v, c);
+    });
+    ms = span_sum(q, sp, part + 4 * kMaxRowWaves) / count + __builtin_ldexpf(eps, -2 * by);
+    n.by = by;
+    *scaled = true;
   }
-  const float r = 1.0f / sqrtf(ms);
-  each([&](float& x) { x *= r; });
+  n.r = 1.0f / sqrtf(ms);
+  return n;
 }
 
-template <bool F16>
-__device__ __forceinline__ void weigh(float (&v)[2][8], const uint16_t* w, int c0, int c1,
-                                      bool in0, bool in1) {
-  float f[8];
-  if (in0) {
-    mx4_unpack8<F16>(*reinterpret_cast<const u4*>(w + c0 * 8), f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[0][e] *= f[e];
-  }
-  if (in1) {
-    mx4_unpack8<F16>(*reinterpret_cast<const u4*>(w + c1 * 8), f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[1][e] *= f[e];
-  }
-}
-
-// How the heads of one tensor lie on blocks: 2^lanes_shift lanes a head, then
-// per-head norms: 2^slot_shift heads of a token at once, in steps over the rest.
+// How the heads of one tensor lie on lanes: 2^lanes_shift lanes a head. A unit is a
+// token's heads, or NI per lane group of them for norms of single heads: 2^shift lanes
+// of a wave, or a block's `waves`.
 struct HeadsShape {
   int lanes_shift;
-  int slot_shift[2];
-  uint32_t blocks[2];
-  int waves;  // row norms: waves of a row (blocks of one row), or 0: 2^row_shift lanes
-  int row_shift[2];
+  struct {
+    int shift, segments;
+    uint32_t blocks;
+  } t[2];
+  int waves;
 };
 
-// Norms of single heads.
-template <bool F16, bool HALVES>
-__global__ __launch_bounds__(kHeadThreads) void heads_kernel(HeadsArgs a, HeadsShape sh) {
-  const bool second = blockIdx.x >= sh.blocks[0];
-  const HeadsTensor& x = a.t[second];
-  const uint32_t block = blockIdx.x - (second ? sh.blocks[0] : 0);
-  const int slot_shift = sh.slot_shift[second];
-  const int t = threadIdx.x & ((1 << sh.lanes_shift) - 1);
-  const int g = threadIdx.x >> sh.lanes_shift;
-  const int slot = g & ((1 << slot_shift) - 1);
-  const int per_block = kHeadThreads >> (sh.lanes_shift + slot_shift);
-  const int64_t at = (int64_t)block * per_block + (g >> slot_shift);
-  const bool live = at < a.tokens;
-  const int64_t token = live ? at : a.tokens - 1;
-  const Place<HALVES> pl(t, a.d, a.pairs);
-  float cs[8], sn[8];
-  load_turns<HALVES>(a, pl, t, token, cs, sn);
-  const u4 zero = {0, 0, 0, 0};
-  const uint16_t* in = x.in + token * x.in_stride;
-  uint16_t* out = x.out + token * x.out_stride;
-  const Span sp = {sh.lanes_shift, 1};
-  // every lane of a wave takes every step: sums are over lanes
-  for (int h0 = 0; h0 < x.heads; h0 += 1 << slot_shift) {
-    const int h = min(h0 + slot, x.heads - 1);
-    const bool write = live && h0 + slot < x.heads;
-    const uint16_t* p = in + h * x.in_head_stride;
-    u4 xw[1][2];
-    xw[0][0] = pl.in0 ? *reinterpret_cast<const u4*>(p + pl.c0 * 8) : zero;
-    xw[0][1] = pl.in1 ? *reinterpret_cast<const u4*>(p + pl.c1 * 8) : zero;
-    const bool inside[1][2] = {{pl.in0, pl.in1}};
-    float v[1][2][8];
-    mx4_unpack8<F16>(xw[0][0], v[0][0]);
-    mx4_unpack8<F16>(xw[0][1], v[0][1]);
-    normalise<1, F16>(v, xw, inside, a.norm, (float)a.d, a.eps, sp, nullptr);
-    if (x.weight) weigh<F16>(v[0], x.weight, pl.c0, pl.c1, pl.in0, pl.in1);
-    turn<HALVES>(v[0], cs, sn);
-    uint16_t* o = out + h * x.out_head_stride;
-    if (write && pl.in0) *reinterpret_cast<u4*>(o + pl.c0 * 8) = pack8<F16>(v[0][0]);
-    if (write && pl.in1) *reinterpret_cast<u4*>(o + pl.c1 * 8) = pack8<F16>(v[0][1]);
-  }
-}
-
-// Norms over all heads of a token: NI heads of the row a lane group.
-template <int NI, bool F16, bool HALVES>
-__global__ __launch_bounds__(64 * kMaxSpanWaves) void rows_kernel(HeadsArgs a, HeadsShape sh) {
+template <int NI, bool F16, bool HALVES, bool ROW>
+__global__ __launch_bounds__(ROW ? 64 * kMaxRowWaves : kHeadThreads) void heads_kernel(
+    HeadsArgs a, HeadsShape sh) {
   __shared__ float part[kPartSlots];
-  const bool second = blockIdx.x >= sh.blocks[0];
+  const bool second = blockIdx.x >= sh.t[0].blocks;
   const HeadsTensor& x = a.t[second];
-  const uint32_t block = blockIdx.x - (second ? sh.blocks[0] : 0);
-  const int t = threadIdx.x & ((1 << sh.lanes_shift) - 1);
-  int64_t at;
-  int group, groups;
+  const uint32_t block = blockIdx.x - (second ? sh.t[0].blocks : 0);
+  const int ls = sh.lanes_shift;
+  const int lane = threadIdx.x & ((1 << ls) - 1);
+  int64_t unit;
+  int g, groups;
   Span sp;
-  if (sh.waves) {
-    at = block;
-    group = threadIdx.x >> sh.lanes_shift;
-    groups = blockDim.x >> sh.lanes_shift;
+  if (ROW && sh.waves > 1) {
+    unit = block;
+    g = threadIdx.x >> ls;
+    groups = blockDim.x >> ls;
     sp = {6, sh.waves};
   } else {
-    const int shift = sh.row_shift[second];
-    at = (int64_t)block * (blockDim.x >> shift) + (threadIdx.x >> shift);
-    group = (threadIdx.x & ((1 << shift) - 1)) >> sh.lanes_shift;
-    groups = 1 << (shift - sh.lanes_shift);
-    sp = {shift, 1};
+    const int shift = sh.t[second].shift;
+    unit = (int64_t)block * (kHeadThreads >> shift) + (threadIdx.x >> shift);
+    g = (threadIdx.x & ((1 << shift) - 1)) >> ls;
+    groups = 1 << (shift - ls);
+    sp = {ROW ? shift : ls, 1};
   }
-  const bool live = at < a.tokens;
-  const int64_t token = live ? at : a.tokens - 1;
-  const Place<HALVES> pl(t, a.d, a.pairs);
+  int64_t token = unit;
+  int first = g;
+  if (!ROW && sh.t[second].segments > 1) {
+    const uint32_t n = sh.t[second].segments;  // units below 2^32
+    token = (uint32_t)unit / n;
+    first += (int)((uint32_t)unit - (uint32_t)token * n) * groups * NI;
+  }
+  const bool live = token < a.tokens;  // the others go along and write nothing
+  if (!live) token = a.tokens - 1;
+  const Place<HALVES> pl(lane, a.d, a.pairs);
   const u4 zero = {0, 0, 0, 0};
   u4 xw[NI][2];
-  bool inside[NI][2];
-  float v[NI][2][8];
-  int head[NI];
+  bool in[NI][2];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    head[i] = group + i * groups;
-    const bool in = head[i] < x.heads;
-    inside[i][0] = in && pl.in0;
-    inside[i][1] = in && pl.in1;
-    const uint16_t* p = x.in + token * x.in_stride + head[i] * x.in_head_stride;
-    xw[i][0] = inside[i][0] ? *reinterpret_cast<const u4*>(p + pl.c0 * 8) : zero;
-    xw[i][1] = inside[i][1] ? *reinterpret_cast<const u4*>(p + pl.c1 * 8) : zero;
+    const int head = first + i * groups;
+    const bool held = head < x.heads;
+    in[i][0] = held && pl.in0;
+    in[i][1] = held && pl.in1;
+    const uint16_t* p = x.in + token * x.in_stride + (int64_t)head * x.in_head_stride;
+    xw[i][0] = in[i][0] ? *reinterpret_cast<const u4*>(p + pl.c0 * 8) : zero;
+    xw[i][1] = in[i][1] ? *reinterpret_cast<const u4*>(p + pl.c1 * 8) : zero;
   }
   float cs[8], sn[8];
-  load_turns<HALVES>(a, pl, t, token, cs, sn);
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    mx4_unpack8<F16>(xw[i][0], v[i][0]);
-    mx4_unpack8<F16>(xw[i][1], v[i][1]);
+  load_turns<HALVES>(a, pl, token, cs, sn);
+  u4 ww[2] = {zero, zero};
+  if (!ROW && x.weight) {
+    if (pl.in0) ww[0] = *reinterpret_cast<const u4*>(x.weight + pl.c0 * 8);
+    if (pl.in1) ww[1] = *reinterpret_cast<const u4*>(x.weight + pl.c1 * 8);
   }
-  normalise<NI, F16>(v, xw, inside, a.norm, (float)(a.d * x.heads), a.eps, sp, part);
+  bool scaled = false;
+  Norm all;
+  if (ROW)
+    all = norm_of<NI, F16>(xw, in, a.norm, (float)(a.d * x.heads), a.eps, sp, part, &scaled);
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    if (x.weight)
-      weigh<F16>(v[i], x.weight + (int64_t)head[i] * a.d, pl.c0, pl.c1, inside[i][0],
-                 inside[i][1]);
-    turn<HALVES>(v[i], cs, sn);
-    uint16_t* o = x.out + token * x.out_stride + head[i] * x.out_head_stride;
-    if (live && inside[i][0]) *reinterpret_cast<u4*>(o + pl.c0 * 8) = pack8<F16>(v[i][0]);
-    if (live && inside[i][1]) *reinterpret_cast<u4*>(o + pl.c1 * 8) = pack8<F16>(v[i][1]);
+    const int head = first + i * groups;
+    if (ROW && x.weight) {
+      const uint16_t* w = x.weight + (int64_t)head * a.d;
+      if (in[i][0]) ww[0] = *reinterpret_cast<const u4*>(w + pl.c0 * 8);
+      if (in[i][1]) ww[1] = *reinterpret_cast<const u4*>(w + pl.c1 * 8);
+    }
+    const Norm n = ROW ? all
+                       : norm_of<1, F16>(&xw[i], &in[i], a.norm, (float)a.d, a.eps, sp, nullptr,
+                                         &scaled);
+    float v[2][8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      mx4_unpack8<F16>(xw[i][j], v[j]);
+      if (__builtin_expect(scaled, 0)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] = __builtin_ldexpf(v[j][e], -n.by);
+      }
+      if (a.norm != NormKind::kNone) {
+        if (a.norm == NormKind::kLayer) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[j][e] -= n.mean;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] *= n.r;
+      }
+      if (x.weight) {
+        float w[8];
+        mx4_unpack8<F16>(ww[j], w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
+      }
+    }
+    if (a.table) turn<HALVES>(v, cs, sn);
+    uint16_t* o = x.out + token * x.out_stride + (int64_t)head * x.out_head_stride;
+    if (live && in[i][0]) *reinterpret_cast<u4*>(o + pl.c0 * 8) = pack8<F16>(v[0]);
+    if (live && in[i][1]) *reinterpret_cast<u4*>(o + pl.c1 * 8) = pack8<F16>(v[1]);
   }
 }
 
@@ -359,53 +361,77 @@ int log2_up(int64_t n) {
 // lanes of a head: two chunks each
 int lanes_shift(int d) { return log2_up((d / 8 + 1) / 2); }
 
-HeadsShape shape(const HeadsArgs& a) {
-  HeadsShape sh = {};
-  sh.lanes_shift = lanes_shift(a.d);
-  for (int i = 0; i < 2; ++i) {
-    const HeadsTensor& x = a.t[i];
-    if (!x.heads) continue;
-    if (!a.row) {
-      const int most = log2_up(kHeadThreads) - sh.lanes_shift;
-      int s = log2_up(x.heads);
-      if (s > most) s = most;
-      sh.slot_shift[i] = s;
-      const int64_t per = kHeadThreads >> (sh.lanes_shift + s);
-      sh.blocks[i] = (uint32_t)((a.tokens + per - 1) / per);
+// Lanes of a unit that takes `heads` heads, ni per lane group: a power of two within a
+// wave, whole waves beyond.
+int64_t unit_lanes(int64_t heads, int ls, int ni) {
+  const int64_t lanes = ((heads + ni - 1) / ni) << ls;
+  return lanes <= 64 ? (int64_t)1 << log2_up(lanes) : (lanes + 63) / 64 * 64;
+}
+
+// Heads per lane group: as many loads under way as there are, unless lanes then lie idle
+// (32760 tokens x 40 heads of 128, norms over rows: one 347 us, five TODO us), or the
+// call has too few tokens to fill the card so.
+int heads_of_lane(const HeadsArgs& a, int ls) {
+  const int64_t most = a.t[0].heads > a.t[1].heads ? a.t[0].heads : a.t[1].heads;
+  int best = 1;
+  double held = 0;
+  for (int ni = 1; ni <= kMaxHeadsOfLane; ++ni) {
+    const int64_t lanes = unit_lanes(most, ls, ni);
+    if (ni > 1 && a.tokens * lanes < (int64_t)compute_units() * 1024) continue;
+    if (a.row && lanes > 64 * kMaxRowWaves) continue;
+    const double use = (double)(most << ls) / (double)(lanes * ni);
+    if (use >= held * 0.95) {
+      best = ni;
+      if (use > held) held = use;
     }
   }
-  if (a.row) {
-    const int most = a.t[0].heads > a.t[1].heads ? a.t[0].heads : a.t[1].heads;
-    const int64_t lanes = (int64_t)most << sh.lanes_shift;
-    if (lanes > 64) {
-      sh.waves = (int)((lanes + 63) / 64);
-      if (sh.waves > kMaxSpanWaves) sh.waves = (sh.waves + 1) / 2;
+  // a row too long for that many lanes
+  while (a.row && unit_lanes(most, ls, best) > 64 * kMaxRowWaves) ++best;
+  return best;
+}
+
+HeadsShape shape(const HeadsArgs& a, int ni) {
+  HeadsShape sh = {};
+  sh.lanes_shift = lanes_shift(a.d);
+  sh.waves = 1;
+  if (a.row)
+    for (const HeadsTensor& x : a.t) {
+      const int64_t waves = (unit_lanes(x.heads, sh.lanes_shift, ni) + 63) / 64;
+      if (waves > sh.waves) sh.waves = (int)waves;
     }
-    for (int i = 0; i < 2; ++i) {
-      if (!a.t[i].heads) continue;
-      sh.row_shift[i] = log2_up((int64_t)a.t[i].heads << sh.lanes_shift);
-      const int64_t per = sh.waves ? 1 : kHeadThreads >> sh.row_shift[i];
-      sh.blocks[i] = (uint32_t)((a.tokens + per - 1) / per);
-    }
+  for (int i = 0; i < 2; ++i) {
+    if (!a.t[i].heads) continue;
+    int64_t lanes = unit_lanes(a.t[i].heads, sh.lanes_shift, ni);
+    sh.t[i].segments = a.row || lanes <= 64 ? 1 : (int)(lanes / 64);
+    if (lanes > 64) lanes = 64;
+    sh.t[i].shift = log2_up(lanes);
+    const int64_t per = sh.waves > 1 ? 1 : kHeadThreads / lanes;
+    sh.t[i].blocks = (uint32_t)((a.tokens * sh.t[i].segments + per - 1) / per);
   }
   return sh;
 }
 
+template <int NI, bool F16, bool HALVES>
+hipError_t launch_ni(const HeadsArgs& a, hipStream_t st) {
+  const HeadsShape sh = shape(a, NI);
+  const dim3 grid(sh.t[0].blocks + sh.t[1].blocks);
+  const dim3 block(sh.waves > 1 ? 64 * sh.waves : kHeadThreads);
+  if (a.row)
+    heads_kernel<NI, F16, HALVES, true><<<grid, block, 0, st>>>(a, sh);
+  else
+    heads_kernel<NI, F16, HALVES, false><<<grid, block, 0, st>>>(a, sh);
+  return hipGetLastError();
+}
+
 template <bool F16, bool HALVES>
 hipError_t launch(const HeadsArgs& a, hipStream_t st) {
-  const HeadsShape sh = shape(a);
-  const dim3 grid(sh.blocks[0] + sh.blocks[1]);
-  if (!a.row) {
-    heads_kernel<F16, HALVES><<<grid, dim3(kHeadThreads), 0, st>>>(a, sh);
-  } else {
-    const int most = a.t[0].heads > a.t[1].heads ? a.t[0].heads : a.t[1].heads;
-    const dim3 block(sh.waves ? 64 * sh.waves : kHeadThreads);
-    if (sh.waves * 64 < (int64_t)most << sh.lanes_shift && sh.waves)
-      rows_kernel<2, F16, HALVES><<<grid, block, 0, st>>>(a, sh);
-    else
-      rows_kernel<1, F16, HALVES><<<grid, block, 0, st>>>(a, sh);
+  switch (heads_of_lane(a, lanes_shift(a.d))) {
+    case 1: return launch_ni<1, F16, HALVES>(a, st);
+    case 2: return launch_ni<2, F16, HALVES>(a, st);
+    case 3: return launch_ni<3, F16, HALVES>(a, st);
+    case 4: return launch_ni<4, F16, HALVES>(a, st);
+    default: return launch_ni<5, F16, HALVES>(a, st);
   }
-  return hipGetLastError();
 }
 
 }  // namespace
@@ -421,14 +447,18 @@ hipError_t launch_rope_table(const RopeTableArgs& a, PosType type, hipStream_t s
   return hipGetLastError();
 }
 
-bool heads_row_fits(int64_t heads, int d) {
-  return (heads << lanes_shift(d)) <= 2 * 64 * kMaxSpanWaves;
-}
+bool heads_row_fits(int64_t heads, int d) { return (heads << lanes_shift(d)) <= 2048; }
 
 bool heads_grid_fits(const HeadsArgs& a) {
-  const HeadsShape sh = shape(a);
-  const int waves = sh.waves ? sh.waves : kHeadThreads / 64;
-  return ((int64_t)sh.blocks[0] + sh.blocks[1]) * waves <= kMaxLaunchWaves;
+  // the most blocks and units: one head per lane group
+  const int ls = lanes_shift(a.d);
+  int64_t blocks = 0;
+  for (const HeadsTensor& x : a.t) {
+    const int64_t waves = x.heads ? (unit_lanes(x.heads, ls, 1) + 63) / 64 : 0;
+    if (waves * a.tokens > kMaxLaunchWaves) return false;
+    blocks += waves * a.tokens;
+  }
+  return blocks <= kMaxLaunchWaves / kMaxRowWaves;
 }
 
 hipError_t launch_qk_norm_rope(const HeadsArgs& a, bool halves, DType dt, hipStream_t st) {
