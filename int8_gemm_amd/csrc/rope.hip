@@ -1,9 +1,11 @@
 // Rotary tables of positions with several axes, and norms of queries and keys
 // with the rotation in the same pass (gfx950).
 //
-// Table: pair p of an axis turns by position * theta^(-2 j / n). Angles are
-// formed and reduced in float64 (a position of 10^5 leaves fp32 three digits of
-// its angle) and their cos and sin rounded once.
+// Table: pair p of an axis turns by position * theta^(-2 j / n). Angles are formed and
+// reduced in float64 (a position of 10^5 leaves fp32 three digits of its angle), in
+// quarter turns, whose whole part is exact; cos and sin of the rest, at most an eighth
+// of a turn, are their Taylor series to x^12, off by 10^-11, and rounded once. Bound by
+// the writes (32760 x 64 pairs: TODO us).
 //
 // Norm and rotation: v = x / sqrt(mean(x^2) + eps) * weight (or the layer norm)
 // over a head, or over all heads of a token, then (a, b) -> (a cos - b sin,
@@ -25,32 +27,56 @@ namespace {
 // ---- table -----------------------------------------------------------------
 
 constexpr int kTableThreads = 256;
-constexpr int kTableTokens = 16;  // of a block
+constexpr int kTableTokens = 32;  // of a block
+
+// (cos, sin) of a quarter turn times `quarters`.
+__device__ __forceinline__ float2 cos_sin(double quarters) {
+  const double whole = __builtin_rint(quarters);
+  const double x = (quarters - whole) * 1.57079632679489661923;
+  const double x2 = x * x;
+  double c = 1.0 / 479001600;  // 12!
+  c = __builtin_fma(c, x2, -1.0 / 3628800);
+  c = __builtin_fma(c, x2, 1.0 / 40320);
+  c = __builtin_fma(c, x2, -1.0 / 720);
+  c = __builtin_fma(c, x2, 1.0 / 24);
+  c = __builtin_fma(c, x2, -1.0 / 2);
+  c = __builtin_fma(c, x2, 1.0);
+  double s = -1.0 / 39916800;  // 11!
+  s = __builtin_fma(s, x2, 1.0 / 362880);
+  s = __builtin_fma(s, x2, -1.0 / 5040);
+  s = __builtin_fma(s, x2, 1.0 / 120);
+  s = __builtin_fma(s, x2, -1.0 / 6);
+  s = __builtin_fma(s * x2, x, x);
+  const float fc = (float)c, fs = (float)s;
+  const int turn = (int)(whole - 4.0 * __builtin_floor(whole * 0.25));
+  float2 r = turn & 1 ? make_float2(-fs, fc) : make_float2(fc, fs);
+  return turn & 2 ? make_float2(-r.x, -r.y) : r;
+}
 
 template <typename P>
 __global__ __launch_bounds__(kTableThreads) void rope_table_kernel(RopeTableArgs a) {
-  __shared__ double freq[kMaxRopePairs];
+  __shared__ double freq[kMaxRopePairs];  // quarter turns of a position
   __shared__ int axis_of[kMaxRopePairs];
   for (int p = threadIdx.x; p < a.pairs; p += kTableThreads) {
     int axis = 0;
     while (axis + 1 < a.axes && p >= a.first[axis + 1]) ++axis;
     const int j = a.shared ? p : p - a.first[axis];
     const int n = a.shared ? a.pairs : a.first[axis + 1] - a.first[axis];
-    freq[p] = exp2(-a.log2_theta * ((double)j / n));  // 2 j of 2 n elements
+    // 2 j of 2 n elements; 2 / pi quarter turns a radian
+    freq[p] = exp2(-a.log2_theta * ((double)j / n)) * 0.63661977236758134308;
     axis_of[p] = axis;
   }
   __syncthreads();
   const int64_t token0 = (int64_t)blockIdx.x * kTableTokens;
   const int tokens = (int)min((int64_t)kTableTokens, a.tokens - token0);
-  const P* positions = static_cast<const P*>(a.positions);
+  const P* positions = static_cast<const P*>(a.positions) + token0 * a.token_stride;
+  float2* table = reinterpret_cast<float2*>(a.table) + token0 * a.pairs;
+  const float inv = 1.0f / (float)a.pairs;
   for (int i = threadIdx.x; i < tokens * a.pairs; i += kTableThreads) {
-    const int64_t token = token0 + i / a.pairs;
-    const int p = i % a.pairs;
-    const double angle =
-        (double)positions[token * a.token_stride + axis_of[p] * a.axis_stride] * freq[p];
-    double s, c;
-    sincos(angle, &s, &c);
-    reinterpret_cast<float2*>(a.table)[token * a.pairs + p] = make_float2((float)c, (float)s);
+    const int t = (int)(((float)i + 0.5f) * inv);  // i / pairs: i < 2^12, off by less than half
+    const int p = i - t * a.pairs;
+    table[i] =
+        cos_sin((double)positions[t * a.token_stride + axis_of[p] * a.axis_stride] * freq[p]);
   }
 }
 
@@ -368,25 +394,32 @@ int64_t unit_lanes(int64_t heads, int ls, int ni) {
   return lanes <= 64 ? (int64_t)1 << log2_up(lanes) : (lanes + 63) / 64 * 64;
 }
 
-// Heads per lane group: as many loads under way as there are, unless lanes then lie idle
-// (32760 tokens x 40 heads of 128, norms over rows: one 347 us, five TODO us), or the
-// call has too few tokens to fill the card so.
+// Heads per lane group. Single heads: two, if that leaves the card filled (4608 tokens x
+// 30 heads of 128: one 29.8 us, two 25.9, four 27.3; 32760 x 24 of 64: 95, 82, 84). Rows
+// of up to four waves: one (4608 x 30 of 128: 26.9 us, two 27.9, four 30.4; 16384 x 16 of
+// 256: 103.5, 102.7, 109). Longer rows: the number that leaves fewest lanes idle, the
+// larger of equals, as fewer waves wait for each other (32760 x 40 of 128: one 280 us on
+// five waves, two 265, three 263, four 284 with a third of the lanes idle, five 257 on one).
+// By sizes alone: how a row's sum is cut decides its last bit.
+constexpr int64_t kFilled = 256 * 2048;  // threads of a full card
 int heads_of_lane(const HeadsArgs& a, int ls) {
   const int64_t most = a.t[0].heads > a.t[1].heads ? a.t[0].heads : a.t[1].heads;
-  int best = 1;
+  const int64_t lanes1 = unit_lanes(most, ls, 1);
+  if (!a.row) return most > 1 && a.tokens * lanes1 >= kFilled ? 2 : 1;
+  if (lanes1 <= 256) return 1;
+  int best = 0;
   double held = 0;
   for (int ni = 1; ni <= kMaxHeadsOfLane; ++ni) {
     const int64_t lanes = unit_lanes(most, ls, ni);
-    if (ni > 1 && a.tokens * lanes < (int64_t)compute_units() * 1024) continue;
-    if (a.row && lanes > 64 * kMaxRowWaves) continue;
+    if (lanes > 64 * kMaxRowWaves) continue;
+    // few tokens: as many waves as there are
+    if (best && a.tokens * lanes < kFilled) break;
     const double use = (double)(most << ls) / (double)(lanes * ni);
-    if (use >= held * 0.95) {
+    if (use >= held) {
       best = ni;
-      if (use > held) held = use;
+      held = use;
     }
   }
-  // a row too long for that many lanes
-  while (a.row && unit_lanes(most, ls, best) > 64 * kMaxRowWaves) ++best;
   return best;
 }
 
