@@ -577,7 +577,9 @@ convrot_status convrot_norm_residual(const convrot_norm_args* args, void* stream
  *   workspace (256-byte aligned, convrot_attention_workspace_size bytes, nullable
  *   where that is 0) holds the parts of calls with few queries, whose keys are
  *   split over the card; with less, a call splits less, and sums in another order.
- *   k and v tokens are at most 2^22 elements apart. scale > 0. */
+ *   k and v tokens are at most 2^22 elements apart. scale > 0. tile, a test / tuning
+ *   hook: 0 = automatic, 32 (the kernel for few rows), 128 or, for 64 < d <= 128, 256
+ *   = rows (query, head of a group) of a block. */
 typedef enum convrot_position_type {
   CONVROT_POSITION_I32 = 0,
   CONVROT_POSITION_I64 = 1,
@@ -620,6 +622,7 @@ typedef struct convrot_attention_args {
   int32_t q_heads, k_heads, d, causal;
   convrot_dtype dtype;
   float scale;
+  int32_t tile;
 } convrot_attention_args;
 /* Workspace bytes of a call of these sizes (its pointers are not read, but whether
  * q_offsets is null counts); 0 where none is used, and for invalid sizes. */

@@ -39,7 +39,7 @@ class _AttentionArgs(ctypes.Structure):
                     "v_head_stride", "out_stride", "out_head_stride", "q_tokens", "k_tokens",
                     "batch")]
                 + [(f, ctypes.c_int32) for f in ("q_heads", "k_heads", "d", "causal")]
-                + [("dtype", ctypes.c_int), ("scale", ctypes.c_float)])
+                + [("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("tile", ctypes.c_int32)])
 
 
 # As in mx4.py: one expression on the good path, what is wrong is worked out behind it.
@@ -206,7 +206,7 @@ def _sequences(offsets, name: str, of: torch.Tensor, batch: int, dev: int):
     return p, n
 
 
-def _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale):
+def _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale, tile):
     """The arguments of a call but its outputs, and the device index."""
     dev, dtype = _first(q, "q"), q.dtype
     pq, tokens, heads, d, qs, qh, batch = _heads(q, "q", dtype, dev)
@@ -222,14 +222,15 @@ def _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale):
     pkl = None if k_lens is None else _tensor(k_lens, "k_lens", _I32, (batch,), dev)
     return _AttentionArgs(pq, pk, pv, None, None, pqo, pko, pkl, qs, qh, ks, kh, vs, vh, 0, 0,
                           tokens, k_tokens, batch, heads, k_heads, d, causal, _DTYPES[dtype],
-                          d ** -0.5 if scale is None else scale), dev
+                          d ** -0.5 if scale is None else scale, tile), dev
 
 
 def convrot_attention_workspace_size(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
                                      q_offsets: torch.Tensor | None = None,
-                                     k_offsets: torch.Tensor | None = None) -> int:
+                                     k_offsets: torch.Tensor | None = None,
+                                     causal: bool = False, tile: int = 0) -> int:
     """Workspace bytes of a convrot_attention call with these tensors."""
-    a, _ = _attention_args(q, k, v, q_offsets, k_offsets, None, False, None)
+    a, _ = _attention_args(q, k, v, q_offsets, k_offsets, None, causal, None, tile)
     return int(load_library().convrot_attention_workspace_size(ctypes.byref(a)))
 
 
@@ -239,7 +240,7 @@ def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
                       k_lens: torch.Tensor | None = None, causal: bool = False,
                       scale: float | None = None, return_lse: bool = False,
                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-                      workspace: torch.Tensor | None = None):
+                      workspace: torch.Tensor | None = None, tile: int = 0):
     """softmax(scale q k^T) v per sequence and head; out like q, and lse
     [q_heads, tokens] fp32 where `return_lse` or `lse` ask for it.
 
@@ -248,8 +249,8 @@ def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     [batch, length, heads, d]; k_lens (int32 [batch]): the keys in use of each
     sequence. `causal` masks lower right; `scale` defaults to d^-1/2. Rows that no
     sequence owns are not written. `workspace` (uint8 on the device) defaults to what
-    the call asks for."""
-    a, dev = _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale)
+    the call asks for. `tile` != 0 forces a kernel (test / tuning hook)."""
+    a, dev = _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale, tile)
     if out is None:
         out, a.out, a.out_stride, a.out_head_stride = _like(q, a.q_tokens, a.q_heads, a.d)
     else:

@@ -105,6 +105,8 @@ convrot_status check_attention(const char* fn, const convrot_attention_args& a, 
   if ((!a.q_offsets && a.q_tokens % a.batch) || (!a.k_offsets && a.k_tokens % a.batch))
     return fail(CONVROT_E_INVALID_ARG, "%s: tokens without offsets do not divide into %lld "
                 "sequences", fn, (long long)a.batch);
+  if (a.tile != 0 && a.tile != 32 && a.tile != 128 && !(a.tile == 256 && a.d > 64 && a.d <= 128))
+    return fail(CONVROT_E_INVALID_ARG, "%s: tile=%d not supported (d=%d)", fn, a.tile, a.d);
   if (!(a.scale > 0.0f) || a.scale > 3.0e38f)
     return fail(CONVROT_E_INVALID_ARG, "%s: scale=%g", fn, (double)a.scale);
   return CONVROT_OK;
@@ -136,6 +138,7 @@ AttentionArgs attention_args(const convrot_attention_args& a) {
   n.d = a.d;
   n.causal = a.causal != 0;
   n.scale = a.scale;
+  n.tile = a.tile;
   n.splits = 1;
   return n;
 }

@@ -56,6 +56,7 @@ struct AttentionArgs {
   int batch, q_heads, k_heads, d;
   bool causal;
   float scale;
+  int tile;  // rows of a block's tile, 0: by the sizes
   int group, q_each, k_each;  // query heads of a key head; tokens of equal sequences
   // splits > 1: the tiles from `whole` on (few rows: all) go by parts, each split's
   // normalised rows and their log2 sums, joined by a second launch
@@ -63,6 +64,7 @@ struct AttentionArgs {
   uint32_t whole;
   float* part;        // few rows: [split][q_tokens * q_heads][d]; else [tile][split][row][d]
   float* part_lse;    // the same without d
+  int part_step;      // rows of a tile
   int64_t* part_map;  // [tile][row]: row of the output, -1 for none; null for few rows
 };
 // How a call is cut.

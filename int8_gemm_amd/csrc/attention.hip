@@ -14,6 +14,9 @@
 // contraction takes keys in the order in which the first product's result has
 // them. V^T comes from LDS through the transposing reads.
 
+#include <type_traits>
+#include <utility>
+
 #include "attention.h"
 #include "lds_copy.h"
 
@@ -29,6 +32,7 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileKeys = 64;   // keys of a copied tile
 constexpr int kRowsOfTile = 128;
+constexpr int kRowsOfWide = 256;
 constexpr int kMaxSplits = 512;  // two rounds of a block per compute unit
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -60,6 +64,16 @@ __device__ __forceinline__ int k_slot(int row, int chunk) {
 template <int DP>
 __device__ __forceinline__ int v_slot(int row, int chunk) {
   return DP == 64 ? chunk ^ (((row >> 1) & 1) << 2) : chunk ^ ((row & 3) << 2);
+}
+
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_each(F& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+// f(0), f(1), .. as constants
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F f) {
+  static_for_each(f, std::make_integer_sequence<int, N>{});
 }
 
 __device__ __forceinline__ float other_half(float v) {
@@ -229,9 +243,166 @@ __device__ __forceinline__ void add_nonfinite(const AttentionArgs& a, int64_t ke
   }
 }
 
+// A block's tile of rows and its keys.
+struct Tile {
+  Where w;
+  int hk;           // key head
+  int rows, row0;   // of the sequence, first of the tile
+  int shift;        // query i sees keys below i + shift (causal)
+  int end, full;    // keys that the tile's last query sees, that all of them see
+  int t0, tiles;    // key tiles [t0, tiles)
+  bool tail;        // a part of a split tile,
+  uint32_t piece;   // ... this one
+};
+
+// Blocks of an XCD (they are dealt in turn) take neighbouring tiles of the same heads,
+// whose keys then meet in its L2. Causal tiles differ in length, so XCDs that share
+// heads take a head's tiles in turn. The first a.whole tiles are a block's each, the
+// last ones are split. False for a block without a tile.
+template <int ROWS, bool CAUSAL>
+__device__ __forceinline__ bool locate(const AttentionArgs& a, uint32_t slots, uint32_t xcds,
+                                       uint32_t share, Tile* t) {
+  t->tail = a.splits > 1 && blockIdx.x >= a.whole;
+  uint32_t id = t->tail ? blockIdx.x - a.whole : blockIdx.x;
+  if (CAUSAL && !t->tail) {
+    const uint32_t x = id % xcds, heads = (uint32_t)a.k_heads * share / xcds;
+    const uint32_t at = id / xcds * share + x % share;
+    if (at >= heads * slots) return false;
+    id = x / share * heads * slots + at;
+  } else {
+    const uint32_t total = t->tail ? gridDim.x - a.whole : a.splits > 1 ? a.whole : gridDim.x;
+    const uint32_t full = total / xcds, rest = total % xcds;
+    const uint32_t x = id % xcds, i = id / xcds;
+    id = x * full + min(x, rest) + i;
+  }
+  t->piece = id;
+  uint32_t split = 0;
+  if (t->tail) {
+    split = id % (uint32_t)a.splits;
+    id = a.whole + id / (uint32_t)a.splits;
+  }
+  uint32_t slot = id % slots;
+  t->hk = (int)(id / slots);
+  if (CAUSAL) slot = slots - 1 - slot;  // long tiles first
+  Where& w = t->w;
+  const bool found = find<ROWS>(a, slot, &w);
+  t->rows = w.lq * a.group;  // < 2^31 checked
+  t->row0 = w.tile * ROWS;
+  if (t->tail && split == 0 && threadIdx.x < ROWS) {
+    // which row of the output each of the tile's is
+    const int r = t->row0 + (int)threadIdx.x;
+    int64_t to = -1;
+    if (found && r < t->rows)
+      to = (int64_t)(w.q0 + r / a.group) * a.q_heads + t->hk * a.group + r % a.group;
+    a.part_map[(int64_t)(id - a.whole) * ROWS + threadIdx.x] = to;
+  }
+  if (!found) return false;
+  t->shift = w.lk - w.lq + 1;
+  t->end = t->full = w.lk;
+  if (CAUSAL) {
+    const int last = min(t->rows - 1, t->row0 + ROWS - 1) / a.group, first = t->row0 / a.group;
+    t->end = min(w.lk, max(0, last + t->shift));
+    t->full = min(w.lk, max(0, first + t->shift));
+  }
+  t->t0 = 0;
+  t->tiles = (t->end + kTileKeys - 1) / kTileKeys;
+  if (t->tail) {
+    const int per = (t->tiles + a.splits - 1) / a.splits;
+    t->t0 = min(t->tiles, (int)split * per);
+    t->tiles = min(t->tiles, t->t0 + per);
+  }
+  return true;
+}
+
+// A row's result, of which this lane holds o, its part l of the sum and the reference m.
+template <int ROWS, int DTILES, bool F16>
+__device__ __forceinline__ void finish(const AttentionArgs& a, const Tile& t, int row, float l,
+                                       float m, float c, const v16f (&o)[DTILES]) {
+  const int half = (threadIdx.x >> 5) & 1;
+  const float sum = l + other_half(l);
+  const bool some = sum > 0.f || sum != sum;
+  const float inv = some ? 1.0f / sum : 0.f;
+  const float lse2 = some ? log2f(sum) - kLift<F16> + m * c : -__builtin_inff();
+  if (row >= t.rows) return;
+  if (t.tail) {
+    const int64_t at = (int64_t)t.piece * ROWS + row - t.row0;
+    if (half == 0) a.part_lse[at] = lse2;
+    if (!some) return;
+    float* to = a.part + at * a.d;
+#pragma unroll
+    for (int d = 0; d < DTILES; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = d * 32 + i * 8 + half * 4;
+        const v4f f = {o[d][4 * i] * inv, o[d][4 * i + 1] * inv, o[d][4 * i + 2] * inv,
+                       o[d][4 * i + 3] * inv};
+        if (e < a.d) *reinterpret_cast<v4f*>(to + e) = f;
+      }
+    return;
+  }
+  const int token = t.w.q0 + row / a.group, head = t.hk * a.group + row % a.group;
+  if (a.lse && half == 0) a.lse[(int64_t)head * a.q_tokens + token] = lse2 * kLn2;
+  uint16_t* to = a.out + (int64_t)token * a.out_stride + (int64_t)head * a.out_head_stride;
+  // the two lanes of a row hold four elements of each eight: they swap, so that each
+  // has every other eight
+#pragma unroll
+  for (int d = 0; d < DTILES; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      u4 f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+        const int n = 4 * i + 2 * j;
+        const u2v x = __builtin_amdgcn_permlane32_swap(
+            pack16x2<F16>(o[d][n] * inv, o[d][n + 1] * inv),
+            pack16x2<F16>(o[d][n + 4] * inv, o[d][n + 5] * inv), false, false);
+        f[j] = x.x;
+        f[2 + j] = x.y;
+      }
+      const int e = d * 32 + (i + half) * 8;
+      if (e < a.d) *reinterpret_cast<u4*>(to + e) = f;
+    }
+}
+
+// The first key and value of a tile's head, as bytes.
+__device__ __forceinline__ const int8_t* head_bytes(const uint16_t* p, const Where& w,
+                                                    int64_t stride, int64_t head_stride, int hk) {
+  return reinterpret_cast<const int8_t*>(p + (int64_t)w.k0 * stride + (int64_t)hk * head_stride);
+}
+
+// A row's query as the first product's operand, and how many keys it sees.
+template <int STEPS, bool CAUSAL>
+__device__ __forceinline__ void load_query(const AttentionArgs& a, const Where& w, int hk, int row,
+                                           u4 (&qf)[STEPS], int* seen) {
+  const int half = (threadIdx.x >> 5) & 1;
+  const int r = min(row, w.lq * a.group - 1);
+  const int token = r / a.group, head = hk * a.group + r % a.group;
+  *seen = CAUSAL ? min(w.lk, token + w.lk - w.lq + 1) : w.lk;
+  const uint16_t* q =
+      a.q + (int64_t)(w.q0 + token) * a.q_stride + (int64_t)head * a.q_head_stride;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int e = (2 * s + half) * 8;
+    const u4 zero = {0, 0, 0, 0};
+    qf[s] = e < a.d ? *reinterpret_cast<const u4*>(q + e) : zero;
+  }
+}
+
+// Scores of keys that a row does not see. The lane's sixteen keys of a unit are those at
+// 8 i + 4 half + (0 .. 3).
+__device__ __forceinline__ void mask(v16f* s, int key0, int seen) {
+  const int left = seen - key0 - 4 * (int)((threadIdx.x >> 5) & 1);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (8 * (i >> 2) + (i & 3) >= left) (*s)[i] = -__builtin_inff();
+}
+
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(AttentionArgs a, uint32_t slots,
-                                                               uint32_t xcds) {
+__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(AttentionArgs a,
+                                                                              uint32_t slots,
+                                                                              uint32_t xcds,
+                                                                              uint32_t share) {
   using T = Kernel<DP, QT, NW, F16>;
   extern __shared__ __align__(1024) uint8_t lds[];
   volatile int* cleared = reinterpret_cast<int*>(lds + 2 * T::kStages * T::kTileBytes);
@@ -239,82 +410,23 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
-  const int group = a.group;
+  Tile w;
+  if (!locate<T::kRows, CAUSAL>(a, slots, xcds, share, &w)) return;
 
-  // blocks of an XCD (they are dealt in turn) take neighbouring tiles of the same
-  // heads, whose keys then meet in its L2
-  // the first a.whole tiles are a block's each, the last ones are split
-  const bool tail = blockIdx.x >= a.whole;
-  uint32_t id = tail ? blockIdx.x - a.whole : blockIdx.x;
-  {
-    const uint32_t total = tail ? gridDim.x - a.whole : a.whole;
-    const uint32_t full = total / xcds, rest = total % xcds;
-    const uint32_t x = id % xcds, i = id / xcds;
-    id = x * full + min(x, rest) + i;
-  }
-  const int splits = tail ? a.splits : 1;
-  const int split = tail ? (int)(id % (uint32_t)splits) : 0;
-  const uint32_t piece = id;  // of the tail
-  if (tail) id = a.whole + id / (uint32_t)splits;
-  uint32_t slot = id % slots;
-  const int hk = (int)(id / slots);
-  if (CAUSAL) slot = slots - 1 - slot;  // long tiles first
-  Where w;
-  const bool found = find<T::kRows>(a, slot, &w);
-  if (tail && split == 0 && threadIdx.x < T::kRows) {
-    // which row of the output each of the tile's is
-    const int r = w.tile * T::kRows + (int)threadIdx.x;
-    int64_t to = -1;
-    if (found && r < w.lq * group)
-      to = (int64_t)(w.q0 + r / group) * a.q_heads + hk * group + r % group;
-    a.part_map[(int64_t)(id - a.whole) * T::kRows + threadIdx.x] = to;
-  }
-  if (!found) return;
-
-  const int rows = w.lq * group;  // < 2^31 checked
-  const int row0 = w.tile * T::kRows;
-  // keys that the tile's last and first query see
-  const int shift = w.lk - w.lq + 1;
-  int end = w.lk, full = w.lk;
-  if (CAUSAL) {
-    const int last = min(rows - 1, row0 + T::kRows - 1) / group, first = row0 / group;
-    end = min(w.lk, max(0, last + shift));
-    full = min(w.lk, max(0, first + shift));
-  }
-  int tiles = (end + kTileKeys - 1) / kTileKeys;
-  int t0 = 0;
-  if (splits > 1) {
-    const int per = (tiles + splits - 1) / splits;
-    t0 = min(tiles, split * per);
-    tiles = min(tiles, t0 + per);
-  }
-
-  // this lane's rows
   int row[QT], seen[QT];
   u4 qf[QT][T::kSteps];
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    row[t] = row0 + (wave * QT + t) * 32 + col;
-    const int r = min(row[t], rows - 1);
-    const int token = r / group, head = hk * group + r % group;
-    seen[t] = CAUSAL ? min(w.lk, token + shift) : w.lk;
-    const uint16_t* q = a.q + (int64_t)(w.q0 + token) * a.q_stride + (int64_t)head * a.q_head_stride;
-#pragma unroll
-    for (int s = 0; s < T::kSteps; ++s) {
-      const int c = 2 * s + half;
-      const u4 zero = {0, 0, 0, 0};
-      qf[t][s] = c * 8 < a.d ? *reinterpret_cast<const u4*>(q + c * 8) : zero;
-    }
+  for (int q = 0; q < QT; ++q) {
+    row[q] = w.row0 + (wave * QT + q) * 32 + col;
+    load_query<T::kSteps, CAUSAL>(a, w.w, w.hk, row[q], qf[q], &seen[q]);
   }
 
   // copies: lane i of a copy fills the 16 bytes behind 16 i
-  const int8_t* kbase =
-      reinterpret_cast<const int8_t*>(a.k + (int64_t)w.k0 * a.k_stride + (int64_t)hk * a.k_head_stride);
-  const int8_t* vbase =
-      reinterpret_cast<const int8_t*>(a.v + (int64_t)w.k0 * a.v_stride + (int64_t)hk * a.v_head_stride);
+  const int8_t* kbase = head_bytes(a.k, w.w, a.k_stride, a.k_head_stride, w.hk);
+  const int8_t* vbase = head_bytes(a.v, w.w, a.v_stride, a.v_head_stride, w.hk);
   const uint32_t kstride = (uint32_t)a.k_stride * 2, vstride = (uint32_t)a.v_stride * 2;
   auto issue = [&](int t, int stage) {
-    const int last = w.lk - 1 - t * kTileKeys;  // rows behind it repeat it
+    const int last = w.w.lk - 1 - t * kTileKeys;  // rows behind it repeat it
     const int8_t* kp = kbase + (int64_t)t * kTileKeys * a.k_stride * 2;
     const int8_t* vp = vbase + (int64_t)t * kTileKeys * a.v_stride * 2;
 #pragma unroll
@@ -324,32 +436,31 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
       const int from = min(r, last);
       const int kc = min(k_slot<DP>(r, c), a.d / 8 - 1), vc = min(v_slot<DP>(r, c), a.d / 8 - 1);
       dma16(kp, from * kstride + kc * 16, stage * T::kTileBytes + at * 16);
-      dma16(vp, from * vstride + vc * 16,
-            (T::kStages + stage) * T::kTileBytes + at * 16);
+      dma16(vp, from * vstride + vc * 16, (T::kStages + stage) * T::kTileBytes + at * 16);
     }
   };
 
   v16f o[QT][T::kDTiles];
-  v16f below[QT];           // -m in every place: the first product starts from it
+  v16f below[QT];  // -m in every place: the first product starts from it
   float l[QT], raise_at[QT];
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    below[t] = (v16f){0};
-    raise_at[t] = -__builtin_inff();  // no m yet
-    l[t] = 0.f;
+  for (int q = 0; q < QT; ++q) {
+    below[q] = (v16f){0};
+    raise_at[q] = -__builtin_inff();  // no m yet
+    l[q] = 0.f;
 #pragma unroll
-    for (int d = 0; d < T::kDTiles; ++d) o[t][d] = (v16f){0};
+    for (int d = 0; d < T::kDTiles; ++d) o[q][d] = (v16f){0};
   }
   const float c = a.scale * kLog2e;
   const float room = kRoom / c;
 
-  if (t0 < tiles) issue(t0, 0);
-  for (int t = t0; t < tiles; ++t) {
-    const int stage = (t - t0) & 1;
+  if (w.t0 < w.tiles) issue(w.t0, 0);
+  for (int t = w.t0; t < w.tiles; ++t) {
+    const int stage = (t - w.t0) & 1;
     wait_vmcnt<0>();
     wait_lgkm0();
     lds_barrier();
-    if (t + 1 < tiles) issue(t + 1, stage ^ 1);
+    if (t + 1 < w.tiles) issue(t + 1, stage ^ 1);
     const uint8_t* kt = lds + stage * T::kTileBytes;
     uint8_t* vt = lds + (T::kStages + stage) * T::kTileBytes;
     v16f s[2][QT];
@@ -365,17 +476,12 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
           s[u][q] = mfma<F16>(kf, qf[q][st], st == 0 ? below[q] : s[u][q]);
       }
     }
-    const int key0 = t * kTileKeys;
-    if (key0 + kTileKeys > full) {
+    const bool masked = (t + 1) * kTileKeys > w.full;
+    if (masked) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int q = 0; q < QT; ++q)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int key = key0 + u * 32 + 8 * (i >> 2) + 4 * half + (i & 3);
-            if (key >= seen[q]) s[u][q][i] = -__builtin_inff();
-          }
+        for (int q = 0; q < QT; ++q) mask(&s[u][q], t * kTileKeys + u * 32, seen[q]);
     }
     float top[QT];
     bool raise = false;
@@ -429,7 +535,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
             p[u][q][h][e] = pack16x2<F16>(s[u][q][8 * h + 2 * e], s[u][q][8 * h + 2 * e + 1]);
       }
     }
-    if (CAUSAL && key0 + kTileKeys > full && clear_nonfinite<F16, DP, kTileKeys>(vt)) *cleared = 1;
+    if (CAUSAL && masked && clear_nonfinite<F16, DP, kTileKeys>(vt)) *cleared = 1;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -446,61 +552,383 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
     wait_lgkm0();
     lds_barrier();
     if (__builtin_expect(*cleared, 0)) {
-      const int to = min(end, tiles * kTileKeys);
+      const int to = min(w.end, w.tiles * kTileKeys);
 #pragma unroll 1
-      for (int key = max(full / kTileKeys, t0) * kTileKeys; key < to; ++key)
+      for (int key = max(w.full / kTileKeys, w.t0) * kTileKeys; key < to; ++key)
 #pragma unroll
         for (int q = 0; q < QT; ++q)
-          add_nonfinite<T::kDTiles, F16>(a, w.k0 + key, hk, key < seen[q], o[q]);
+          add_nonfinite<T::kDTiles, F16>(a, w.w.k0 + key, w.hk, key < seen[q], o[q]);
     }
   }
+#pragma unroll
+  for (int q = 0; q < QT; ++q)
+    finish<T::kRows, T::kDTiles, F16>(a, w, row[q], l[q], -below[q][0], c, o[q]);
+}
 
+// MFMAs of the pipeline below, whose accumulators stay where they are put: the output in
+// accumulation registers, which no vector instruction but the rare rescaling touches.
+template <bool F16>
+__device__ __forceinline__ void mfma_out(v16f* o, const u4& v, const u4& p) {
+  if constexpr (F16)
+    asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(*o) : "v"(v), "v"(p));
+  else
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(*o) : "v"(v), "v"(p));
+}
+template <bool F16>
+__device__ __forceinline__ void mfma_first(v16f* s, const u4& k, const u4& q, const v16f& below) {
+  if constexpr (F16)
+    asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %3"
+                 : "=&v"(*s) : "v"(k), "v"(q), "v"(below));
+  else
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %3"
+                 : "=&v"(*s) : "v"(k), "v"(q), "v"(below));
+}
+template <bool F16>
+__device__ __forceinline__ void mfma_score(v16f* s, const u4& k, const u4& q) {
+  if constexpr (F16)
+    asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+v"(*s) : "v"(k), "v"(q));
+  else
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(*s) : "v"(k), "v"(q));
+}
+// Before a vector instruction reads what such an MFMA wrote, or the other way round.
+template <int N>
+__device__ __forceinline__ void settle_acc(v16f (&o)[N]) {
+  asm volatile("s_nop 15\n\ts_nop 3" : "+a"(o[0]));
+#pragma unroll
+  for (int i = 1; i < N; ++i) asm volatile("" : "+a"(o[i]));
+}
+template <int N>
+__device__ __forceinline__ void settle_vec(v16f (&s)[N]) {
+  asm volatile("s_nop 15\n\ts_nop 3" : "+v"(s[0]));
+#pragma unroll
+  for (int i = 1; i < N; ++i) asm volatile("" : "+v"(s[i]));
+}
+
+// ---- many rows: 64 a wave, one wave a SIMD -----------------------------------
+//
+// A pipeline over units of 32 keys: a step computes the scores of unit u + 1, the
+// weights of unit u and the output of unit u - 1, one MFMA after the other with a few
+// vector instructions and an LDS read (three operands ahead) behind each. An operand
+// read serves both of a wave's 32-row halves.
+template <int DP, int QT>
+struct Wide {
+  static constexpr int kWaves = 4;
+  static constexpr int kRows = 32 * QT * kWaves;
+  static constexpr int kRowBytes = DP * 2;
+  static constexpr int kChunks = DP / 8;
+  static constexpr int kTileBytes = kTileKeys * kRowBytes;
+  static constexpr int kUnitBytes = 32 * kRowBytes;
+  static constexpr int kStages = 3;
+  static constexpr int kV = kStages * kTileBytes;  // values behind the keys
+  static constexpr int kLds = 2 * kStages * kTileBytes + 16;
+  static constexpr int kCopies = kTileBytes / 1024 / kWaves;
+  static constexpr int kSteps = DP / 16;
+  static constexpr int kDTiles = DP / 32;
+};
+
+template <int DP, int QT, bool F16, bool CAUSAL>
+__global__ __launch_bounds__(256, 1) void attention_wide_kernel(AttentionArgs a, uint32_t slots,
+                                                                uint32_t xcds, uint32_t share) {
+  using T = Wide<DP, QT>;
+  constexpr int kFrags = 2 * T::kSteps, kSlots = kFrags * QT, kAhead = 3, kRing = 4;
+  constexpr int kElems = 16 * QT;  // of a lane and unit
+  extern __shared__ __align__(1024) uint8_t lds[];
+  volatile int* cleared = reinterpret_cast<int*>(lds + 2 * T::kStages * T::kTileBytes);
+  if (CAUSAL && threadIdx.x == 0) *cleared = 0;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, col = lane & 31;
+  Tile w;
+  if (!locate<T::kRows, CAUSAL>(a, slots, xcds, share, &w)) return;
+
+  const int8_t* kbase = head_bytes(a.k, w.w, a.k_stride, a.k_head_stride, w.hk);
+  const int8_t* vbase = head_bytes(a.v, w.w, a.v_stride, a.v_head_stride, w.hk);
+  const uint32_t kstride = (uint32_t)a.k_stride * 2, vstride = (uint32_t)a.v_stride * 2;
+  auto copy = [&](const int8_t* base, uint32_t stride, bool values, int t, int to) __attribute__((always_inline)) {
+    const int last = w.w.lk - 1 - t * kTileKeys;  // rows behind it repeat it
+    const int8_t* p = base + (int64_t)t * kTileKeys * stride;
+#pragma unroll
+    for (int i = 0; i < T::kCopies; ++i) {
+      const int at = (wave * T::kCopies + i) * 64;
+      const int r = (at + lane) / T::kChunks, c = (at + lane) % T::kChunks;
+      const int from = values ? v_slot<DP>(r, c) : k_slot<DP>(r, c);
+      dma16(p, min(r, last) * stride + min(from, a.d / 8 - 1) * 16, to + at * 16);
+    }
+  };
+  auto copy_k = [&](int t, int stage) __attribute__((always_inline)) {
+    if (t < w.tiles) copy(kbase, kstride, false, t, stage * T::kTileBytes);
+  };
+  auto copy_v = [&](int t, int stage) __attribute__((always_inline)) {
+    if (t < w.tiles) copy(vbase, vstride, true, t, T::kV + stage * T::kTileBytes);
+  };
+  copy_k(w.t0, 0);
+  copy_v(w.t0, 0);
+  copy_k(w.t0 + 1, 1);
+
+  int row[QT], seen[QT];
+  u4 qf[QT][T::kSteps];
 #pragma unroll
   for (int q = 0; q < QT; ++q) {
-    const float sum = l[q] + other_half(l[q]);
-    const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
-    const float lse2 = sum > 0.f || sum != sum ? log2f(sum) - kLift<F16> - below[q][0] * c : -__builtin_inff();
-    if (row[q] >= rows) continue;
-    if (tail) {
-      const int64_t at = (int64_t)piece * T::kRows + row[q] - row0;
-      if (half == 0) a.part_lse[at] = lse2;
-      if (lse2 == -__builtin_inff()) continue;
-      float* to = a.part + at * a.d;
+    row[q] = w.row0 + (wave * QT + q) * 32 + col;
+    load_query<T::kSteps, CAUSAL>(a, w.w, w.hk, row[q], qf[q], &seen[q]);
+  }
+  v16f o[QT][T::kDTiles], below[QT], sa[QT], sb[QT];
+  u4 pa[QT][2], pb[QT][2];
+  float l[QT], raise_at[QT], top[QT];
 #pragma unroll
-      for (int d = 0; d < T::kDTiles; ++d)
+  for (int q = 0; q < QT; ++q) {
+    below[q] = (v16f){0};
+    raise_at[q] = -__builtin_inff();
+    l[q] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = d * 32 + i * 8 + half * 4;
-          const v4f f = {o[q][d][4 * i] * inv, o[q][d][4 * i + 1] * inv, o[q][d][4 * i + 2] * inv,
-                         o[q][d][4 * i + 3] * inv};
-          if (e < a.d) *reinterpret_cast<v4f*>(to + e) = f;
+    for (int d = 0; d < T::kDTiles; ++d) o[q][d] = (v16f){0};
+  }
+  const float c = a.scale * kLog2e;
+  const float room = kRoom / c;
+
+  // lane's addresses of a unit's operands
+  const uint8_t* kat[T::kSteps];
+#pragma unroll
+  for (int st = 0; st < T::kSteps; ++st)
+    kat[st] = lds + col * T::kRowBytes + k_slot<DP>(col, 2 * st + half) * 16;
+  const uint8_t* vat[T::kDTiles];
+#pragma unroll
+  for (int d = 0; d < T::kDTiles; ++d) {
+    const int r = half * 4 + ((lane & 15) >> 2);
+    const int chunk = d * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+    vat[d] = lds + T::kV + r * T::kRowBytes + v_slot<DP>(r, chunk) * 16 + (lane & 1) * 8;
+  }
+  auto read_k = [&](int st, int at) __attribute__((always_inline)) { return *reinterpret_cast<const u4*>(kat[st] + at); };
+  auto read_v = [&](int h, int d, int at) __attribute__((always_inline)) {
+    typedef __attribute__((address_space(3))) s4* lp;
+    uint8_t* p = const_cast<uint8_t*>(vat[d]) + at + h * 16 * T::kRowBytes;
+    const u2 w0 = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)p));
+    const u2 w1 = __builtin_bit_cast(
+        u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p + 8 * T::kRowBytes)));
+    return (u4){w0.x, w0.y, w1.x, w1.y};
+  };
+
+  u4 ring[kRing];
+  // One step. k_at: unit u + 1's keys, v_at: unit u - 1's values, next_at: unit u + 2's
+  // keys, all as offsets of LDS. cur: scores, then weights of u; nxt: scores of u + 1.
+  auto step = [&](auto pv, v16f(&cur)[QT], v16f(&nxt)[QT], u4(&pin)[QT][2], u4(&pout)[QT][2],
+                  int k_at, int v_at, int next_at) __attribute__((always_inline)) {
+    constexpr bool kPv = decltype(pv)::value;
+    auto fetch = [&](auto nn) __attribute__((always_inline)) {  // operand n of this step, or of the next
+      constexpr int n = decltype(nn)::value;
+      if constexpr (n < T::kSteps) {
+        ring[n % kRing] = read_k(n, k_at);
+      } else if constexpr (n < kFrags) {
+        constexpr int i = n - T::kSteps;
+        if constexpr (kPv) ring[n % kRing] = read_v(i / T::kDTiles, i % T::kDTiles, v_at);
+      } else {
+        ring[n % kRing] = read_k(n - kFrags, next_at);
+      }
+    };
+    auto weight = [&](int n) __attribute__((always_inline)) {  // element n: 2^(c s)
+      const int q = n / 16, i = n % 16;
+      cur[q][i] = __builtin_amdgcn_exp2f(F16 ? __builtin_fmaf(cur[q][i], c, kLift<F16>)
+                                             : cur[q][i] * c);
+      asm volatile("" : "+v"(cur[q][i]));
+    };
+    auto gather = [&](int n) __attribute__((always_inline)) {
+      const int q = n / 16, i = n % 16;
+      l[q] += cur[q][i];
+      asm volatile("" : "+v"(l[q]));
+      if (i & 1) {
+        uint32_t x = pack16x2<F16>(cur[q][i - 1], cur[q][i]);
+        asm volatile("" : "+v"(x));
+        pout[q][i / 8][i % 8 / 2] = x;
+      }
+    };
+    static_for<kSlots>([&](auto ss) __attribute__((always_inline)) {
+      constexpr int slot = decltype(ss)::value, n = slot / QT, q = slot % QT;
+      if constexpr (q == 0) fetch(std::integral_constant<int, n + kAhead>{});
+      if constexpr (n < T::kSteps) {
+        if constexpr (n == 0)
+          mfma_first<F16>(&nxt[q], ring[n % kRing], qf[q][n], below[q]);
+        else
+          mfma_score<F16>(&nxt[q], ring[n % kRing], qf[q][n]);
+      } else if constexpr (kPv) {
+        constexpr int i = n - T::kSteps, h = i / T::kDTiles, d = i % T::kDTiles;
+        mfma_out<F16>(&o[q][d], ring[n % kRing], pin[q][h]);
+      }
+      constexpr int e0 = slot * kElems / kSlots, e1 = (slot + 1) * kElems / kSlots;
+      constexpr int g0 = slot == 0 ? 0 : (slot - 1) * kElems / kSlots;
+      if constexpr (slot > 0) {
+#pragma unroll
+        for (int e = g0; e < e0; ++e) gather(e);
+      }
+#pragma unroll
+      for (int e = e0; e < e1; ++e) weight(e);
+      // the next scores are complete some slots behind their last product
+      constexpr int first = QT * T::kSteps + 2, left = kSlots - first;
+      if constexpr (slot >= first) {
+        constexpr int m0 = (slot - first) * kElems / 2 / left,
+                      m1 = (slot - first + 1) * kElems / 2 / left;
+#pragma unroll
+        for (int e = m0; e < m1; ++e) {
+          const int q = e / 8, i = e % 8 * 2;
+          if (i == 0) top[q] = -__builtin_inff();
+          asm volatile("v_max3_f32 %0, %0, %1, %2"
+                       : "+v"(top[q]) : "v"(nxt[q][i]), "v"(nxt[q][i + 1]));
         }
-      continue;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+#pragma unroll
+    for (int e = (kSlots - 1) * kElems / kSlots; e < kElems; ++e) gather(e);
+  };
+  // Scores of a unit before they become weights: its mask, and a new m where one is passed
+  auto settle = [&](v16f(&s)[QT], v16f(&before)[QT], u4(&p)[QT][2], int key0) __attribute__((always_inline)) {
+    if (key0 + 32 > w.full) {
+#pragma unroll
+      for (int q = 0; q < QT; ++q) {
+        mask(&s[q], key0, seen[q]);
+        top[q] = s[q][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top[q] = fmaxf(top[q], s[q][i]);
+      }
     }
-    const int token = row[q] / group, head = hk * group + row[q] % group;
-    if (a.lse && half == 0) a.lse[(int64_t)head * a.q_tokens + w.q0 + token] = lse2 * kLn2;
-    uint16_t* to = a.out + (int64_t)(w.q0 + token) * a.out_stride + (int64_t)head * a.out_head_stride;
-    // the two lanes of a row hold four elements of each eight: they swap, so that each
-    // has every other eight
+    bool raise = false;
 #pragma unroll
-    for (int d = 0; d < T::kDTiles; ++d)
+    for (int q = 0; q < QT; ++q) raise |= top[q] > raise_at[q];
+    if (__any(raise)) {
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        u4 f;
+      for (int q = 0; q < QT; ++q) settle_acc(o[q]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          typedef uint32_t u2v __attribute__((ext_vector_type(2)));
-          const int n = 4 * i + 2 * j;
-          const u2v x = __builtin_amdgcn_permlane32_swap(
-              pack16x2<F16>(o[q][d][n] * inv, o[q][d][n + 1] * inv),
-              pack16x2<F16>(o[q][d][n + 4] * inv, o[q][d][n + 5] * inv), false, false);
-          f[j] = x.x;
-          f[2 + j] = x.y;
+      for (int q = 0; q < QT; ++q) {
+        const float to = fmaxf(top[q], other_half(top[q]));
+        const bool up = to > raise_at[q];
+        const float by = up ? to : 0.f;
+        // a row without an m has nothing to scale yet (or NaN, which stays)
+        const float alpha =
+            up && raise_at[q] > kLowest ? __builtin_amdgcn_exp2f(-by * c) : 1.f;
+        raise_at[q] = up ? room : raise_at[q];
+        l[q] *= alpha;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          below[q][i] -= by;
+          s[q][i] -= by;
         }
-        const int e = d * 32 + (i + half) * 8;
-        if (e < a.d) *reinterpret_cast<u4*>(to + e) = f;
+        // weights that the second product has not had yet
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            p[q][h][e] = pack16x2<F16>(before[q][8 * h + 2 * e] * alpha,
+                                       before[q][8 * h + 2 * e + 1] * alpha);
+#pragma unroll
+        for (int d = 0; d < T::kDTiles; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[q][d][i] *= alpha;
+      }
+#pragma unroll
+      for (int q = 0; q < QT; ++q) settle_acc(o[q]);
+      settle_vec(below);
+    }
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+
+  if (w.t0 < w.tiles) {
+    // keys of the first tile (and of the second, its values) have landed
+    wait_vmcnt<0>();
+    wait_lgkm0();
+    lds_barrier();
+    copy_k(w.t0 + 2, 2);
+    copy_v(w.t0 + 1, 1);
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+      sa[q] = below[q];
+      sb[q] = (v16f){0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) pa[q][h] = (u4){0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int st = 0; st < T::kSteps; ++st) {
+      const u4 kf = read_k(st, 0);
+#pragma unroll
+      for (int q = 0; q < QT; ++q) mfma_score<F16>(&sa[q], kf, qf[q][st]);
+    }
+    settle_vec(sa);
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+      top[q] = sa[q][0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top[q] = fmaxf(top[q], sa[q][i]);
+    }
+    settle(sa, sb, pa, w.t0 * kTileKeys);
+    // a tile: its first unit's scores are in sa, weights of the unit before in pb
+    auto tile = [&](auto pv, auto stage, int t) __attribute__((always_inline)) {
+      constexpr int st = decltype(stage)::value, before = (st + 2) % 3, after = (st + 1) % 3;
+      const int key0 = t * kTileKeys;
+      if (CAUSAL && key0 + kTileKeys > w.full &&
+          clear_nonfinite<F16, DP, kTileKeys>(lds + T::kV + st * T::kTileBytes))
+        *cleared = 1;
+      step(pv, sa, sb, pb, pa, st * T::kTileBytes + T::kUnitBytes,
+           before * T::kTileBytes + T::kUnitBytes, after * T::kTileBytes);
+      settle(sb, sa, pa, key0 + 32);
+      step(Yes{}, sb, sa, pa, pb, after * T::kTileBytes, st * T::kTileBytes,
+           after * T::kTileBytes + T::kUnitBytes);
+      if (t + 1 < w.tiles) settle(sa, sb, pb, key0 + 64);
+    };
+    auto turn = [&](auto stage, int t) __attribute__((always_inline)) {
+      constexpr int st = decltype(stage)::value;
+      wait_vmcnt<0>();
+      wait_lgkm0();
+      lds_barrier();
+      copy_k(t + 2, (st + 2) % 3);
+      copy_v(t + 1, (st + 1) % 3);
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    using S2 = std::integral_constant<int, 2>;
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) ring[n % kRing] = read_k(n, T::kUnitBytes);
+    tile(No{}, S0{}, w.t0);
+    int t = w.t0 + 1, last = 0;
+    while (t < w.tiles) {
+      turn(S1{}, t);
+      tile(Yes{}, S1{}, t);
+      last = 1;
+      if (++t >= w.tiles) break;
+      turn(S2{}, t);
+      tile(Yes{}, S2{}, t);
+      last = 2;
+      if (++t >= w.tiles) break;
+      turn(S0{}, t);
+      tile(Yes{}, S0{}, t);
+      last = 0;
+      ++t;
+    }
+    // the last unit's output
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int d = 0; d < T::kDTiles; ++d) {
+        const u4 vf = read_v(h, d, last * T::kTileBytes + T::kUnitBytes);
+#pragma unroll
+        for (int q = 0; q < QT; ++q) mfma_out<F16>(&o[q][d], vf, pb[q][h]);
       }
   }
+#pragma unroll
+  for (int q = 0; q < QT; ++q) settle_acc(o[q]);
+  if (CAUSAL) {
+    wait_lgkm0();
+    lds_barrier();
+    if (__builtin_expect(*cleared, 0)) {
+      const int to = min(w.end, w.tiles * kTileKeys);
+#pragma unroll 1
+      for (int key = max(w.full / kTileKeys, w.t0) * kTileKeys; key < to; ++key)
+#pragma unroll
+        for (int q = 0; q < QT; ++q)
+          add_nonfinite<T::kDTiles, F16>(a, w.w.k0 + key, w.hk, key < seen[q], o[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < QT; ++q)
+    finish<T::kRows, T::kDTiles, F16>(a, w, row[q], l[q], -below[q][0], c, o[q]);
 }
 
 // ---- few rows: single tokens against a long cache ----------------------------
@@ -553,25 +981,15 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
   const int per = max(chunk, (units + a.splits - 1) / a.splits);
   const int first = min(units, split * per), last = min(units, first + per);
 
-  const int row = row0 + col;
-  const int r = min(row, rows - 1);
-  const int token = r / group, head = hk * group + r % group;
-  const int seen = a.causal ? min(w.lk, token + shift) : w.lk;
   u4 qf[kSteps];
-  {
-    const uint16_t* q = a.q + (int64_t)(w.q0 + token) * a.q_stride + (int64_t)head * a.q_head_stride;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int e = (2 * s + half) * 8;
-      const u4 zero = {0, 0, 0, 0};
-      qf[s] = e < a.d ? *reinterpret_cast<const u4*>(q + e) : zero;
-    }
-  }
+  int seen;
+  if (a.causal)
+    load_query<kSteps, true>(a, w, hk, row0 + col, qf, &seen);
+  else
+    load_query<kSteps, false>(a, w, hk, row0 + col, qf, &seen);
 
-  const int8_t* kbase =
-      reinterpret_cast<const int8_t*>(a.k + (int64_t)w.k0 * a.k_stride + (int64_t)hk * a.k_head_stride);
-  const int8_t* vbase =
-      reinterpret_cast<const int8_t*>(a.v + (int64_t)w.k0 * a.v_stride + (int64_t)hk * a.v_head_stride);
+  const int8_t* kbase = head_bytes(a.k, w, a.k_stride, a.k_head_stride, hk);
+  const int8_t* vbase = head_bytes(a.v, w, a.v_stride, a.v_head_stride, hk);
   const uint32_t kstride = (uint32_t)a.k_stride * 2, vstride = (uint32_t)a.v_stride * 2;
   const int ring = wave * T::kWaveBytes;
   auto issue = [&](int u, int stage) {
@@ -622,11 +1040,7 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
       s = mfma<F16>(kf, qf[st], s);
     }
     const int key0 = u * T::kUnit;
-    if (key0 + T::kUnit > full) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (key0 + 8 * (i >> 2) + 4 * half + (i & 3) >= seen) s[i] = -__builtin_inff();
-    }
+    if (key0 + T::kUnit > full) mask(&s, key0, seen);
     float top = s[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
@@ -667,8 +1081,8 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
     else
       wait_vmcnt<0>();
     asm volatile("" ::: "memory");
-    const bool cleared =
-        a.causal && key0 + T::kUnit > full && clear_nonfinite<F16, DP, T::kUnit>(vt);
+    // in every unit: the weights' second part would turn an infinity into NaN
+    const bool cleared = clear_nonfinite<F16, DP, T::kUnit>(vt);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -758,7 +1172,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
   // few rows: parts [split][row of the output]; tiles: [tile][split][row of the tile]
   int64_t r = blockIdx.x, at = r, step = a.q_tokens * a.q_heads;
   if (a.part_map) {
-    step = kRowsOfTile;
+    step = a.part_step;
     at = r / step * step * a.splits + r % step;
     r = a.part_map[r];
     if (r < 0) return;
@@ -828,20 +1242,44 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
   }
 }
 
-template <int DP, int QT, int NW, bool F16>
-hipError_t launch_tile(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
-  using T = Kernel<DP, QT, NW, F16>;
-  auto kern = a.causal ? attention_kernel<DP, QT, NW, F16, true>
-                       : attention_kernel<DP, QT, NW, F16, false>;
-  if (T::kLds > 65536) {
+template <typename K>
+hipError_t launch_tiles(K kern, int threads, int lds, const AttentionArgs& a,
+                        const AttentionPlan& p, hipStream_t st) {
+  if (lds > 65536) {
     // per device: the attribute is set on every call (a host-side table write)
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  kern<<<dim3((uint32_t)p.grid), dim3(64 * NW), T::kLds, st>>>(a, (uint32_t)p.slots,
-                                                               xcd_count(compute_units()));
+  const uint32_t xcds = (uint32_t)xcd_count(compute_units());
+  uint32_t common = xcds;  // greatest common divisor with the heads
+  for (uint32_t y = (uint32_t)a.k_heads; y;) {
+    const uint32_t r = common % y;
+    common = y;
+    y = r;
+  }
+  const uint32_t share = xcds / common;
+  int64_t grid = p.grid;
+  if (a.causal && p.splits == 1) {
+    const int64_t of_group = p.slots * (a.k_heads / (int)common);
+    grid = (of_group + share - 1) / share * xcds;
+  }
+  kern<<<dim3((uint32_t)grid), dim3(threads), lds, st>>>(a, (uint32_t)p.slots, xcds, share);
   return hipGetLastError();
+}
+
+template <int DP, int QT, int NW, bool F16>
+hipError_t launch_tile(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
+  return launch_tiles(a.causal ? attention_kernel<DP, QT, NW, F16, true>
+                               : attention_kernel<DP, QT, NW, F16, false>,
+                      64 * NW, Kernel<DP, QT, NW, F16>::kLds, a, p, st);
+}
+
+template <int DP, int QT, bool F16>
+hipError_t launch_wide(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
+  return launch_tiles(a.causal ? attention_wide_kernel<DP, QT, F16, true>
+                               : attention_wide_kernel<DP, QT, F16, false>,
+                      256, Wide<DP, QT>::kLds, a, p, st);
 }
 
 template <int DP, bool F16>
@@ -864,6 +1302,8 @@ hipError_t launch_dtype(const AttentionArgs& a, const AttentionPlan& p, hipStrea
     e = a.d <= 64    ? launch_few<64, F16>(a, p, st)
         : a.d <= 128 ? launch_few<128, F16>(a, p, st)
                      : launch_few<256, F16>(a, p, st);
+  else if (p.rows == kRowsOfWide)
+    e = launch_wide<128, 2, F16>(a, p, st);
   else if (a.d <= 64)
     e = launch_tile<64, 1, 4, F16>(a, p, st);
   else if (a.d <= 128)
@@ -882,69 +1322,126 @@ size_t workspace_bytes(const AttentionPlan& p, int d) {
   return (size_t)p.part_rows * ((size_t)p.splits * (d + 1) * 4 + (p.rows == 32 ? 0 : 8));
 }
 
+// A kernel's blocks on a full card (256 compute units; a constant, as the split decides
+// the order of sums): `room` at a time, a round of which takes `tile` us per key tile and
+// `start` us beside. Fitted to 16384 queries x 40 heads of 128 over 256 to 4608 keys
+// (10 rounds; measured 142 to 1457 us with 128 rows a block, 175 to 1331 us with 256).
+// In a round of at most half its blocks, those of a kernel that runs two a compute unit
+// have one to themselves and take 0.62 of the time.
+struct Rounds {
+  int rows;
+  int64_t room;
+  double tile, start, half;
+};
+constexpr Rounds kRounds64 = {kRowsOfTile, kMaxSplits, 1.1, 5.0, 0.62};
+constexpr Rounds kRounds128 = {kRowsOfTile, kMaxSplits, 1.93, 6.5, 0.62};
+constexpr Rounds kRoundsWide = {kRowsOfWide, kMaxSplits / 2, 1.70, 10.6, 1.0};
+constexpr Rounds kRounds256 = {kRowsOfTile, kMaxSplits / 2, 2.7, 8.0, 1.0};
+
+// The plan of least estimated time with this kernel; *cost is that time.
+AttentionPlan plan_tiles(const AttentionArgs& a, const Rounds& k, size_t workspace,
+                         double* cost) {
+  AttentionPlan p;
+  const int64_t group = a.q_heads / a.k_heads;
+  const int64_t rows = a.q_tokens * group, each = a.q_tokens / a.batch;
+  p.rows = k.rows;
+  int64_t tiles = 0;  // that there are, as far as is known here
+  if (a.batch == 1 || !a.q_offsets) {
+    p.slots = a.batch * ((each * group + k.rows - 1) / k.rows);
+    tiles = p.slots * a.k_heads;
+  } else {
+    p.slots = (rows + k.rows - 1) / k.rows + a.batch;
+    tiles = (rows / k.rows + (a.batch + 1) / 2) * a.k_heads;
+  }
+  const int64_t blocks = p.slots * a.k_heads;
+  p.whole = blocks;
+  p.grid = blocks;
+  const double keys = (double)(a.k_tokens / a.batch) / kTileKeys;
+  // key tiles of a row tile: causal ones differ, come longest first and even out
+  double mean = keys;
+  if (a.causal) mean = keys > (double)each / 64 ? keys - (double)each / 128 : keys / 2;
+  *cost = 1e30;
+  // n parts of each of the last `rest` tiles
+  auto consider = [&](int64_t whole, int64_t rest, int64_t n) {
+    if (n > 1 && n > keys / 4) n = (int64_t)(keys / 4);
+    if (n < 1) return;
+    AttentionPlan t = p;
+    if (n > 1) {
+      t.whole = whole;
+      t.splits = (int)n;
+      t.part_rows = (blocks - whole) * k.rows;
+      t.grid = whole + (blocks - whole) * n;
+    }
+    const size_t bytes = workspace_bytes(t, a.d);
+    if (bytes > workspace) return;
+    const int64_t all = rest * n, full = all / k.room, last = all % k.room;
+    double rounds = (double)full + (last == 0 ? 0 : 2 * last <= k.room ? k.half : 1.0);
+    if (a.causal && full > 0) rounds = (double)all / k.room;
+    double us = rounds * (mean / n * k.tile + k.start);
+    // the longest block
+    if (a.causal && us < keys / n * k.tile * k.half) us = keys / n * k.tile * k.half;
+    us += (double)(whole / k.room) * (mean * k.tile + k.start);
+    if (n > 1) us += 5 + (double)bytes / 2e6;
+    if (us < *cost) {
+      *cost = us;
+      p = t;
+    }
+  };
+  consider(0, tiles, 1);
+  if (tiles < k.room) {
+    for (int64_t n = 2; n <= 8; ++n) consider(0, tiles, n);
+    for (int64_t of = k.room / 2; of <= 2 * k.room; of *= 2)
+      if (tiles) consider(0, tiles, of / tiles);
+  } else if (!a.causal && tiles == blocks && tiles % k.room) {
+    const int64_t rest = tiles % k.room;
+    for (int64_t n = 2; n <= 8; ++n) consider(tiles - rest, rest, n);
+    for (int64_t of = k.room / 2; of <= 2 * k.room; of *= 2)
+      consider(tiles - rest, rest, of / rest);
+  }
+  return p;
+}
+
+AttentionPlan plan_few(const AttentionArgs& a, size_t workspace) {
+  AttentionPlan p;
+  const int64_t rows = a.q_tokens * (a.q_heads / a.k_heads), each = a.q_tokens / a.batch;
+  const int64_t keys = a.k_tokens / a.batch;
+  p.rows = 32;
+  int64_t tiles = (rows + 31) / 32;
+  if (a.batch == 1 || !a.q_offsets) {
+    p.slots = a.batch * ((each * (a.q_heads / a.k_heads) + 31) / 32);
+    tiles = p.slots;
+  } else {
+    p.slots = tiles + a.batch;
+    if (tiles < a.batch) tiles = a.batch;
+  }
+  // sequences may use less of their keys than there is room for: splits of a fixed
+  // length, about two rounds of a block per compute unit if all is used
+  const int64_t units = (keys + 31) / 32;
+  int64_t chunk = (units * tiles * a.k_heads + kMaxSplits - 1) / kMaxSplits;
+  if (chunk < 8) chunk = 8;
+  int64_t splits = (units + chunk - 1) / chunk;
+  if (splits > kMaxSplits) splits = kMaxSplits;
+  p.part_rows = a.q_tokens * a.q_heads;
+  p.splits = splits < 1 ? 1 : (int)splits;
+  while (workspace_bytes(p, a.d) > workspace) --p.splits;
+  if (p.splits == 1) p.part_rows = 0;
+  p.chunk = (int)((units + p.splits - 1) / p.splits);
+  p.grid = p.slots * a.k_heads * p.splits;
+  return p;
+}
+
 }  // namespace
 
 AttentionPlan plan_attention(const AttentionArgs& a, size_t workspace) {
-  AttentionPlan p;
-  const int64_t group = a.q_heads / a.k_heads;
-  const int64_t rows = a.q_tokens * group;  // of a key head
-  const int64_t keys = a.k_tokens / a.batch;
-  p.rows = rows <= 32 * (int64_t)a.batch ? 32 : kRowsOfTile;
-  if (a.q_offsets)
-    p.slots = (rows + p.rows - 1) / p.rows + a.batch;
-  else
-    p.slots = a.batch * ((rows / a.batch + p.rows - 1) / p.rows);
-  const int64_t blocks = p.slots * a.k_heads;
-  if (p.rows == 32) {
-    // sequences may use less of their keys than there is room for: splits of a fixed
-    // length, about two rounds of a block per compute unit if all is used
-    const int64_t units = (keys + 31) / 32;
-    int64_t tiles = (rows + 31) / 32;
-    tiles = (tiles > a.batch ? tiles : a.batch) * a.k_heads;
-    int64_t chunk = (units * tiles + kMaxSplits - 1) / kMaxSplits;
-    if (chunk < 8) chunk = 8;
-    int64_t splits = (units + chunk - 1) / chunk;
-    if (splits > kMaxSplits) splits = kMaxSplits;
-    p.part_rows = a.q_tokens * a.q_heads;
-    p.splits = splits < 1 ? 1 : (int)splits;
-    while (workspace_bytes(p, a.d) > workspace) --p.splits;
-    if (p.splits == 1) p.part_rows = 0;
-    p.chunk = (int)((units + p.splits - 1) / p.splits);
-    p.grid = blocks * p.splits;
-    return p;
-  }
-  // Blocks run `room` at a time. The tiles behind the last whole round (all, if there
-  // are not that many) are split over their keys into as many parts as cost least:
-  // rounds of the parts, each with its start and end (about 2.5 key tiles' time), and
-  // the join. In a round of at most half its blocks these have a compute unit to
-  // themselves and take 0.62 of the time. Causal tiles come longest first and even
-  // out by themselves if there is more than one round.
-  const int64_t room = a.d > 128 ? kMaxSplits / 2 : kMaxSplits;
-  const int64_t tiles = (keys + kTileKeys - 1) / kTileKeys;
-  const int64_t whole = blocks / room * room, rest = blocks - whole;
-  p.whole = blocks;
-  p.grid = blocks;
-  if (rest == 0 || (a.causal && whole > 0)) return p;
-  double least = 0;
-  auto consider = [&](int64_t n) {
-    if (n > tiles / 4) n = tiles / 4;
-    if (n < 1) return;
-    AttentionPlan t = p;
-    t.whole = whole;
-    t.splits = (int)n;
-    t.part_rows = rest * p.rows;
-    t.grid = whole + rest * n;
-    const int64_t full = rest * n / room, last = rest * n % room;
-    const double rounds = full + (last == 0 ? 0 : 2 * last <= room ? 0.62 : 1.0);
-    const double cost = rounds * (1.0 / n + 2.5 / tiles) + (n > 1 ? 5.0 / tiles : 0);
-    if (least != 0 && (cost >= least || workspace_bytes(t, a.d) > workspace)) return;
-    least = cost;
-    if (n > 1) p = t;
-  };
-  for (int64_t n = 1; n <= 8; ++n) consider(n);
-  // half a round, one, two
-  for (int64_t of = room / 2; of <= 2 * room; of *= 2) consider(of / rest);
-  return p;
+  const int64_t rows = a.q_tokens * (a.q_heads / a.k_heads);
+  if (a.tile == 32 || (a.tile == 0 && rows <= 32 * (int64_t)a.batch))
+    return plan_few(a, workspace);
+  double cost, wide;
+  if (a.d <= 64) return plan_tiles(a, kRounds64, workspace, &cost);
+  if (a.d > 128) return plan_tiles(a, kRounds256, workspace, &cost);
+  const AttentionPlan p = plan_tiles(a, kRounds128, workspace, &cost);
+  const AttentionPlan w = plan_tiles(a, kRoundsWide, workspace, &wide);
+  return a.tile ? (a.tile == kRowsOfWide ? w : p) : wide < cost ? w : p;
 }
 
 size_t attention_workspace(const AttentionArgs& a, const AttentionPlan& p) {
@@ -957,6 +1454,7 @@ void attention_use(AttentionArgs* a, const AttentionPlan& p, void* workspace) {
   a->k_each = (int)(a->k_tokens / a->batch);
   a->splits = p.splits;
   a->whole = (uint32_t)p.whole;
+  a->part_step = p.rows;
   if (p.splits == 1) return;
   char* at = static_cast<char*>(workspace);
   if (p.rows != 32) {

@@ -110,6 +110,8 @@ def test_attention_refusals(lib):
     assert st(batch=3, q_offsets=E) == 1 and st(batch=3, k_offsets=E) == 1
     for scale in (0.0, -0.1, NAN, INF):
         assert st(scale=scale) == 1
+    for tile, d in ((-1, 128), (1, 128), (64, 128), (512, 128), (256, 64), (256, 136)):
+        assert st(tile=tile, d=d) == 1
     for name in ("q", "k", "v", "out"):
         assert st(**{name: None}) == 1, name
         assert st(**{name: F + 8}) == 4, name

@@ -112,6 +112,41 @@ def test_lengths(q_lens, k_lens, hq, hk, d, causal, dtype):
 
 @DTYPES
 @pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("tile,hq,hk,d", [(256, 2, 2, 128), (256, 6, 2, 72), (256, 8, 1, 96),
+                                          (32, 3, 1, 128), (32, 4, 2, 64), (32, 2, 2, 256),
+                                          (128, 4, 1, 128), (128, 2, 1, 256)])
+@pytest.mark.parametrize("q_lens,k_lens", [([1], [64]), ([300], [300]), ([129], [200]),
+                                           ([200], [129]), ([1, 0, 7, 530, 64], [1, 5, 0, 530, 31]),
+                                           ([257, 3], [300, 1000]), ([600], [1500]),
+                                           ([40, 700], [2000, 90]), ([3, 2], [65, 193])])
+def test_each_kernel(q_lens, k_lens, tile, hq, hk, d, causal, dtype):
+    """The kernels that sizes choose from, at sizes that would choose another."""
+    rng = np.random.default_rng(sum(q_lens) + tile)
+    q, k, v = make(rng, q_lens, k_lens, hq, hk, d, dtype, 3.0)
+    out, lse = run_packed(q, k, v, q_lens, k_lens, causal, tile=tile)
+    check_packed(q, k, v, out, lse, q_lens, k_lens, causal)
+
+
+@DTYPES
+@pytest.mark.parametrize("tile,hq,hk,d", [(256, 4, 2, 128), (128, 4, 2, 128), (32, 4, 2, 128),
+                                          (128, 3, 1, 64), (128, 1, 1, 256)])
+def test_scores_that_climb_and_fall(tile, hq, hk, d, dtype):
+    """Keys whose scores rise from tile to tile move every row's reference many times;
+    falling ones never do; both with rows beside them that see other keys."""
+    rng = np.random.default_rng(d + tile)
+    n, length = 300, 700
+    q, k, v = make(rng, [n], [length], hq, hk, d, dtype, 0.3)
+    slope = torch.linspace(-1, 1, length, device=DEV)[:, None, None] * 40 / d ** 0.5
+    for sign in (1, -1):
+        qs = (q.float() + 1).to(dtype)
+        ks = (k.float() * 0.3 + sign * slope).to(dtype)
+        for causal in (False, True):
+            out, lse = cr.convrot_attention(qs, ks, v, causal=causal, return_lse=True, tile=tile)
+            close(qs, ks, v, out, lse, d ** -0.5, causal)
+
+
+@DTYPES
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
 @pytest.mark.parametrize("hq,hk,d", [(1, 1, 8), (3, 3, 16), (4, 2, 40), (5, 1, 64), (2, 1, 72),
                                      (4, 4, 80), (3, 1, 96), (2, 2, 112), (7, 1, 128),
                                      (2, 1, 136), (3, 3, 192), (4, 2, 256)])
@@ -137,9 +172,11 @@ def test_larger(hq, hk, d, n, length, causal, dtype):
 
 @DTYPES
 @pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
-@pytest.mark.parametrize("hq,hk,d,lens", [(4, 4, 128, [700, 65]), (8, 2, 64, [1, 300, 33]),
-                                          (2, 1, 256, [200, 5]), (4, 1, 72, [130, 64])])
-def test_each_query_finds_its_key(hq, hk, d, lens, causal, dtype):
+@pytest.mark.parametrize("hq,hk,d,lens,tile", [
+    (4, 4, 128, [700, 65], 0), (8, 2, 64, [1, 300, 33], 0), (2, 1, 256, [200, 5], 0),
+    (4, 1, 72, [130, 64], 0), (4, 4, 128, [700, 65], 256), (4, 1, 72, [130, 64], 256),
+    (4, 4, 128, [300, 65], 32)])
+def test_each_query_finds_its_key(hq, hk, d, lens, tile, causal, dtype):
     """Scores that leave one key: the output is that key's value, to the bit."""
     rng = np.random.default_rng(d)
     q, k, v = make(rng, lens, lens, hq, hk, d, dtype)
@@ -148,7 +185,7 @@ def test_each_query_finds_its_key(hq, hk, d, lens, causal, dtype):
                          + sum(lens[:i]) for i, n in enumerate(lens)])
     at = torch.from_numpy(at).to(DEV)
     q = (torch.sign(k)[at] * 4).repeat_interleave(hq // hk, 1)
-    out, _ = run_packed(q, k, v, lens, lens, causal, scale=8.0)
+    out, _ = run_packed(q, k, v, lens, lens, causal, scale=8.0, tile=tile)
     # equal keys share the weight: drop queries whose key comes again
     for h in range(hq):
         kh = k[:, h // (hq // hk)].float()
@@ -189,20 +226,21 @@ def test_a_padded_cache_and_what_it_holds_behind_its_use(dtype):
 
 
 @DTYPES
-@pytest.mark.parametrize("hq,hk,d,n,length", [(2, 2, 128, 200, 200), (4, 1, 64, 90, 300),
-                                              (2, 1, 256, 70, 70), (8, 1, 128, 2, 3000),
-                                              (3, 3, 40, 300, 100)])
+@pytest.mark.parametrize("hq,hk,d,n,length,tile", [
+    (2, 2, 128, 200, 200, 0), (4, 1, 64, 90, 300, 0), (2, 1, 256, 70, 70, 0),
+    (8, 1, 128, 2, 3000, 0), (3, 3, 40, 300, 100, 0), (2, 2, 128, 600, 600, 256),
+    (4, 2, 96, 300, 500, 256), (2, 2, 128, 200, 200, 32)])
 @pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
-def test_keys_that_the_mask_hides_have_no_part(hq, hk, d, n, length, what, dtype):
+def test_keys_that_the_mask_hides_have_no_part(hq, hk, d, n, length, tile, what, dtype):
     """Non-finite keys and values: queries that do not see them are what they are
     without them, the others get what they get from them."""
     rng = np.random.default_rng(n)
     q, k, v = make(rng, [n], [length], hq, hk, d, dtype)
-    clean = cr.convrot_attention(q, k, v, causal=True)
+    clean = cr.convrot_attention(q, k, v, causal=True, tile=tile)
     at = length - 1 - min(length, n) // 2      # seen by the later queries only
     col = d - 3
     v[at, :, col] = what
-    got = cr.convrot_attention(q, k, v, causal=True)
+    got = cr.convrot_attention(q, k, v, causal=True, tile=tile)
     sees = torch.arange(n, device=DEV) + length - n >= at
     assert torch.equal(got[~sees], clean[~sees])
     hit = got[sees][:, :, col]
@@ -212,15 +250,15 @@ def test_keys_that_the_mask_hides_have_no_part(hq, hk, d, n, length, what, dtype
     # two of opposite sign meet
     if math.isinf(what) and at + 1 < length:
         v[at + 1, :, col] = -what
-        got = cr.convrot_attention(q, k, v, causal=True)
+        got = cr.convrot_attention(q, k, v, causal=True, tile=tile)
         both = torch.arange(n, device=DEV) + length - n >= at + 1
         assert torch.isnan(got[both][:, :, col]).all()
         assert (got[sees & ~both][:, :, col] == what).all()
     # a key: its scores are hidden as well
     v[:, :, col] = 0
-    clean = cr.convrot_attention(q, k, v, causal=True)
+    clean = cr.convrot_attention(q, k, v, causal=True, tile=tile)
     k[at] = what
-    got = cr.convrot_attention(q, k, v, causal=True)
+    got = cr.convrot_attention(q, k, v, causal=True, tile=tile)
     assert torch.equal(got[~sees], clean[~sees])
 
 
@@ -249,12 +287,28 @@ def test_offsets_that_leave_the_tensors_stay_inside():
     guard = torch.full((300, 4, 64), 7.0, dtype=torch.bfloat16, device=DEV)
     for qo, ko in (([0, 20, 1 << 30], [0, 50, 1 << 30]), ([0, 20, 10], [0, 50, 40]),
                    ([0, 20, 100], [0, 50, -7]), ([0, 20, -(1 << 31)], [0, 50, 200])):
-        out = guard[100:200]
-        cr.convrot_attention(q, k, v, q_offsets=torch.tensor(qo, dtype=torch.int32, device=DEV),
-                             k_offsets=torch.tensor(ko, dtype=torch.int32, device=DEV), out=out)
-        torch.cuda.synchronize()
-        close(q[:10], k[:50], v[:50], out[:10], None, 1 / 8, False)
-        assert (guard[:100] == 7).all() and (guard[200:] == 7).all()
+        for tile in (32, 128):
+            out = guard[100:200]
+            cr.convrot_attention(q, k, v, tile=tile, out=out,
+                                 q_offsets=torch.tensor(qo, dtype=torch.int32, device=DEV),
+                                 k_offsets=torch.tensor(ko, dtype=torch.int32, device=DEV))
+            torch.cuda.synchronize()
+            close(q[:10], k[:50], v[:50], out[:10], None, 1 / 8, False)
+            assert (guard[:100] == 7).all() and (guard[200:] == 7).all()
+
+
+@DTYPES
+def test_a_last_round_that_is_split(dtype):
+    """More tiles than run at a time: those behind the last whole round go by parts."""
+    rng = np.random.default_rng(13)
+    n, length, heads, d = 2200, 2100, 33, 128
+    q, k, v = make(rng, [n], [length], heads, heads, d, dtype, 3.0)
+    for tile in (128, 256):
+        assert cr.convrot_attention_workspace_size(q, k, v, tile=tile) > 0
+        out, lse = cr.convrot_attention(q, k, v, return_lse=True, tile=tile)
+        for h in (0, 15, 30, 31, 32):
+            close(q[:, h:h + 1], k[:, h:h + 1], v[:, h:h + 1], out[:, h:h + 1], lse[h:h + 1],
+                  d ** -0.5, False)
 
 
 @DTYPES
@@ -322,15 +376,19 @@ def test_workspaces(n, length, hq, hk):
 
 def test_results_repeat_and_do_not_depend_on_the_device():
     rng = np.random.default_rng(10)
-    for n, length, hq, hk in ((300, 900, 4, 2), (1, 5000, 8, 1)):
+    for n, length, hq, hk, tile in ((300, 900, 4, 2, 0), (1, 5000, 8, 1, 0), (900, 900, 3, 3, 256),
+                                    (700, 700, 5, 5, 128)):
         q, k, v = make(rng, [n], [length], hq, hk, 128, torch.bfloat16)
-        want = cr.convrot_attention(q, k, v, causal=True)
-        for cus in (3, 64):
-            cr.convrot_set_compute_units(cus)
-            try:
-                assert torch.equal(cr.convrot_attention(q, k, v, causal=True), want)
-            finally:
-                cr.convrot_set_compute_units(0)
+        for causal in (False, True):
+            want, lse = cr.convrot_attention(q, k, v, causal=causal, tile=tile, return_lse=True)
+            close(q, k, v, want, lse, 128 ** -0.5, causal)
+            for cus in (0, 3, 64, 128, 192):
+                cr.convrot_set_compute_units(cus)
+                try:
+                    assert torch.equal(cr.convrot_attention(q, k, v, causal=causal, tile=tile),
+                                       want)
+                finally:
+                    cr.convrot_set_compute_units(0)
 
 
 def test_streams_and_graphs():
