@@ -38,10 +38,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 // A row's reference m is a largest score of it: it is raised when a score passes it by
 // kRoom / c, so weights stay below 2^(kRoom + kLift). Half weights are lifted so that
-// those of 2^-20 of the largest are normal numbers; the sum is lifted with them.
-constexpr float kRoom = 8.f;
+// those of 2^-18 of the reference's are normal numbers; the sum is lifted with them.
 template <bool F16>
-constexpr float kLift = F16 ? 6.f : 0.f;
+constexpr float kRoom = F16 ? 10.f : 32.f;
+template <bool F16>
+constexpr float kLift = F16 ? 4.f : 0.f;
 constexpr float kLowest = -3.402823466e38f;
 
 template <bool F16>
@@ -452,7 +453,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
     for (int d = 0; d < T::kDTiles; ++d) o[q][d] = (v16f){0};
   }
   const float c = a.scale * kLog2e;
-  const float room = kRoom / c;
+  const float room = kRoom<F16> / c;
 
   if (w.t0 < w.tiles) issue(w.t0, 0);
   for (int t = w.t0; t < w.tiles; ++t) {
@@ -567,10 +568,18 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
 
 // MFMAs of the pipeline below, whose accumulators stay where they are put: the output in
 // accumulation registers, which no vector instruction but the rare rescaling touches.
-template <bool F16>
+// `last`: with the wait before anything else may read what it and those before it wrote,
+// which copies that the compiler puts behind it do not know of.
+template <bool F16, bool LAST = false>
 __device__ __forceinline__ void mfma_out(v16f* o, const u4& v, const u4& p) {
-  if constexpr (F16)
+  if constexpr (F16 && LAST)
+    asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0\n\ts_nop 15"
+                 : "+a"(*o) : "v"(v), "v"(p));
+  else if constexpr (F16)
     asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(*o) : "v"(v), "v"(p));
+  else if constexpr (LAST)
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 15"
+                 : "+a"(*o) : "v"(v), "v"(p));
   else
     asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(*o) : "v"(v), "v"(p));
 }
@@ -610,9 +619,9 @@ __device__ __forceinline__ void settle_vec(v16f (&s)[N]) {
 // weights of unit u and the output of unit u - 1, one MFMA after the other with a few
 // vector instructions and an LDS read (three operands ahead) behind each. An operand
 // read serves both of a wave's 32-row halves.
-template <int DP, int QT>
+template <int DP, int QT, int NW>
 struct Wide {
-  static constexpr int kWaves = 4;
+  static constexpr int kWaves = NW;
   static constexpr int kRows = 32 * QT * kWaves;
   static constexpr int kRowBytes = DP * 2;
   static constexpr int kChunks = DP / 8;
@@ -626,10 +635,10 @@ struct Wide {
   static constexpr int kDTiles = DP / 32;
 };
 
-template <int DP, int QT, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(256, 1) void attention_wide_kernel(AttentionArgs a, uint32_t slots,
+template <int DP, int QT, int NW, bool F16, bool CAUSAL>
+__global__ __launch_bounds__(64 * NW, NW / 4) void attention_wide_kernel(AttentionArgs a, uint32_t slots,
                                                                 uint32_t xcds, uint32_t share) {
-  using T = Wide<DP, QT>;
+  using T = Wide<DP, QT, NW>;
   constexpr int kFrags = 2 * T::kSteps, kSlots = kFrags * QT, kAhead = 3, kRing = 4;
   constexpr int kElems = 16 * QT;  // of a lane and unit
   extern __shared__ __align__(1024) uint8_t lds[];
@@ -684,7 +693,7 @@ __global__ __launch_bounds__(256, 1) void attention_wide_kernel(AttentionArgs a,
     for (int d = 0; d < T::kDTiles; ++d) o[q][d] = (v16f){0};
   }
   const float c = a.scale * kLog2e;
-  const float room = kRoom / c;
+  const float room = kRoom<F16> / c;
 
   // lane's addresses of a unit's operands
   const uint8_t* kat[T::kSteps];
@@ -903,17 +912,14 @@ __global__ __launch_bounds__(256, 1) void attention_wide_kernel(AttentionArgs a,
       ++t;
     }
     // the last unit's output
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int d = 0; d < T::kDTiles; ++d) {
-        const u4 vf = read_v(h, d, last * T::kTileBytes + T::kUnitBytes);
-#pragma unroll
-        for (int q = 0; q < QT; ++q) mfma_out<F16>(&o[q][d], vf, pb[q][h]);
-      }
+    constexpr int kLast = 2 * T::kDTiles * QT;
+    static_for<kLast>([&](auto ii) __attribute__((always_inline)) {
+      constexpr int i = decltype(ii)::value, h = i / QT / T::kDTiles, d = i / QT % T::kDTiles,
+                    q = i % QT;
+      if constexpr (q == 0) ring[0] = read_v(h, d, last * T::kTileBytes + T::kUnitBytes);
+      mfma_out<F16, i == kLast - 1>(&o[q][d], ring[0], pb[q][h]);
+    });
   }
-#pragma unroll
-  for (int q = 0; q < QT; ++q) settle_acc(o[q]);
   if (CAUSAL) {
     wait_lgkm0();
     lds_barrier();
@@ -1015,7 +1021,7 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
 #pragma unroll
   for (int d = 0; d < kDTiles; ++d) o[d] = (v16f){0};
   float l = 0.f, raise_at = -__builtin_inff();
-  const float c = a.scale * kLog2e, room = kRoom / c;
+  const float c = a.scale * kLog2e, room = kRoom<F16> / c;
 
   int u = first + wave, stage = 0;
   if (u < last) issue(u, 0);
@@ -1275,11 +1281,11 @@ hipError_t launch_tile(const AttentionArgs& a, const AttentionPlan& p, hipStream
                       64 * NW, Kernel<DP, QT, NW, F16>::kLds, a, p, st);
 }
 
-template <int DP, int QT, bool F16>
+template <int DP, int QT, int NW, bool F16>
 hipError_t launch_wide(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
-  return launch_tiles(a.causal ? attention_wide_kernel<DP, QT, F16, true>
-                               : attention_wide_kernel<DP, QT, F16, false>,
-                      256, Wide<DP, QT>::kLds, a, p, st);
+  return launch_tiles(a.causal ? attention_wide_kernel<DP, QT, NW, F16, true>
+                               : attention_wide_kernel<DP, QT, NW, F16, false>,
+                      64 * NW, Wide<DP, QT, NW>::kLds, a, p, st);
 }
 
 template <int DP, bool F16>
@@ -1303,7 +1309,7 @@ hipError_t launch_dtype(const AttentionArgs& a, const AttentionPlan& p, hipStrea
         : a.d <= 128 ? launch_few<128, F16>(a, p, st)
                      : launch_few<256, F16>(a, p, st);
   else if (p.rows == kRowsOfWide)
-    e = launch_wide<128, 2, F16>(a, p, st);
+    e = launch_wide<128, 2, 4, F16>(a, p, st);
   else if (a.d <= 64)
     e = launch_tile<64, 1, 4, F16>(a, p, st);
   else if (a.d <= 128)
