@@ -365,8 +365,9 @@ def test_workspaces(n, length, hq, hk):
     want, lse = cr.convrot_attention(q, k, v, return_lse=True)
     close(q, k, v, want, lse, 128 ** -0.5, False)
     guard = torch.full((size + 1024,), 77, dtype=torch.uint8, device=DEV)
-    got = cr.convrot_attention(q, k, v, workspace=guard[256:256 + size])
-    assert torch.equal(got, want)
+    got, got_lse = cr.convrot_attention(q, k, v, workspace=guard[256:256 + size], return_lse=True)
+    assert torch.equal(got, want) and torch.equal(got_lse, lse)
+    assert torch.equal(cr.convrot_attention(q, k, v), want)
     assert (guard[:256] == 77).all() and (guard[256 + size:] == 77).all()
     for part in (0, 256, size // 2, size - 256):
         got, lse = cr.convrot_attention(q, k, v, workspace=guard[:part], return_lse=True)
@@ -385,8 +386,8 @@ def test_results_repeat_and_do_not_depend_on_the_device():
             for cus in (0, 3, 64, 128, 192):
                 cr.convrot_set_compute_units(cus)
                 try:
-                    assert torch.equal(cr.convrot_attention(q, k, v, causal=causal, tile=tile),
-                                       want)
+                    got = cr.convrot_attention(q, k, v, causal=causal, tile=tile, return_lse=True)
+                    assert torch.equal(got[0], want) and torch.equal(got[1], lse)
                 finally:
                     cr.convrot_set_compute_units(0)
 
