@@ -62,10 +62,13 @@ struct AttentionArgs {
   // normalised rows and their log2 sums, joined by a second launch
   int splits;
   uint32_t whole;
-  float* part;        // few rows: [split][q_tokens * q_heads][d]; else [tile][split][row][d]
-  float* part_lse;    // the same without d
-  int part_step;      // rows of a tile
-  int64_t* part_map;  // [tile][row]: row of the output, -1 for none; null for few rows
+  int few_blocks;   // few rows: blocks that the keys in use are shared out to
+  float* part;      // few rows: [block][row of its tile][d]; else [tile][split][row][d]
+  float* part_lse;  // the same without d
+  int part_step;    // rows of a tile
+  int64_t parts;    // rows of all blocks' parts
+  int64_t* part_map;  // [tile][row]: row of the output, -1 for none; few rows: by row of
+                      // the output, its first part and how many there are (int32 each)
 };
 // How a call is cut.
 struct AttentionPlan {
@@ -73,8 +76,9 @@ struct AttentionPlan {
   int64_t slots = 0;   // tiles per key head, at most
   int64_t whole = 0;   // tiles of a block each
   int splits = 1;      // parts of each of the others
-  int64_t part_rows = 0;
-  int chunk = 0;       // few rows: units of 32 keys of a split
+  int64_t part_rows = 0;  // entries of the map
+  int part_step = 0;      // rows of a tile's part
+  int few_blocks = 0;     // few rows: as above
   int64_t grid = 0;
 };
 // By sizes and the workspace's bytes alone, so that results do not depend on the device.

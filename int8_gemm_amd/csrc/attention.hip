@@ -33,6 +33,7 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 constexpr int kTileKeys = 64;   // keys of a copied tile
 constexpr int kRowsOfTile = 128;
 constexpr int kRowsOfWide = 256;
+constexpr int kFewUnits = 4;     // least units of a part, few rows
 constexpr int kMaxSplits = 512;  // two rounds of a block per compute unit
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -945,7 +946,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_wide_kernel(Attenti
 // go into the second product in two 16-bit parts, which costs nothing here.
 template <int DP>
 struct Few {
-  static constexpr int kWaves = DP == 256 ? 2 : 4;
+  static constexpr int kWaves = DP == 64 ? 4 : 2;
   static constexpr int kUnit = 32;
   static constexpr int kRowBytes = DP * 2;
   static constexpr int kChunks = DP / 8;
@@ -958,9 +959,70 @@ struct Few {
   static_assert(kWaves * (32 * kJoinRow + 64) * 4 <= kLds, "sums fit the ring");
 };
 
+// What a block does: a tile of a sequence's rows with one of the `splits` parts of its
+// keys, the sequence's blocks lying `heads` apart from block `first` on. All sequences
+// share a.few_blocks blocks by the keys that they use, whatever room their caches have
+// (0: a block a tile). False for a block without work.
+struct FewWork {
+  Where w;
+  int split, splits;
+  uint32_t first;
+};
+__device__ __forceinline__ bool locate_few(const AttentionArgs& a, uint32_t at, FewWork* t) {
+  const int lane = threadIdx.x & 63;
+  auto tiles_of = [&](const Where& w) { return (uint32_t)(w.lq * a.group + 31) / 32; };
+  auto units_of = [&](const Where& w) { return (uint32_t)(w.lk + 31) / 32; };
+  Where w = {0, 0, 0, 0, 0};
+  if (lane < a.batch) w = sequence(a, lane);
+  uint32_t chunk = INT32_MAX, before = 0;  // units of a part
+  if (a.few_blocks) {
+    float work = (float)tiles_of(w) * (float)units_of(w);
+    for (int b = 64 + lane; b < a.batch; b += 64) {
+      const Where v = sequence(a, b);
+      work += (float)tiles_of(v) * (float)units_of(v);
+    }
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) work += __shfl_xor(work, s);
+    // rounded up, so that there are no more parts than blocks
+    work *= 1.0001f * (float)a.k_heads / (float)a.few_blocks;
+    chunk = max((uint32_t)kFewUnits, (uint32_t)min(ceilf(work), 2147483520.0f));
+  }
+  for (int base = 0; base < a.batch; base += 64) {
+    if (base) {
+      w = {0, 0, 0, 0, 0};
+      if (base + lane < a.batch) w = sequence(a, base + lane);
+    }
+    const uint32_t tiles = tiles_of(w), units = units_of(w);  // both below 2^27
+    const uint32_t splits =
+        min(max((units + chunk - 1) / chunk, 1u), (uint32_t)kMaxSplits);
+    uint32_t upto = (uint32_t)min((uint64_t)tiles * splits, (uint64_t)1 << 24);
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const uint32_t below = __shfl_up(upto, s);
+      if (lane >= s) upto += below;
+    }
+    const uint64_t past = __ballot(upto > at - before);  // before <= at
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const uint32_t begin = l ? __builtin_amdgcn_readlane(upto, l - 1) : 0;
+      t->splits = __builtin_amdgcn_readlane(splits, l);
+      const uint32_t local = at - before - begin;
+      t->w.q0 = __builtin_amdgcn_readlane(w.q0, l);
+      t->w.k0 = __builtin_amdgcn_readlane(w.k0, l);
+      t->w.lq = __builtin_amdgcn_readlane(w.lq, l);
+      t->w.lk = __builtin_amdgcn_readlane(w.lk, l);
+      t->w.tile = (int)(local / (uint32_t)t->splits);
+      t->split = (int)(local % (uint32_t)t->splits);
+      t->first = at - (uint32_t)t->split;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
 template <int DP, bool F16>
-__global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(AttentionArgs a,
-                                                                                int chunk) {
+__global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(AttentionArgs a) {
   using T = Few<DP>;
   constexpr int kSteps = DP / 16, kDTiles = DP / 32;
   extern __shared__ __align__(1024) uint8_t lds[];
@@ -968,12 +1030,10 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
   const int group = a.group;
-  const uint32_t id = blockIdx.x;
-  const int split = (int)(id % (uint32_t)a.splits);
-  const uint32_t rest = id / (uint32_t)a.splits;
-  const int hk = (int)(rest % (uint32_t)a.k_heads);
-  Where w;
-  if (!find<32>(a, rest / (uint32_t)a.k_heads, &w)) return;
+  const int hk = (int)(blockIdx.x % (uint32_t)a.k_heads);
+  FewWork work;
+  if (!locate_few(a, blockIdx.x / (uint32_t)a.k_heads, &work)) return;
+  const Where& w = work.w;
 
   const int rows = w.lq * group, row0 = w.tile * 32;
   const int shift = w.lk - w.lq + 1;
@@ -982,10 +1042,10 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
     end = min(w.lk, max(0, min(rows - 1, row0 + 31) / group + shift));
     full = min(w.lk, max(0, row0 / group + shift));
   }
-  // units of this split, dealt to the waves: `chunk`, or more where the sequence is longer
+  // units of this part, dealt to the waves
   const int units = (end + T::kUnit - 1) / T::kUnit;
-  const int per = max(chunk, (units + a.splits - 1) / a.splits);
-  const int first = min(units, split * per), last = min(units, first + per);
+  const int per = (units + work.splits - 1) / work.splits;
+  const int first = min(units, work.split * per), last = min(units, first + per);
 
   u4 qf[kSteps];
   int seen;
@@ -1152,8 +1212,15 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
     const int jtoken = (row0 + jr) / group, jhead = hk * group + (row0 + jr) % group;
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[q] *= inv;
-    if (a.splits > 1) {
-      const int64_t at = ((int64_t)split * a.q_tokens + w.q0 + jtoken) * a.q_heads + jhead;
+    if (a.splits > 1 && e == 0 && work.split == 0) {
+      // where the row's parts are; none to join where the row has one
+      int2* map = reinterpret_cast<int2*>(a.part_map);
+      map[(int64_t)(w.q0 + jtoken) * a.q_heads + jhead] =
+          make_int2((int)(work.first * (uint32_t)a.k_heads + (uint32_t)hk) * a.part_step + jr,
+                    work.splits > 1 ? work.splits : 0);
+    }
+    if (work.splits > 1) {
+      const int64_t at = (int64_t)blockIdx.x * a.part_step + jr;
       if (e == 0) a.part_lse[at] = lse2;
       if (some) *reinterpret_cast<v4f*>(a.part + at * a.d + e) = acc;
       continue;
@@ -1175,18 +1242,27 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
   __shared__ float factor[kMaxSplits];
   __shared__ float red[2][kJoinThreads / 64];
   __shared__ __align__(16) float acc[kJoinThreads * 4];
-  // few rows: parts [split][row of the output]; tiles: [tile][split][row of the tile]
-  int64_t r = blockIdx.x, at = r, step = a.q_tokens * a.q_heads;
-  if (a.part_map) {
+  // few rows: a block a row of the output, which knows its parts; tiles: a block a row of
+  // a tile, which knows its row of the output
+  int64_t r = blockIdx.x, at, step;
+  int splits = a.splits;
+  if (a.tile == 32) {
+    const int token = (int)(r / a.q_heads);
+    if (a.q_offsets && (token < a.q_offsets[0] || token >= a.q_offsets[a.batch])) return;
+    const int2 map = reinterpret_cast<const int2*>(a.part_map)[r];
+    at = map.x;
+    splits = map.y;
+    step = (int64_t)a.k_heads * a.part_step;
+    // rows that offsets which decrease leave out have no entry: nothing outside is read
+    if (splits < 2 || splits > kMaxSplits || at < 0 || at + (splits - 1) * step >= a.parts) return;
+  } else {
     step = a.part_step;
-    at = r / step * step * a.splits + r % step;
+    at = r / step * step * splits + r % step;
     r = a.part_map[r];
     if (r < 0) return;
   }
   const int64_t token = r / a.q_heads;
   const int head = (int)(r % a.q_heads);
-  if (!a.part_map && a.q_offsets && (token < a.q_offsets[0] || token >= a.q_offsets[a.batch]))
-    return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int group = tid / lanes, groups = kJoinThreads / lanes, e = tid % lanes * 4;
 
@@ -1195,7 +1271,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
 #pragma unroll
   for (int i = 0; i < kMaxSplits / kJoinThreads; ++i) {
     const int s = tid + i * kJoinThreads;
-    x[i] = s < a.splits ? a.part_lse[at + s * step] : -__builtin_inff();
+    x[i] = s < splits ? a.part_lse[at + s * step] : -__builtin_inff();
     top = fmaxf(top, x[i]);
   }
 #pragma unroll
@@ -1208,7 +1284,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
 #pragma unroll
   for (int i = 0; i < kMaxSplits / kJoinThreads; ++i) {
     const float f = __builtin_amdgcn_exp2f(x[i] - top);  // 0 for a split that saw nothing
-    if (tid + i * kJoinThreads < a.splits) factor[tid + i * kJoinThreads] = f;
+    if (tid + i * kJoinThreads < splits) factor[tid + i * kJoinThreads] = f;
     sum += f;
   }
 #pragma unroll
@@ -1223,7 +1299,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
   if (e < a.d) {
     const float* from = a.part + at * a.d + e;
 #pragma unroll 8
-    for (int s = group; s < a.splits; s += groups) {
+    for (int s = group; s < splits; s += groups) {
       const float f = factor[s];
       const v4f p = *reinterpret_cast<const v4f*>(from + s * step * a.d);
 #pragma unroll
@@ -1297,7 +1373,7 @@ hipError_t launch_few(const AttentionArgs& a, const AttentionPlan& p, hipStream_
                                              hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
     if (e != hipSuccess) return e;
   }
-  kern<<<dim3((uint32_t)p.grid), dim3(64 * T::kWaves), T::kLds, st>>>(a, p.chunk);
+  kern<<<dim3((uint32_t)p.grid), dim3(64 * T::kWaves), T::kLds, st>>>(a);
   return hipGetLastError();
 }
 
@@ -1325,7 +1401,9 @@ hipError_t launch_dtype(const AttentionArgs& a, const AttentionPlan& p, hipStrea
 
 size_t workspace_bytes(const AttentionPlan& p, int d) {
   if (p.splits <= 1) return 0;
-  return (size_t)p.part_rows * ((size_t)p.splits * (d + 1) * 4 + (p.rows == 32 ? 0 : 8));
+  if (p.rows == 32)  // parts by block, places by row of the output
+    return (size_t)p.grid * p.part_step * (d + 1) * 4 + (size_t)p.part_rows * 8 + 8;
+  return (size_t)p.part_rows * ((size_t)p.splits * (d + 1) * 4 + 8);
 }
 
 // A kernel's blocks on a full card (256 compute units; a constant, as the split decides
@@ -1350,7 +1428,7 @@ AttentionPlan plan_tiles(const AttentionArgs& a, const Rounds& k, size_t workspa
   AttentionPlan p;
   const int64_t group = a.q_heads / a.k_heads;
   const int64_t rows = a.q_tokens * group, each = a.q_tokens / a.batch;
-  p.rows = k.rows;
+  p.rows = p.part_step = k.rows;
   int64_t tiles = 0;  // that there are, as far as is known here
   if (a.batch == 1 || !a.q_offsets) {
     p.slots = a.batch * ((each * group + k.rows - 1) / k.rows);
@@ -1409,30 +1487,40 @@ AttentionPlan plan_tiles(const AttentionArgs& a, const Rounds& k, size_t workspa
 
 AttentionPlan plan_few(const AttentionArgs& a, size_t workspace) {
   AttentionPlan p;
-  const int64_t rows = a.q_tokens * (a.q_heads / a.k_heads), each = a.q_tokens / a.batch;
-  const int64_t keys = a.k_tokens / a.batch;
+  const int64_t group = a.q_heads / a.k_heads, each = a.q_tokens / a.batch;
+  const int64_t rows = a.q_tokens * group;
   p.rows = 32;
-  int64_t tiles = (rows + 31) / 32;
-  if (a.batch == 1 || !a.q_offsets) {
-    p.slots = a.batch * ((each * (a.q_heads / a.k_heads) + 31) / 32);
-    tiles = p.slots;
-  } else {
-    p.slots = tiles + a.batch;
-    if (tiles < a.batch) tiles = a.batch;
+  p.slots = a.batch * ((each * group + 31) / 32);
+  int64_t longest = a.k_tokens / a.batch, part = each * group;
+  if (a.batch > 1 && a.q_offsets) {
+    p.slots = (rows + 31) / 32 + a.batch;
+    part = rows;
   }
-  // sequences may use less of their keys than there is room for: splits of a fixed
-  // length, about two rounds of a block per compute unit if all is used
-  const int64_t units = (keys + 31) / 32;
-  int64_t chunk = (units * tiles * a.k_heads + kMaxSplits - 1) / kMaxSplits;
-  if (chunk < 8) chunk = 8;
-  int64_t splits = (units + chunk - 1) / chunk;
-  if (splits > kMaxSplits) splits = kMaxSplits;
+  if (a.batch > 1 && a.k_offsets) longest = a.k_tokens;
+  p.part_step = part < 32 ? (int)part : 32;
   p.part_rows = a.q_tokens * a.q_heads;
-  p.splits = splits < 1 ? 1 : (int)splits;
-  while (workspace_bytes(p, a.d) > workspace) --p.splits;
-  if (p.splits == 1) p.part_rows = 0;
-  p.chunk = (int)((units + p.splits - 1) / p.splits);
-  p.grid = p.slots * a.k_heads * p.splits;
+  // a round of two blocks a compute unit (heads of 256: one), less about half a block a tile
+  const int64_t room = a.d > 128 ? kMaxSplits / 2 : kMaxSplits, tiles = p.slots * a.k_heads;
+  p.few_blocks = (int)(tiles < room ? room - tiles / 2 : room / 2);
+  // nothing to share out: short keys, blocks enough, or too many sequences to read
+  p.splits = longest > kFewUnits * 32 && tiles < 2 * room && a.batch <= 1024 ? kMaxSplits : 1;
+  p.grid = tiles + p.few_blocks;
+  const size_t bytes = workspace_bytes(p, a.d);
+  if (p.splits > 1 && bytes > workspace) {  // as many blocks as it holds
+    const size_t over = (bytes - workspace + (size_t)p.part_step * (a.d + 1) * 4 - 1) /
+                        ((size_t)p.part_step * (a.d + 1) * 4);
+    if (over >= (size_t)p.few_blocks) {
+      p.splits = 1;
+    } else {
+      p.few_blocks -= (int)over;
+      p.grid -= (int64_t)over;
+    }
+  }
+  if (p.splits == 1) {
+    p.few_blocks = 0;
+    p.part_rows = 0;
+    p.grid = tiles;
+  }
   return p;
 }
 
@@ -1460,15 +1548,17 @@ void attention_use(AttentionArgs* a, const AttentionPlan& p, void* workspace) {
   a->k_each = (int)(a->k_tokens / a->batch);
   a->splits = p.splits;
   a->whole = (uint32_t)p.whole;
-  a->part_step = p.rows;
+  a->part_step = p.part_step;
+  a->few_blocks = p.few_blocks;
+  a->tile = p.rows;
+  a->parts = p.grid * p.part_step;
   if (p.splits == 1) return;
   char* at = static_cast<char*>(workspace);
-  if (p.rows != 32) {
-    a->part_map = reinterpret_cast<int64_t*>(at);
-    at += p.part_rows * 8;
-  }
+  a->part_map = reinterpret_cast<int64_t*>(at);
+  at += (p.part_rows * 8 + 15) / 16 * 16;
   a->part = reinterpret_cast<float*>(at);
-  a->part_lse = a->part + (size_t)p.splits * (size_t)p.part_rows * a->d;
+  const int64_t parts = p.rows == 32 ? a->parts : p.splits * p.part_rows;
+  a->part_lse = a->part + (size_t)parts * a->d;
 }
 
 hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& p, DType dt,

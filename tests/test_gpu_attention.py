@@ -199,6 +199,31 @@ def test_each_query_finds_its_key(hq, hk, d, lens, tile, causal, dtype):
 
 
 @DTYPES
+@pytest.mark.parametrize("batch,hq,hk,d,room", [(1, 8, 2, 128, 9000), (12, 8, 2, 128, 2000),
+                                                (70, 4, 1, 64, 700), (200, 2, 1, 64, 300),
+                                                (5, 6, 3, 256, 3000), (1030, 1, 1, 64, 200)])
+def test_single_tokens_over_caches_of_different_use(batch, hq, hk, d, room, dtype):
+    rng = np.random.default_rng(batch)
+    used = rng.integers(0, room + 1, batch)
+    used[0], used[-1] = room, 1 if batch > 1 else room
+    q = dev(rng.standard_normal((batch, 1, hq, d)) * 2, dtype)
+    k = dev(rng.standard_normal((batch, room, hk, d)), dtype)
+    v = dev(rng.standard_normal((batch, room, hk, d)), dtype)
+    lens = torch.from_numpy(used).to(torch.int32).to(DEV)
+    out, lse = cr.convrot_attention(q, k, v, k_lens=lens, causal=True, return_lse=True)
+    # the same packed, by offsets
+    flat = [torch.cat([t[b, :n] for b, n in enumerate(used)]) for t in (k, v)]
+    packed, packed_lse = cr.convrot_attention(q[:, 0], *flat, q_offsets=offsets([1] * batch),
+                                              k_offsets=offsets(used), return_lse=True)
+    some = range(batch) if batch <= 70 else [0, 1, 63, 64, 65, 127, 128, batch - 2, batch - 1]
+    for b in some:
+        n = int(used[b])
+        close(q[b], k[b, :n], v[b, :n], out[b], lse[:, b:b + 1], d ** -0.5, True)
+        close(q[b], k[b, :n], v[b, :n], packed[b:b + 1], packed_lse[:, b:b + 1], d ** -0.5, True)
+    assert (packed - out[:, 0]).abs().max() <= 2 * H16[dtype][0] * 8
+
+
+@DTYPES
 def test_a_padded_cache_and_what_it_holds_behind_its_use(dtype):
     rng = np.random.default_rng(3)
     batch, room, hq, hk, d = 5, 300, 8, 2, 128
