@@ -972,9 +972,27 @@ __device__ __forceinline__ bool locate_few(const AttentionArgs& a, uint32_t at, 
   const int lane = threadIdx.x & 63;
   auto tiles_of = [&](const Where& w) { return (uint32_t)(w.lq * a.group + 31) / 32; };
   auto units_of = [&](const Where& w) { return (uint32_t)(w.lk + 31) / 32; };
+  // rounded up, so that there are no more parts than blocks
+  const float share = 1.0001f * (float)a.k_heads / (float)max(a.few_blocks, 1);
+  auto units_of_part = [&](float work) {
+    return max((uint32_t)kFewUnits, (uint32_t)min(ceilf(work * share), 2147483520.0f));
+  };
+  auto splits_of = [](uint32_t units, uint32_t chunk) {
+    return min(max((units + chunk - 1) / chunk, 1u), (uint32_t)kMaxSplits);
+  };
+  uint32_t chunk = INT32_MAX, before = 0;  // units of a part
+  if (a.batch == 1) {  // no counting
+    t->w = sequence(a, 0);
+    const uint32_t tiles = tiles_of(t->w), units = units_of(t->w);
+    if (a.few_blocks) chunk = units_of_part((float)tiles * (float)units);
+    t->splits = (int)splits_of(units, chunk);
+    t->w.tile = (int)(at / (uint32_t)t->splits);
+    t->split = (int)(at % (uint32_t)t->splits);
+    t->first = at - (uint32_t)t->split;
+    return (uint32_t)t->w.tile < tiles;
+  }
   Where w = {0, 0, 0, 0, 0};
   if (lane < a.batch) w = sequence(a, lane);
-  uint32_t chunk = INT32_MAX, before = 0;  // units of a part
   if (a.few_blocks) {
     float work = (float)tiles_of(w) * (float)units_of(w);
     for (int b = 64 + lane; b < a.batch; b += 64) {
@@ -983,9 +1001,7 @@ __device__ __forceinline__ bool locate_few(const AttentionArgs& a, uint32_t at, 
     }
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) work += __shfl_xor(work, s);
-    // rounded up, so that there are no more parts than blocks
-    work *= 1.0001f * (float)a.k_heads / (float)a.few_blocks;
-    chunk = max((uint32_t)kFewUnits, (uint32_t)min(ceilf(work), 2147483520.0f));
+    chunk = units_of_part(work);
   }
   for (int base = 0; base < a.batch; base += 64) {
     if (base) {
@@ -993,8 +1009,7 @@ __device__ __forceinline__ bool locate_few(const AttentionArgs& a, uint32_t at, 
       if (base + lane < a.batch) w = sequence(a, base + lane);
     }
     const uint32_t tiles = tiles_of(w), units = units_of(w);  // both below 2^27
-    const uint32_t splits =
-        min(max((units + chunk - 1) / chunk, 1u), (uint32_t)kMaxSplits);
+    const uint32_t splits = splits_of(units, chunk);
     uint32_t upto = (uint32_t)min((uint64_t)tiles * splits, (uint64_t)1 << 24);
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
