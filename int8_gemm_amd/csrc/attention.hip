@@ -569,20 +569,26 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
 
 // MFMAs of the pipeline below, whose accumulators stay where they are put: the output in
 // accumulation registers, which no vector instruction but the rare rescaling touches.
-// `last`: with the wait before anything else may read what it and those before it wrote,
-// which copies that the compiler puts behind it do not know of.
-template <bool F16, bool LAST = false>
+// ACC: in accumulation registers. LAST: with the wait before anything else may read what
+// it and those before it wrote, which copies that the compiler puts behind it do not
+// know of.
+template <bool F16, bool ACC, bool LAST = false>
 __device__ __forceinline__ void mfma_out(v16f* o, const u4& v, const u4& p) {
-  if constexpr (F16 && LAST)
-    asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0\n\ts_nop 15"
-                 : "+a"(*o) : "v"(v), "v"(p));
-  else if constexpr (F16)
-    asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(*o) : "v"(v), "v"(p));
-  else if constexpr (LAST)
-    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 15"
-                 : "+a"(*o) : "v"(v), "v"(p));
-  else
-    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(*o) : "v"(v), "v"(p));
+#define CONVROT_MFMA_OUT(NAME, CLASS)                                                          \
+  if constexpr (LAST)                                                                          \
+    asm volatile(NAME " %0, %1, %2, %0\n\ts_nop 15" : CLASS(*o) : "v"(v), "v"(p));             \
+  else                                                                                         \
+    asm volatile(NAME " %0, %1, %2, %0" : CLASS(*o) : "v"(v), "v"(p))
+  if constexpr (F16 && ACC) {
+    CONVROT_MFMA_OUT("v_mfma_f32_32x32x16_f16", "+a");
+  } else if constexpr (F16) {
+    CONVROT_MFMA_OUT("v_mfma_f32_32x32x16_f16", "+v");
+  } else if constexpr (ACC) {
+    CONVROT_MFMA_OUT("v_mfma_f32_32x32x16_bf16", "+a");
+  } else {
+    CONVROT_MFMA_OUT("v_mfma_f32_32x32x16_bf16", "+v");
+  }
+#undef CONVROT_MFMA_OUT
 }
 template <bool F16>
 __device__ __forceinline__ void mfma_first(v16f* s, const u4& k, const u4& q, const v16f& below) {
@@ -623,6 +629,7 @@ __device__ __forceinline__ void settle_vec(v16f (&s)[N]) {
 template <int DP, int QT, int NW>
 struct Wide {
   static constexpr int kWaves = NW;
+  static constexpr bool kAcc = DP * QT > 64;  // where vector registers do not hold the output
   static constexpr int kRows = 32 * QT * kWaves;
   static constexpr int kRowBytes = DP * 2;
   static constexpr int kChunks = DP / 8;
@@ -637,7 +644,7 @@ struct Wide {
 };
 
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW, NW / 4) void attention_wide_kernel(AttentionArgs a, uint32_t slots,
+__global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kernel(AttentionArgs a, uint32_t slots,
                                                                 uint32_t xcds, uint32_t share) {
   using T = Wide<DP, QT, NW>;
   constexpr int kFrags = 2 * T::kSteps, kSlots = kFrags * QT, kAhead = 3, kRing = 4;
@@ -761,7 +768,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_wide_kernel(Attenti
           mfma_score<F16>(&nxt[q], ring[n % kRing], qf[q][n]);
       } else if constexpr (kPv) {
         constexpr int i = n - T::kSteps, h = i / T::kDTiles, d = i % T::kDTiles;
-        mfma_out<F16>(&o[q][d], ring[n % kRing], pin[q][h]);
+        mfma_out<F16, T::kAcc>(&o[q][d], ring[n % kRing], pin[q][h]);
       }
       constexpr int e0 = slot * kElems / kSlots, e1 = (slot + 1) * kElems / kSlots;
       constexpr int g0 = slot == 0 ? 0 : (slot - 1) * kElems / kSlots;
@@ -805,7 +812,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_wide_kernel(Attenti
     for (int q = 0; q < QT; ++q) raise |= top[q] > raise_at[q];
     if (__any(raise)) {
 #pragma unroll
-      for (int q = 0; q < QT; ++q) settle_acc(o[q]);
+      for (int q = 0; q < QT; ++q) {
+        if constexpr (T::kAcc)
+          settle_acc(o[q]);
+        else
+          settle_vec(o[q]);
+      }
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
         const float to = fmaxf(top[q], other_half(top[q]));
@@ -834,7 +846,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_wide_kernel(Attenti
           for (int i = 0; i < 16; ++i) o[q][d][i] *= alpha;
       }
 #pragma unroll
-      for (int q = 0; q < QT; ++q) settle_acc(o[q]);
+      for (int q = 0; q < QT; ++q) {
+        if constexpr (T::kAcc)
+          settle_acc(o[q]);
+        else
+          settle_vec(o[q]);
+      }
       settle_vec(below);
     }
   };
@@ -918,7 +935,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_wide_kernel(Attenti
       constexpr int i = decltype(ii)::value, h = i / QT / T::kDTiles, d = i / QT % T::kDTiles,
                     q = i % QT;
       if constexpr (q == 0) ring[0] = read_v(h, d, last * T::kTileBytes + T::kUnitBytes);
-      mfma_out<F16, i == kLast - 1>(&o[q][d], ring[0], pb[q][h]);
+      mfma_out<F16, T::kAcc, i == kLast - 1>(&o[q][d], ring[0], pb[q][h]);
     });
   }
   if (CAUSAL) {
@@ -1402,7 +1419,7 @@ hipError_t launch_dtype(const AttentionArgs& a, const AttentionPlan& p, hipStrea
   else if (p.rows == kRowsOfWide)
     e = launch_wide<128, 2, 4, F16>(a, p, st);
   else if (a.d <= 64)
-    e = launch_tile<64, 1, 4, F16>(a, p, st);
+    e = launch_wide<64, 1, 4, F16>(a, p, st);
   else if (a.d <= 128)
     e = launch_tile<128, 1, 4, F16>(a, p, st);
   else
@@ -1432,10 +1449,10 @@ struct Rounds {
   int64_t room;
   double tile, start, half;
 };
-constexpr Rounds kRounds64 = {kRowsOfTile, kMaxSplits, 1.1, 5.0, 0.62};
+constexpr Rounds kRounds64 = {kRowsOfTile, kMaxSplits * 3 / 2, 1.59, 4.3, 0.62};
 constexpr Rounds kRounds128 = {kRowsOfTile, kMaxSplits, 1.93, 6.5, 0.62};
 constexpr Rounds kRoundsWide = {kRowsOfWide, kMaxSplits / 2, 1.70, 10.6, 1.0};
-constexpr Rounds kRounds256 = {kRowsOfTile, kMaxSplits / 2, 2.7, 8.0, 1.0};
+constexpr Rounds kRounds256 = {kRowsOfTile, kMaxSplits / 2, 2.56, 7.8, 1.0};
 
 // The plan of least estimated time with this kernel; *cost is that time.
 AttentionPlan plan_tiles(const AttentionArgs& a, const Rounds& k, size_t workspace,

@@ -7,7 +7,8 @@ attention kernels, branches included, behind each of them (eight passes):
   - 12 wait states before anything but a matrix instruction touches its result, or a
     matrix instruction reads it as an operand or as part of another accumulator;
   - 8 before anything but a matrix instruction writes the accumulator it started from.
-A matrix instruction that goes on with the same accumulator needs none."""
+A matrix instruction that goes on with the same accumulator needs none. And before each:
+  - 2 behind a vector instruction that writes an operand of it."""
 
 import os
 import re
@@ -20,7 +21,7 @@ import int8_gemm_amd as cr
 
 OBJDUMP = next((p for p in ("/opt/rocm/llvm/bin/llvm-objdump", shutil.which("llvm-objdump"))
                 if p and os.path.exists(p)), None)
-RESULT, STARTED = 12, 8
+RESULT, STARTED, OPERAND = 12, 8, 2
 
 
 def registers(operand):
@@ -102,6 +103,11 @@ def test_matrix_results_are_waited_for(kernels):
     seen, bad = 0, []
     for name, code in kernels.items():
         for i, c in enumerate(code):
+            near = code[i + 1:i + 1 + OPERAND]
+            if c.op.startswith("v_") and not c.mfma and any(d.mfma or d.target for d in near):
+                for d, gone in paths(code, i, OPERAND):
+                    if d.mfma and c.writes & set().union(*d.regs[1:4]):
+                        bad.append((name, gone, c.text, d.text))
             if not c.mfma:
                 continue
             seen += 1
