@@ -153,7 +153,7 @@ def test_workspace_sizes(lib):
     assert lib.convrot_attention_workspace_size(None) == 0
     assert size(d=60) == 0 and size(batch=0) == 0 and size(scale=0.0) == 0
     # enough tiles for the card, and keys too few to split
-    assert size(q_tokens=32760, k_tokens=32760, q_heads=40, k_heads=40) == 0
+    assert size(q_tokens=32760, k_tokens=32760, q_heads=40, k_heads=40, d=128) == 0
     assert size(q_tokens=1, k_tokens=64) == 0
     one = size(q_tokens=1, k_tokens=30000)
     assert one > 0
