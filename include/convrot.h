@@ -625,7 +625,8 @@ typedef struct convrot_attention_args {
   int32_t tile;
 } convrot_attention_args;
 /* Workspace bytes of a call of these sizes (its pointers are not read, but whether
- * q_offsets is null counts); 0 where none is used, and for invalid sizes. */
+ * q_offsets and k_offsets are null counts); 0 where none is used, and for invalid
+ * sizes. */
 size_t convrot_attention_workspace_size(const convrot_attention_args* args);
 convrot_status convrot_attention(const convrot_attention_args* args, void* workspace,
                                  size_t workspace_bytes, void* stream);

@@ -400,6 +400,16 @@ __device__ __forceinline__ void mask(v16f* s, int key0, int seen) {
     if (8 * (i >> 2) + (i & 3) >= left) (*s)[i] = -__builtin_inff();
 }
 
+// ---- 128 rows a block: a wave's 32, tile after tile ----------------------------
+//
+// Two 64-key tiles of K and V in LDS, one in use and one on its way. Heads of 65 to 128
+// elements run two blocks a compute unit, so that one block's start, softmax and end lie
+// under the other's products: the better choice for keys of a few tiles and for rows that
+// do not fill the card with 256 (16384 queries x 40 heads of 128 over 256 keys: 142 us, with
+// 256 rows a block 175; over 4608: 1457 and 1331). 32760 x 40 heads over 512 keys take 424 us,
+// 0.81 PFLOP/s: of a round's 21 us 6.5 are a block's start and end, and the MFMAs are
+// busy 0.37 of the cycles at 2.0 GHz. Heads of up to 256: 8192 x 8 heads of 256 in
+// 685 us (0.80 PFLOP/s), one block a compute unit, its output a whole 128 registers a lane.
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
 __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(AttentionArgs a,
                                                                               uint32_t slots,
@@ -626,6 +636,18 @@ __device__ __forceinline__ void settle_vec(v16f (&s)[N]) {
 // weights of unit u and the output of unit u - 1, one MFMA after the other with a few
 // vector instructions and an LDS read (three operands ahead) behind each. An operand
 // read serves both of a wave's 32-row halves.
+//
+// Heads of 65 to 128 elements: 256 rows a block, one wave a SIMD with the output in
+// accumulation registers. 32760 x 32760 x 40 heads of 128 take 17.9 to 18.5 ms, 1.2
+// PFLOP/s, bound by power: the clock falls to 1.83 GHz with the MFMAs busy 0.59 of the
+// cycles, and on zeros the same instructions reach 1.51 PFLOP/s. 4.8 vector instructions
+// a score; no bank conflicts. Eight waves of 32 rows take twice the LDS reads: 1.53
+// PFLOP/s on zeros, 1.14 on random values (this: 1.21 then). Causal, 16384 x 16384 x 16
+// heads: 0.94 ms (1.17 PFLOP/s of the scores that count).
+//
+// Heads of up to 64: 128 rows a block, 32 a wave, the output beside the scores, three waves
+// a SIMD; half the products a score, so bound by vector instructions and their latency.
+// 16384 x 16384 x 16 heads of 64: 1.11 ms (0.99 PFLOP/s), the kernel above 1.18.
 template <int DP, int QT, int NW>
 struct Wide {
   static constexpr int kWaves = NW;
@@ -644,8 +666,8 @@ struct Wide {
 };
 
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kernel(AttentionArgs a, uint32_t slots,
-                                                                uint32_t xcds, uint32_t share) {
+__global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kernel(
+    AttentionArgs a, uint32_t slots, uint32_t xcds, uint32_t share) {
   using T = Wide<DP, QT, NW>;
   constexpr int kFrags = 2 * T::kSteps, kSlots = kFrags * QT, kAhead = 3, kRing = 4;
   constexpr int kElems = 16 * QT;  // of a lane and unit
@@ -661,7 +683,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
   const int8_t* kbase = head_bytes(a.k, w.w, a.k_stride, a.k_head_stride, w.hk);
   const int8_t* vbase = head_bytes(a.v, w.w, a.v_stride, a.v_head_stride, w.hk);
   const uint32_t kstride = (uint32_t)a.k_stride * 2, vstride = (uint32_t)a.v_stride * 2;
-  auto copy = [&](const int8_t* base, uint32_t stride, bool values, int t, int to) __attribute__((always_inline)) {
+  auto copy = [&](const int8_t* base, uint32_t stride, bool values, int t,
+                  int to) __attribute__((always_inline)) {
     const int last = w.w.lk - 1 - t * kTileKeys;  // rows behind it repeat it
     const int8_t* p = base + (int64_t)t * kTileKeys * stride;
 #pragma unroll
@@ -715,7 +738,9 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
     const int chunk = d * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
     vat[d] = lds + T::kV + r * T::kRowBytes + v_slot<DP>(r, chunk) * 16 + (lane & 1) * 8;
   }
-  auto read_k = [&](int st, int at) __attribute__((always_inline)) { return *reinterpret_cast<const u4*>(kat[st] + at); };
+  auto read_k = [&](int st, int at) __attribute__((always_inline)) {
+    return *reinterpret_cast<const u4*>(kat[st] + at);
+  };
   auto read_v = [&](int h, int d, int at) __attribute__((always_inline)) {
     typedef __attribute__((address_space(3))) s4* lp;
     uint8_t* p = const_cast<uint8_t*>(vat[d]) + at + h * 16 * T::kRowBytes;
@@ -731,7 +756,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
   auto step = [&](auto pv, v16f(&cur)[QT], v16f(&nxt)[QT], u4(&pin)[QT][2], u4(&pout)[QT][2],
                   int k_at, int v_at, int next_at) __attribute__((always_inline)) {
     constexpr bool kPv = decltype(pv)::value;
-    auto fetch = [&](auto nn) __attribute__((always_inline)) {  // operand n of this step, or of the next
+    // operand n of this step, or of the next
+    auto fetch = [&](auto nn) __attribute__((always_inline)) {
       constexpr int n = decltype(nn)::value;
       if constexpr (n < T::kSteps) {
         ring[n % kRing] = read_k(n, k_at);
@@ -797,7 +823,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
     for (int e = (kSlots - 1) * kElems / kSlots; e < kElems; ++e) gather(e);
   };
   // Scores of a unit before they become weights: its mask, and a new m where one is passed
-  auto settle = [&](v16f(&s)[QT], v16f(&before)[QT], u4(&p)[QT][2], int key0) __attribute__((always_inline)) {
+  auto settle = [&](v16f(&s)[QT], v16f(&before)[QT], u4(&p)[QT][2],
+                    int key0) __attribute__((always_inline)) {
     if (key0 + 32 > w.full) {
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
@@ -961,6 +988,11 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
 // streams its own units of 32 keys, copied two ahead into its own part of LDS, and
 // waits for no other wave until the end, where the waves' sums are joined. Weights
 // go into the second product in two 16-bit parts, which costs nothing here.
+//
+// One token of 32 / 4 heads of 128 against 100000 keys streams at 4.7 TB/s, 32 caches of
+// 4096 keys at 4.9 (a large copy: 4.9); 12 caches of 1 to 8192 used keys take 48 us, 4.7 of
+// them the second launch, which joins the parts; blocks cut by the room of the caches took
+// 64.
 template <int DP>
 struct Few {
   static constexpr int kWaves = DP == 64 ? 4 : 2;
@@ -1259,8 +1291,8 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
     }
     if (a.lse && e == 0) a.lse[(int64_t)jhead * a.q_tokens + w.q0 + jtoken] = lse2 * kLn2;
     const u2 f = {pack16x2<F16>(acc[0], acc[1]), pack16x2<F16>(acc[2], acc[3])};
-    *reinterpret_cast<u2*>(a.out + (int64_t)(w.q0 + jtoken) * a.out_stride + (int64_t)jhead * a.out_head_stride + e) =
-        f;
+    *reinterpret_cast<u2*>(a.out + (int64_t)(w.q0 + jtoken) * a.out_stride +
+                           (int64_t)jhead * a.out_head_stride + e) = f;
   }
 }
 
@@ -1352,7 +1384,8 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
     }
     const float inv = none ? 0.f : 1.0f / sum;
     const u2 f = {pack16x2<F16>(v[0] * inv, v[1] * inv), pack16x2<F16>(v[2] * inv, v[3] * inv)};
-    *reinterpret_cast<u2*>(a.out + token * a.out_stride + (int64_t)head * a.out_head_stride + e) = f;
+    *reinterpret_cast<u2*>(a.out + token * a.out_stride + (int64_t)head * a.out_head_stride + e) =
+        f;
   }
 }
 
@@ -1495,7 +1528,8 @@ size_t workspace_bytes(const AttentionPlan& p, int d) {
 // A kernel's blocks on a full card (256 compute units; a constant, as the split decides
 // the order of sums): `room` at a time, a round of which takes `tile` us per key tile and
 // `start` us beside. Fitted to 16384 queries x 40 heads of 128 over 256 to 4608 keys
-// (10 rounds; measured 142 to 1457 us with 128 rows a block, 175 to 1331 us with 256).
+// (10 rounds; measured 142 to 1457 us with 128 rows a block, 175 to 1331 us with 256),
+// 48 heads of 64 and 16 of 256 alike.
 // In a round of at most half its blocks, those of a kernel that runs two a compute unit
 // have one to themselves and take 0.62 of the time.
 struct Rounds {
