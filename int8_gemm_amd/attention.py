@@ -169,7 +169,7 @@ def convrot_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None,
         raise ValueError("k_weight and k_out need k")
     pt, rows, pairs = None, 0, 0
     if table is not None:
-        shape = table.shape
+        shape = table.shape if isinstance(table, torch.Tensor) else ()
         if len(shape) != 3 or shape[2] != 2:
             raise ValueError(f"table must be [rows, pairs, 2] (got shape {tuple(shape)})")
         pt = _tensor(table, "table", torch.float32, shape, dev)
@@ -189,7 +189,8 @@ def _output(out, name: str, like: torch.Tensor, dev: int):
 
 
 def _weight(t, name: str, dtype, dev: int, d: int, heads: int) -> int:
-    shape = (heads * d,) if heads == 1 or t.dim() == 1 else (heads, d)
+    flat = heads == 1 or not isinstance(t, torch.Tensor) or t.dim() == 1
+    shape = (heads * d,) if flat else (heads, d)
     return _tensor(t, name, dtype, shape, dev)
 
 
@@ -222,7 +223,7 @@ def _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale, tile):
     pkl = None if k_lens is None else _tensor(k_lens, "k_lens", _I32, (batch,), dev)
     return _AttentionArgs(pq, pk, pv, None, None, pqo, pko, pkl, qs, qh, ks, kh, vs, vh, 0, 0,
                           tokens, k_tokens, batch, heads, k_heads, d, causal, _DTYPES[dtype],
-                          d ** -0.5 if scale is None else scale, tile), dev
+                          max(d, 1) ** -0.5 if scale is None else scale, tile), dev
 
 
 def convrot_attention_workspace_size(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
@@ -262,7 +263,7 @@ def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
         a.lse = lse.data_ptr()
     pw, size = None, 0
     if workspace is not None:
-        size = workspace.numel()
+        size = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
         pw = _tensor(workspace, "workspace", _U8, (size,), dev)
     else:
         size = load_library().convrot_attention_workspace_size(ctypes.byref(a))

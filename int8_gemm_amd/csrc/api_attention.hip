@@ -34,6 +34,7 @@ struct Box {
                          (heads == 1 || head_stride >= (tokens - 1) * stride + d);
     return by_token || by_head;
   }
+  Box turned() const { return {p, heads, tokens, d, head_stride, stride, size}; }
   bool same(const Box& o) const {
     return p == o.p && stride == o.stride && head_stride == o.head_stride && heads == o.heads;
   }
@@ -46,9 +47,8 @@ bool meet(uint64_t a, uint64_t na, uint64_t b, uint64_t nb, uint64_t period) {
   return gap < na || period - gap < nb;
 }
 
-// Whether two boxes may share memory. Column ranges of one wider tensor do not,
-// nor do interleaved heads, although the memory they span does.
-bool clash(const Box& a, const Box& b) {
+// Whether two boxes may share memory, by their places within a token's stride and a head's.
+bool clash_by_token(const Box& a, const Box& b) {
   if (a.empty() || b.empty()) return false;
   if (a.at() + a.extent() <= b.at() || b.at() + b.extent() <= a.at()) return false;
   const uint64_t size = a.size;
@@ -63,6 +63,12 @@ bool clash(const Box& a, const Box& b) {
   if (a.head_stride != b.head_stride || a.head_stride <= 0) return true;
   return meet(a.at(), (uint64_t)a.d * size, b.at(), (uint64_t)b.d * size,
               (uint64_t)a.head_stride * size);
+}
+
+// Column ranges of one wider tensor do not clash, nor do interleaved heads, although the
+// memory they span does; the same with heads outside of tokens.
+bool clash(const Box& a, const Box& b) {
+  return clash_by_token(a, b) && clash_by_token(a.turned(), b.turned());
 }
 
 // Strides of a tensor whose rows are read or written 16 bytes at a time.
@@ -107,7 +113,7 @@ convrot_status check_attention(const char* fn, const convrot_attention_args& a, 
                 "sequences", fn, (long long)a.batch);
   if (a.tile != 0 && a.tile != 32 && a.tile != 128 && !(a.tile == 256 && a.d > 64 && a.d <= 128))
     return fail(CONVROT_E_INVALID_ARG, "%s: tile=%d not supported (d=%d)", fn, a.tile, a.d);
-  if (!(a.scale > 0.0f) || a.scale > 3.0e38f)
+  if (!(a.scale > 0.0f) || a.scale > 2.0e38f)  // scale log2 e is finite
     return fail(CONVROT_E_INVALID_ARG, "%s: scale=%g", fn, (double)a.scale);
   return CONVROT_OK;
 }

@@ -279,6 +279,8 @@ struct HeadsShape {
     uint32_t blocks;
   } t[2];
   int waves;
+  int64_t grid;  // blocks of both
+  int threads() const { return waves > 1 ? 64 * waves : kHeadThreads; }
 };
 
 template <int NI, bool F16, bool HALVES, bool ROW>
@@ -441,7 +443,9 @@ HeadsShape shape(const HeadsArgs& a, int ni) {
     if (lanes > 64) lanes = 64;
     sh.t[i].shift = log2_up(lanes);
     const int64_t per = sh.waves > 1 ? 1 : kHeadThreads / lanes;
-    sh.t[i].blocks = (uint32_t)((a.tokens * sh.t[i].segments + per - 1) / per);
+    const int64_t blocks = (a.tokens * sh.t[i].segments + per - 1) / per;
+    sh.t[i].blocks = (uint32_t)blocks;
+    sh.grid += blocks;
   }
   return sh;
 }
@@ -449,8 +453,7 @@ HeadsShape shape(const HeadsArgs& a, int ni) {
 template <int NI, bool F16, bool HALVES>
 hipError_t launch_ni(const HeadsArgs& a, hipStream_t st) {
   const HeadsShape sh = shape(a, NI);
-  const dim3 grid(sh.t[0].blocks + sh.t[1].blocks);
-  const dim3 block(sh.waves > 1 ? 64 * sh.waves : kHeadThreads);
+  const dim3 grid((uint32_t)sh.grid), block(sh.threads());
   if (a.row)
     heads_kernel<NI, F16, HALVES, true><<<grid, block, 0, st>>>(a, sh);
   else
@@ -485,15 +488,8 @@ hipError_t launch_rope_table(const RopeTableArgs& a, PosType type, hipStream_t s
 bool heads_row_fits(int64_t heads, int d) { return (heads << lanes_shift(d)) <= 2048; }
 
 bool heads_grid_fits(const HeadsArgs& a) {
-  // the most blocks and units: one head per lane group
-  const int ls = lanes_shift(a.d);
-  int64_t blocks = 0;
-  for (const HeadsTensor& x : a.t) {
-    const int64_t waves = x.heads ? (unit_lanes(x.heads, ls, 1) + 63) / 64 : 0;
-    if (waves * a.tokens > kMaxLaunchWaves) return false;
-    blocks += waves * a.tokens;
-  }
-  return blocks <= kMaxLaunchWaves / kMaxRowWaves;
+  const HeadsShape sh = shape(a, heads_of_lane(a, lanes_shift(a.d)));
+  return sh.grid * (sh.threads() / 64) <= kMaxLaunchWaves;
 }
 
 hipError_t launch_qk_norm_rope(const HeadsArgs& a, bool halves, DType dt, hipStream_t st) {

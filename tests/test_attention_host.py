@@ -108,7 +108,7 @@ def test_attention_refusals(lib):
     assert st(k_heads=3) == 3 and st(q_heads=1, k_heads=2) == 3 and st(d=60) == 3 and st(d=264) == 3
     assert st(q_tokens=1 << 30) == 3 and st(k_tokens=(1 << 31) - 1) == 3 and st(batch=1 << 24) == 3
     assert st(batch=3, q_offsets=E) == 1 and st(batch=3, k_offsets=E) == 1
-    for scale in (0.0, -0.1, NAN, INF):
+    for scale in (0.0, -0.1, 2.5e38, NAN, INF):
         assert st(scale=scale) == 1
     for tile, d in ((-1, 128), (1, 128), (64, 128), (512, 128), (256, 64), (256, 136)):
         assert st(tile=tile, d=d) == 1
@@ -145,6 +145,12 @@ def test_column_ranges_do_not_clash(lib):
     assert qk_status(lib, **{**inside, "k_out": A + 504}) == 4
     assert qk_status(lib, **{**inside, "k_out": A + 496}) == 1     # one chunk into q
     assert qk_status(lib, **{**inside, "k_out": A + 1008}) == 1    # and into the next token's q
+    # heads outside of tokens, q_out behind q's tokens of each head
+    major = {"q": A, "q_stride": 64, "q_head_stride": 6400, "q_out_stride": 64,
+             "q_out_head_stride": 6400, "k": None, "k_out": None, "k_heads": 0}
+    assert qk_status(lib, **major, q_out=A + 1280, table=A + 2560) == 1
+    assert qk_status(lib, **major, q_out=A + 1264) == 1            # one chunk into q
+    assert qk_status(lib, **major, q_out=A + 11536) == 1           # and into the next head's q
 
 
 def test_workspace_sizes(lib):

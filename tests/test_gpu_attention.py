@@ -367,6 +367,32 @@ def test_layouts():
         close(q[b], k[b], v[b], want[b], None, 1 / 8, False)
 
 
+@pytest.mark.parametrize("far", ["tokens", "heads"])
+@pytest.mark.parametrize("q,tile", [(1, 0), (40, 128), (300, 256), (300, 0)])
+def test_offsets_beyond_32_bits(q, tile, far):
+    """Keys, queries and results of which the last lie past 2^32 bytes and 2^31
+    elements: the bits of the same call on tensors without gaps."""
+    rng = np.random.default_rng(q + tile)
+    n, h, d, dt = 1100, 2, 128, torch.bfloat16
+    room = torch.empty(n << 21, dtype=dt, device=DEV)
+    if far == "tokens":  # column ranges of one wide tensor
+        cols = [room.view(n, 1 << 21)[:, i * h * d:(i + 1) * h * d].view(n, h, d)
+                for i in range(4)]
+    else:  # a head's tokens together
+        cols = [torch.as_strided(room, (n, h, d), (d, (n << 21) - 8 * n * d, 1), i * n * d)
+                for i in range(4)]
+    qc, kc, vc = make(rng, [q], [n], h, h, d, dt)
+    for col, x in zip(cols, (qc, kc, vc)):
+        col[n - x.shape[0]:] = x
+    q_far, out_far = cols[0][n - q:], cols[3][n - q:]
+    out_far.fill_(7.0)
+    want, want_lse = cr.convrot_attention(qc, kc, vc, causal=True, tile=tile, return_lse=True)
+    got, lse = cr.convrot_attention(q_far, cols[1], cols[2], causal=True, tile=tile, out=out_far,
+                                    return_lse=True)
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
+    close(qc, kc, vc, want, want_lse, 1 / math.sqrt(d), True)
+
+
 def test_scale_and_large_scores():
     rng = np.random.default_rng(8)
     q, k, v = make(rng, [64], [100], 2, 2, 64, torch.bfloat16)

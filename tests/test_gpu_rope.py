@@ -245,3 +245,40 @@ def test_runs_streams_and_graphs():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, (*want, want_t)))
         torch.ones(1000, device=DEV).sum().item()
+
+
+def test_offsets_beyond_32_bits():
+    """Rows past 2^31 elements: the bits of the same rows in a call of their own."""
+    dt, h, d, last = torch.bfloat16, 2, 128, 37
+    rng = np.random.default_rng(5)
+    # a table of 2^32 entries
+    t = (1 << 24) + 5
+    pos = torch.arange(t, dtype=torch.int32, device=DEV)
+    table = cr.convrot_rope_table(pos, (256,))
+    want = cr.convrot_rope_table(pos[-last:], (256,))
+    assert torch.equal(table[-last:], want)
+    del table
+    # tokens of a wide tensor, in place, and next to it
+    n = 1100
+    wide = torch.empty((n, 1 << 21), dtype=dt, device=DEV)
+    q, k = (wide[:, i * h * d:(i + 1) * h * d].view(n, h, d) for i in range(2))
+    x = dev(rng.standard_normal((2, n, h, d)), dt)
+    q.copy_(x[0])
+    k.copy_(x[1])
+    turns = cr.convrot_rope_table(pos[:n], (128,))
+    for span in ("head", "row"):
+        want = cr.convrot_qk_norm_rope(x[0], x[1], turns, span=span)
+        got = cr.convrot_qk_norm_rope(q, k, turns, span=span)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    cr.convrot_qk_norm_rope(q, k, turns, span="row", q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    del wide, q, k
+    # more rows than a 32-bit count of elements holds, the table's rows in turn
+    n = (1 << 19) * 20
+    x = torch.empty((n, h, d), dtype=dt, device=DEV)
+    x[:1000] = 0
+    x[-last:] = dev(rng.standard_normal((last, h, d)), dt)
+    got, _ = cr.convrot_qk_norm_rope(x, None, turns[:1024])
+    rows = torch.arange(n - last, n, device=DEV) % 1024
+    want, _ = cr.convrot_qk_norm_rope(x[-last:], None, turns[rows])
+    assert torch.equal(got[-last:], want)
