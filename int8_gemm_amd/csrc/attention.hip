@@ -187,11 +187,11 @@ struct Kernel {
   static constexpr int kDTiles = DP / 32;
 };
 
-// Values of keys that only some rows of a tile see. A weight of 0 does not cancel an
-// infinity or a NaN in the product, so a tile in which some row's mask ends is looked
-// through, infinities and NaN in it are replaced by 0 (by every wave that finds one,
-// before its own reads; they all write the same), and at the end each row adds
-// those of the keys that it sees.
+// Values of keys that only some rows of a tile see, and those that fill a tile behind the
+// last key. A weight of 0 does not cancel an infinity or a NaN in the product, so a tile
+// in which some row's keys end is looked through, infinities and NaN in it are replaced
+// by 0 (by every wave that finds one, before its own reads; they all write the same), and
+// at the end each row adds those of the keys that it sees.
 template <bool F16>
 constexpr uint32_t kExp16 = F16 ? 0x7C007C00u : 0x7F807F80u;
 template <bool F16>
@@ -418,7 +418,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
   using T = Kernel<DP, QT, NW, F16>;
   extern __shared__ __align__(1024) uint8_t lds[];
   volatile int* cleared = reinterpret_cast<int*>(lds + 2 * T::kStages * T::kTileBytes);
-  if (CAUSAL && threadIdx.x == 0) *cleared = 0;  // a barrier follows in every tile
+  if (threadIdx.x == 0) *cleared = 0;  // a barrier follows in every tile
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
@@ -547,7 +547,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
             p[u][q][h][e] = pack16x2<F16>(s[u][q][8 * h + 2 * e], s[u][q][8 * h + 2 * e + 1]);
       }
     }
-    if (CAUSAL && masked && clear_nonfinite<F16, DP, kTileKeys>(vt)) *cleared = 1;
+    if (masked && clear_nonfinite<F16, DP, kTileKeys>(vt)) *cleared = 1;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -560,7 +560,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
         }
   }
 
-  if (CAUSAL) {
+  if (CAUSAL || w.full % kTileKeys) {
     wait_lgkm0();
     lds_barrier();
     if (__builtin_expect(*cleared, 0)) {
@@ -673,7 +673,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
   constexpr int kElems = 16 * QT;  // of a lane and unit
   extern __shared__ __align__(1024) uint8_t lds[];
   volatile int* cleared = reinterpret_cast<int*>(lds + 2 * T::kStages * T::kTileBytes);
-  if (CAUSAL && threadIdx.x == 0) *cleared = 0;
+  if (threadIdx.x == 0) *cleared = 0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
@@ -917,7 +917,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
     auto tile = [&](auto pv, auto stage, int t) __attribute__((always_inline)) {
       constexpr int st = decltype(stage)::value, before = (st + 2) % 3, after = (st + 1) % 3;
       const int key0 = t * kTileKeys;
-      if (CAUSAL && key0 + kTileKeys > w.full &&
+      if (key0 + kTileKeys > w.full &&
           clear_nonfinite<F16, DP, kTileKeys>(lds + T::kV + st * T::kTileBytes))
         *cleared = 1;
       step(pv, sa, sb, pb, pa, st * T::kTileBytes + T::kUnitBytes,
@@ -965,7 +965,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
       mfma_out<F16, T::kAcc, i == kLast - 1>(&o[q][d], ring[0], pb[q][h]);
     });
   }
-  if (CAUSAL) {
+  if (CAUSAL || w.full % kTileKeys) {
     wait_lgkm0();
     lds_barrier();
     if (__builtin_expect(*cleared, 0)) {

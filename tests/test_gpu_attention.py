@@ -287,6 +287,27 @@ def test_keys_that_the_mask_hides_have_no_part(hq, hk, d, n, length, tile, what,
     assert torch.equal(got[~sees], clean[~sees])
 
 
+@DTYPES
+@pytest.mark.parametrize("hq,hk,d,n,length,tile", [
+    (2, 2, 128, 200, 70, 128), (4, 2, 64, 90, 300, 0), (2, 1, 256, 70, 129, 0),
+    (2, 2, 128, 3, 33, 32),
+    (2, 2, 128, 600, 100, 256), (4, 2, 96, 300, 3001, 256), (3, 3, 40, 300, 64, 0),
+    (1, 1, 128, 100, 4097, 128)])
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+def test_the_last_key_of_a_tile_that_ends_early(hq, hk, d, n, length, tile, what, dtype):
+    """The places behind it hold nothing, whatever its value is."""
+    rng = np.random.default_rng(length)
+    q, k, v = make(rng, [n], [length], hq, hk, d, dtype)
+    clean = cr.convrot_attention(q, k, v, tile=tile)
+    col = d - 3
+    v[length - 1, :, col] = what
+    got = cr.convrot_attention(q, k, v, tile=tile)
+    hit = got[:, :, col]
+    assert (torch.isnan(hit) if math.isnan(what) else hit == what).all()
+    rest = [c for c in range(d) if c != col]
+    assert torch.equal(got[:, :, rest], clean[:, :, rest])
+
+
 def test_rows_outside_the_sequences_stay():
     rng = np.random.default_rng(4)
     hq, hk, d = 4, 2, 64
