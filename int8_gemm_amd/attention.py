@@ -6,6 +6,7 @@ the rest of the binding."""
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -31,6 +32,9 @@ class _QkArgs(ctypes.Structure):
                    ("dtype", ctypes.c_int), ("eps", ctypes.c_float)])
 
 
+_pack_qk = struct.Struct("@7Q10q8if4x").pack  # a _QkArgs at a third of its host time
+
+
 class _AttentionArgs(ctypes.Structure):
     _fields_ = ([(f, ctypes.c_void_p) for f in ("q", "k", "v", "out", "lse", "q_offsets",
                                                 "k_offsets", "k_lens")]
@@ -41,6 +45,9 @@ class _AttentionArgs(ctypes.Structure):
                 + [(f, ctypes.c_int32) for f in ("q_heads", "k_heads", "d", "causal")]
                 + [("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("tile", ctypes.c_int32)])
 
+
+_pack_attention = struct.Struct("@8Q11q5ifi4x").pack
+_OUT, _LSE, _OUT_STRIDE, _OUT_HEAD_STRIDE, _TOKENS = 3, 4, 14, 15, 16  # of its fields
 
 # As in mx4.py: one expression on the good path, what is wrong is worked out behind it.
 
@@ -83,6 +90,9 @@ def _heads(t, name: str, dtype, dev: int):
 
 def _like(x: torch.Tensor, tokens: int, heads: int, d: int):
     """A new contiguous tensor of x's shape; with its address and strides as _heads'."""
+    if x.is_contiguous():
+        out = torch.empty_like(x)  # a fifth less host time
+        return out, out.data_ptr(), heads * d, d
     out = torch.empty_strided(x.shape, (heads * d, d, 1) if x.dim() == 3 else
                               (tokens // x.shape[0] * heads * d if x.shape[0] else 1, heads * d,
                                d, 1), dtype=x.dtype, device=x.device)
@@ -117,7 +127,8 @@ def convrot_rope_table(positions: torch.Tensor, dims, theta: float = 10000.0, *,
     tokens, dev = positions.shape[0], positions.get_device()
     pairs = sum(dims) // 2
     if out is None:
-        out = torch.empty((tokens, pairs, 2), dtype=torch.float32, device=positions.device)
+        out = torch.empty_strided((tokens, pairs, 2), (2 * pairs, 2, 1), dtype=torch.float32,
+                                  device=positions.device)
         po = out.data_ptr()
     else:
         po = _tensor(out, "out", torch.float32, (tokens, pairs, 2), dev)
@@ -149,9 +160,9 @@ def convrot_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None,
         pqo, qos, qoh = pq, qs, qh
     else:
         pqo, qos, qoh = _output(q_out, "q_out", q, dev)
-    pqw = None if q_weight is None else _weight(q_weight, "q_weight", dtype, dev, d,
+    pqw = 0 if q_weight is None else _weight(q_weight, "q_weight", dtype, dev, d,
                                                 heads if row else 1)
-    pk = pko = pkw = None
+    pk = pko = pkw = 0
     k_heads = ks = kh = kos = koh = 0
     if k is not None:
         pk, k_tokens, k_heads, k_d, ks, kh, _ = _heads(k, "k", dtype, dev)
@@ -167,16 +178,16 @@ def convrot_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None,
             pkw = _weight(k_weight, "k_weight", dtype, dev, d, k_heads if row else 1)
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
-    pt, rows, pairs = None, 0, 0
+    pt, rows, pairs = 0, 0, 0
     if table is not None:
         shape = table.shape if isinstance(table, torch.Tensor) else ()
         if len(shape) != 3 or shape[2] != 2:
             raise ValueError(f"table must be [rows, pairs, 2] (got shape {tuple(shape)})")
         pt = _tensor(table, "table", torch.float32, shape, dev)
         rows, pairs, _ = shape
-    a = _QkArgs(pq, pk, pqo, pko, pqw, pkw, pt, qs, qh, ks, kh, qos, qoh, kos, koh, tokens, rows,
-                heads, k_heads, d, pairs, _NORMS[norm], row, halves, _DTYPES[dtype], eps)
-    _launch("convrot_qk_norm_rope", dev, ctypes.byref(a))
+    a = _pack_qk(pq, pk, pqo, pko, pqw, pkw, pt, qs, qh, ks, kh, qos, qoh, kos, koh, tokens, rows,
+                 heads, k_heads, d, pairs, _NORMS[norm], row, halves, _DTYPES[dtype], eps)
+    _launch("convrot_qk_norm_rope", dev, a)
     return q_out, k_out
 
 
@@ -197,7 +208,7 @@ def _weight(t, name: str, dtype, dev: int, d: int, heads: int) -> int:
 def _sequences(offsets, name: str, of: torch.Tensor, batch: int, dev: int):
     """Check offsets into `of`, whose own batch counts without them; (address, sequences)."""
     if offsets is None:
-        return None, batch
+        return 0, batch
     n = offsets.numel() - 1 if isinstance(offsets, torch.Tensor) else 0
     p = _tensor(offsets, name, _I32, (n + 1,), dev)
     if of.dim() == 4:
@@ -208,7 +219,7 @@ def _sequences(offsets, name: str, of: torch.Tensor, batch: int, dev: int):
 
 
 def _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale, tile):
-    """The arguments of a call but its outputs, and the device index."""
+    """The fields of _AttentionArgs but the outputs', and the device index."""
     dev, dtype = _first(q, "q"), q.dtype
     pq, tokens, heads, d, qs, qh, batch = _heads(q, "q", dtype, dev)
     pk, k_tokens, k_heads, k_d, ks, kh, k_batch = _heads(k, "k", dtype, dev)
@@ -220,10 +231,10 @@ def _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale, tile):
     pko, k_batch = _sequences(k_offsets, "k_offsets", k, k_batch, dev)
     if batch != k_batch:
         raise ValueError(f"{batch} sequences of queries, {k_batch} of keys")
-    pkl = None if k_lens is None else _tensor(k_lens, "k_lens", _I32, (batch,), dev)
-    return _AttentionArgs(pq, pk, pv, None, None, pqo, pko, pkl, qs, qh, ks, kh, vs, vh, 0, 0,
-                          tokens, k_tokens, batch, heads, k_heads, d, causal, _DTYPES[dtype],
-                          max(d, 1) ** -0.5 if scale is None else scale, tile), dev
+    pkl = 0 if k_lens is None else _tensor(k_lens, "k_lens", _I32, (batch,), dev)
+    return [pq, pk, pv, 0, 0, pqo, pko, pkl, qs, qh, ks, kh, vs, vh, 0, 0, tokens, k_tokens, batch,
+            heads, k_heads, d, causal, _DTYPES[dtype],
+            max(d, 1) ** -0.5 if scale is None else scale, tile], dev
 
 
 def convrot_attention_workspace_size(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
@@ -232,7 +243,7 @@ def convrot_attention_workspace_size(q: torch.Tensor, k: torch.Tensor, v: torch.
                                      causal: bool = False, tile: int = 0) -> int:
     """Workspace bytes of a convrot_attention call with these tensors."""
     a, _ = _attention_args(q, k, v, q_offsets, k_offsets, None, causal, None, tile)
-    return int(load_library().convrot_attention_workspace_size(ctypes.byref(a)))
+    return int(load_library().convrot_attention_workspace_size(_pack_attention(*a)))
 
 
 def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
@@ -252,23 +263,27 @@ def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     sequence owns are not written. `workspace` (uint8 on the device) defaults to what
     the call asks for. `tile` != 0 forces a kernel (test / tuning hook)."""
     a, dev = _attention_args(q, k, v, q_offsets, k_offsets, k_lens, causal, scale, tile)
+    heads, d = q.shape[-2:]
+    tokens = a[_TOKENS]
     if out is None:
-        out, a.out, a.out_stride, a.out_head_stride = _like(q, a.q_tokens, a.q_heads, a.d)
+        out, a[_OUT], a[_OUT_STRIDE], a[_OUT_HEAD_STRIDE] = _like(q, tokens, heads, d)
     else:
-        a.out, a.out_stride, a.out_head_stride = _output(out, "out", q, dev)
+        a[_OUT], a[_OUT_STRIDE], a[_OUT_HEAD_STRIDE] = _output(out, "out", q, dev)
     if lse is not None:
-        a.lse = _tensor(lse, "lse", torch.float32, (a.q_heads, a.q_tokens), dev)
+        a[_LSE] = _tensor(lse, "lse", torch.float32, (heads, tokens), dev)
     elif return_lse:
-        lse = torch.empty((a.q_heads, a.q_tokens), dtype=torch.float32, device=q.device)
-        a.lse = lse.data_ptr()
+        lse = torch.empty_strided((heads, tokens), (tokens, 1), dtype=torch.float32,
+                                  device=q.device)
+        a[_LSE] = lse.data_ptr()
+    a = _pack_attention(*a)
     pw, size = None, 0
     if workspace is not None:
         size = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
         pw = _tensor(workspace, "workspace", _U8, (size,), dev)
     else:
-        size = load_library().convrot_attention_workspace_size(ctypes.byref(a))
+        size = load_library().convrot_attention_workspace_size(a)
         if size:
             workspace = torch.empty_strided((size,), (1,), dtype=_U8, device=q.device)
             pw = workspace.data_ptr()
-    _launch("convrot_attention", dev, ctypes.byref(a), pw, size)
+    _launch("convrot_attention", dev, a, pw, size)
     return out if lse is None else (out, lse)

@@ -232,6 +232,20 @@ def test_structures_match_the_header_and_it_links_as_c99(lib, tmp_path):
         assert got == [getattr(struct, f).offset for f in fields] + [ctypes.sizeof(struct)]
 
 
+def test_packed_arguments():
+    for kind, pack in ((attention._QkArgs, attention._pack_qk),
+                       (attention._AttentionArgs, attention._pack_attention)):
+        values = [0.5 if t is ctypes.c_float else i for i, (_, t) in enumerate(kind._fields_)]
+        packed = pack(*values)
+        a = kind.from_buffer_copy(packed)
+        assert len(packed) == ctypes.sizeof(kind)
+        assert [getattr(a, n) or 0 for n, _ in kind._fields_] == values
+    names = [n for n, _ in attention._AttentionArgs._fields_]
+    assert [names[i] for i in (attention._OUT, attention._LSE, attention._OUT_STRIDE,
+                               attention._OUT_HEAD_STRIDE, attention._TOKENS)] == [
+        "out", "lse", "out_stride", "out_head_stride", "q_tokens"]
+
+
 def test_oracle_pins():
     # a quarter turn, and pairs by halves
     v = np.arange(8.0).reshape(1, 1, 8)
