@@ -308,6 +308,31 @@ def test_the_last_key_of_a_tile_that_ends_early(hq, hk, d, n, length, tile, what
     assert torch.equal(got[:, :, rest], clean[:, :, rest])
 
 
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("n,d,tile", [(1, 128, 0), (5, 64, 0), (300, 128, 0), (300, 128, 256),
+                                      (300, 128, 128), (70, 256, 0), (70, 64, 32)])
+def test_no_keys(n, d, tile, causal):
+    q = torch.ones((n, 4, d), dtype=torch.bfloat16, device=DEV)
+    none = q[:0, :2]
+    for args in ({}, {"q_offsets": offsets([n]), "k_offsets": offsets([0])}):
+        out, lse = cr.convrot_attention(q, none, none, causal=causal, tile=tile,
+                                        return_lse=True, **args)
+        assert not out.any() and (lse == -math.inf).all()
+    k = torch.full((200, 2, d), math.nan, dtype=torch.bfloat16, device=DEV)
+    used = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = cr.convrot_attention(q, k, k, k_lens=used, causal=causal, tile=tile,
+                                    return_lse=True)
+    assert not out.any() and (lse == -math.inf).all()
+    assert cr.convrot_attention(q[:0], k, k, causal=causal, tile=tile).shape == (0, 4, d)
+
+
+@DTYPES
+def test_many_heads(dtype):
+    rng = np.random.default_rng(13)
+    q, k, v = make(rng, [3], [50], 1000, 500, 8, dtype)
+    close(q, k, v, *cr.convrot_attention(q, k, v, causal=True, return_lse=True), 8 ** -0.5, True)
+
+
 def test_rows_outside_the_sequences_stay():
     rng = np.random.default_rng(4)
     hq, hk, d = 4, 2, 64
