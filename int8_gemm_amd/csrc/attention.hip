@@ -408,8 +408,9 @@ __device__ __forceinline__ void mask(v16f* s, int key0, int seen) {
 // do not fill the card with 256 (16384 queries x 40 heads of 128 over 256 keys: 142 us, with
 // 256 rows a block 175; over 4608: 1457 and 1331). 32760 x 40 heads over 512 keys take 424 us,
 // 0.81 PFLOP/s: of a round's 21 us 6.5 are a block's start and end, and the MFMAs are
-// busy 0.37 of the cycles at 2.0 GHz. Heads of up to 256: 8192 x 8 heads of 256 in
-// 685 us (0.80 PFLOP/s), one block a compute unit, its output a whole 128 registers a lane.
+// busy 0.37 of the cycles at 2.0 GHz (power: fetching the next tile early gains nothing).
+// Heads of up to 256: 8192 x 8 heads of 256 in 685 us (0.80 PFLOP/s), one block a compute
+// unit, its output a whole 128 registers a lane.
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
 __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(AttentionArgs a,
                                                                               uint32_t slots,
