@@ -34,7 +34,7 @@ constexpr int kTileKeys = 64;   // keys of a copied tile
 constexpr int kRowsOfTile = 128;
 constexpr int kRowsOfWide = 256;
 constexpr int kFewUnits = 4;     // least units of a part, few rows
-constexpr int kMaxSplits = 512;  // two rounds of a block per compute unit
+constexpr int kMaxSplits = 512;  // of a row's keys: two rounds of a block per compute unit
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 // A row's reference m is a largest score of it: it is raised when a score passes it by
@@ -1569,6 +1569,7 @@ AttentionPlan plan_tiles(const AttentionArgs& a, const Rounds& k, size_t workspa
   // n parts of each of the last `rest` tiles
   auto consider = [&](int64_t whole, int64_t rest, int64_t n) {
     if (n > 1 && n > keys / 4) n = (int64_t)(keys / 4);
+    if (n > kMaxSplits) n = kMaxSplits;  // whose factors the join holds
     if (n < 1) return;
     AttentionPlan t = p;
     if (n > 1) {

@@ -170,6 +170,28 @@ def test_workspace_sizes(lib):
         cr.convrot_set_compute_units(0)
 
 
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("d,tile", [(8, 0), (64, 0), (64, 128), (128, 128), (128, 256), (256, 0)])
+def test_no_more_parts_than_are_joined(lib, d, tile, causal):
+    """The kernel that joins a row's parts holds 512 of their factors. A row of parts takes
+    their d + 1 floats each and an entry of 8 bytes."""
+    rows = 256 if tile == 256 else 128
+
+    def most(q_tokens, group, k_tokens):
+        size = lib.convrot_attention_workspace_size(ctypes.byref(attention_args(
+            q_tokens=q_tokens, k_tokens=k_tokens, q_heads=group, k_heads=1, d=d, tile=tile,
+            causal=causal)))
+        if size == 0:
+            return 1
+        assert size % rows == 0
+        parts, rest = divmod(size // rows - 8, (d + 1) * 4)
+        assert rest == 0
+        return parts
+    counts = [most(q, group, keys) for q, group in ((4, 32), (33, 1), (64, 1), (128, 1))
+              for keys in (1 << 14, 1 << 17, 196608, 262144, 300000, 540672, 1 << 20, 1 << 21)]
+    assert max(counts) <= 512 and max(counts) > 64
+
+
 def test_binding_checks_tensors():
     x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
     for call in (lambda: cr.convrot_attention(x, x, x), lambda: cr.convrot_qk_norm_rope(x),

@@ -368,6 +368,15 @@ def test_offsets_that_leave_the_tensors_stay_inside():
             assert (guard[:100] == 7).all() and (guard[200:] == 7).all()
 
 
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("n,hq,d,length", [(40, 1, 8, 300000), (70, 1, 64, 220000)])
+def test_one_tile_over_so_many_keys_that_the_join_bounds_its_parts(n, hq, d, length, causal):
+    rng = np.random.default_rng(n)
+    q, k, v = make(rng, [n], [length], hq, 1, d, torch.bfloat16, 4.0)
+    out, lse = cr.convrot_attention(q, k, v, causal=causal, return_lse=True)
+    close(q, k, v, out, lse, d ** -0.5, causal)
+
+
 @DTYPES
 def test_a_last_round_that_is_split(dtype):
     """More tiles than run at a time: those behind the last whole round go by parts."""
