@@ -572,8 +572,9 @@ convrot_status convrot_norm_residual(const convrot_norm_args* args, void* stream
  *   call reads and writes nothing out of bounds, its results are not specified.
  *   lse [q_heads, q_tokens] fp32 (nullable): log of the sum of exp of the scores.
  *   Scores, sums and the output are fp32; softmax weights are rounded to dtype for
- *   the product with v (few rows: to twice its bits). Results are the same bits from
- *   run to run and on any number of compute units.
+ *   the product with v (few rows: to twice its bits), whose finite values may have
+ *   any magnitude. Results are the same bits from run to run and on any number of
+ *   compute units.
  *   workspace (256-byte aligned, convrot_attention_workspace_size bytes, nullable
  *   where that is 0) holds the parts of calls with few queries, whose keys are
  *   split over the card; with less, a call splits less, and sums in another order.

@@ -29,6 +29,7 @@ typedef _Float16 hf8 __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) volatile int* lds_ints;
 
 constexpr int kTileKeys = 64;   // keys of a copied tile
 constexpr int kRowsOfTile = 128;
@@ -45,6 +46,25 @@ constexpr float kRoom = F16 ? 10.f : 32.f;
 template <bool F16>
 constexpr float kLift = F16 ? 4.f : 0.f;
 constexpr float kLowest = -3.402823466e38f;
+// bf16 values may be so large (above 2^96 / keys) that such weights take their sum out of
+// fp32 (half ones, below 2^16, are not). A block in whose result something is not finite,
+// although the sum of the weights is, goes over its keys again with the reference raised at
+// every larger score and 2^32 above it, so that no row's weights sum to more than 1: the
+// elements that are finite then replace those that were not, the others stay. Looking costs
+// an instruction an element of the result and a barrier.
+constexpr float kOver = 32.f;
+constexpr float kMostOver = 1e36f;  // finite where the scale is next to nothing
+template <bool F16>
+struct Pass {
+  static constexpr bool kAgain = !F16;
+  float room, over;  // of the first
+  __device__ Pass(float c) : room(kRoom<F16> / c), over(0.f) {}
+  __device__ void again(float c) {
+    over = fminf(kOver / c, kMostOver);
+    room = -over;
+  }
+  __device__ bool first() const { return !kAgain || over == 0.f; }
+};
 
 template <bool F16>
 __device__ __forceinline__ v16f mfma(const u4& a, const u4& b, const v16f& c) {
@@ -205,7 +225,8 @@ __device__ __forceinline__ bool nonfinite16(uint32_t h) {
 // True if the tile holds an infinity or a NaN; none is left then.
 template <bool F16, int DP, int KEYS>
 __device__ __forceinline__ bool clear_nonfinite(uint8_t* vt) {
-  const int lane = threadIdx.x & 63;
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // its addresses are not kept between tiles
   uint32_t found = 0;
 #pragma unroll 1
   for (int i = lane; i < KEYS * DP / 8; i += 64) {
@@ -316,34 +337,68 @@ __device__ __forceinline__ bool locate(const AttentionArgs& a, uint32_t slots, u
   return true;
 }
 
+// What a second pass leaves of the first one's results and its own.
+__device__ __forceinline__ v4f finite_of(v4f before, v4f now) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool keep = __builtin_fabsf(before[i]) < __builtin_inff() ||
+                      !(__builtin_fabsf(now[i]) < __builtin_inff());
+    now[i] = keep ? before[i] : now[i];
+  }
+  return now;
+}
+template <bool F16, typename U>
+__device__ __forceinline__ U finite_of16(U before, U now) {
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(U) / 4); ++i) {
+    uint32_t take = 0;
+#pragma unroll
+    for (int h = 0; h < 32; h += 16)
+      if (nonfinite16<F16>(before[i] >> h) && !nonfinite16<F16>(now[i] >> h)) take |= 0xFFFFu << h;
+    now[i] = (now[i] & take) | (before[i] & ~take);
+  }
+  return now;
+}
+
 // A row's result, of which this lane holds o, its part l of the sum and the reference m.
+// True if something in it is not finite though its sum is.
 template <int ROWS, int DTILES, bool F16>
-__device__ __forceinline__ void finish(const AttentionArgs& a, const Tile& t, int row, float l,
-                                       float m, float c, const v16f (&o)[DTILES]) {
+__device__ __forceinline__ bool finish(const AttentionArgs& a, const Tile& t, int row, float l,
+                                       float m, float c, const v16f (&o)[DTILES], bool first) {
   const int half = (threadIdx.x >> 5) & 1;
   const float sum = l + other_half(l);
   const bool some = sum > 0.f || sum != sum;
   const float inv = some ? 1.0f / sum : 0.f;
   const float lse2 = some ? log2f(sum) - kLift<F16> + m * c : -__builtin_inff();
-  if (row >= t.rows) return;
+  if (row >= t.rows) return false;
+  float probe = 0.f;  // NaN once something is not finite
+  if (Pass<F16>::kAgain) {
+#pragma unroll
+    for (int d = 0; d < DTILES; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) probe = __builtin_fmaf(o[d][i], 0.f, probe);
+  }
+  const bool lost = probe != probe && sum < __builtin_inff();
   if (t.tail) {
     const int64_t at = (int64_t)t.piece * ROWS + row - t.row0;
-    if (half == 0) a.part_lse[at] = lse2;
-    if (!some) return;
+    if (half == 0 && first) a.part_lse[at] = lse2;
+    if (!some) return false;
     float* to = a.part + at * a.d;
 #pragma unroll
     for (int d = 0; d < DTILES; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int e = d * 32 + i * 8 + half * 4;
-        const v4f f = {o[d][4 * i] * inv, o[d][4 * i + 1] * inv, o[d][4 * i + 2] * inv,
-                       o[d][4 * i + 3] * inv};
-        if (e < a.d) *reinterpret_cast<v4f*>(to + e) = f;
+        v4f f = {o[d][4 * i] * inv, o[d][4 * i + 1] * inv, o[d][4 * i + 2] * inv,
+                 o[d][4 * i + 3] * inv};
+        if (e >= a.d) continue;
+        if (!first) f = finite_of(*reinterpret_cast<const v4f*>(to + e), f);
+        *reinterpret_cast<v4f*>(to + e) = f;
       }
-    return;
+    return lost;
   }
   const int token = t.w.q0 + row / a.group, head = t.hk * a.group + row % a.group;
-  if (a.lse && half == 0) a.lse[(int64_t)head * a.q_tokens + token] = lse2 * kLn2;
+  if (a.lse && half == 0 && first) a.lse[(int64_t)head * a.q_tokens + token] = lse2 * kLn2;
   uint16_t* to = a.out + (int64_t)token * a.out_stride + (int64_t)head * a.out_head_stride;
   // the two lanes of a row hold four elements of each eight: they swap, so that each
   // has every other eight
@@ -363,8 +418,33 @@ __device__ __forceinline__ void finish(const AttentionArgs& a, const Tile& t, in
         f[2 + j] = x.y;
       }
       const int e = d * 32 + (i + half) * 8;
-      if (e < a.d) *reinterpret_cast<u4*>(to + e) = f;
+      if (e >= a.d) continue;
+      if (!first) f = finite_of16<F16>(*reinterpret_cast<const u4*>(to + e), f);
+      *reinterpret_cast<u4*>(to + e) = f;
     }
+  return lost;
+}
+
+// Whether the block goes over its keys again: some wave of it lost an element in its first
+// pass. Every wave comes here with what it found. The second pass is code of its own: as
+// the same code in a loop it kept so much from one to the other that the first one of 32760
+// x 512 keys x 40 heads took 444 us for 427.
+template <bool F16>
+__device__ __forceinline__ bool pass_again(Pass<F16>* pass, bool lost, lds_ints flag, float c) {
+  if (!Pass<F16>::kAgain) return false;
+  if (__builtin_expect(__any(lost), 0)) *flag = 1;
+  wait_lgkm0();
+  lds_barrier();
+  if (__builtin_expect(*flag == 0, 1)) return false;
+  pass->again(c);
+  return true;
+}
+// The thread's number, of which the compiler does not know that it is the same: nothing
+// worked out from it for the first pass is kept for the second.
+__device__ __forceinline__ int thread_anew() {
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  return tid;
 }
 
 // The first key and value of a tile's head, as bytes.
@@ -412,20 +492,13 @@ __device__ __forceinline__ void mask(v16f* s, int key0, int seen) {
 // Heads of up to 256: 8192 x 8 heads of 256 in 685 us (0.80 PFLOP/s), one block a compute
 // unit, its output a whole 128 registers a lane.
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(AttentionArgs a,
-                                                                              uint32_t slots,
-                                                                              uint32_t xcds,
-                                                                              uint32_t share) {
+__device__ __forceinline__ bool walk(const AttentionArgs& a, const Tile& w,
+                                     const Pass<F16>& pass, uint8_t* lds, lds_ints flags,
+                                     int tid) {
   using T = Kernel<DP, QT, NW, F16>;
-  extern __shared__ __align__(1024) uint8_t lds[];
-  volatile int* cleared = reinterpret_cast<int*>(lds + 2 * T::kStages * T::kTileBytes);
-  if (threadIdx.x == 0) *cleared = 0;  // a barrier follows in every tile
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
-  Tile w;
-  if (!locate<T::kRows, CAUSAL>(a, slots, xcds, share, &w)) return;
-
   int row[QT], seen[QT];
   u4 qf[QT][T::kSteps];
 #pragma unroll
@@ -453,6 +526,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
     }
   };
 
+  const float c = a.scale * kLog2e;
   v16f o[QT][T::kDTiles];
   v16f below[QT];  // -m in every place: the first product starts from it
   float l[QT], raise_at[QT];
@@ -464,8 +538,6 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
 #pragma unroll
     for (int d = 0; d < T::kDTiles; ++d) o[q][d] = (v16f){0};
   }
-  const float c = a.scale * kLog2e;
-  const float room = kRoom<F16> / c;
 
   if (w.t0 < w.tiles) issue(w.t0, 0);
   for (int t = w.t0; t < w.tiles; ++t) {
@@ -512,11 +584,11 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
         const bool up = top[q] > raise_at[q];
-        const float by = up ? top[q] : 0.f;
+        const float by = up ? top[q] + pass.over : 0.f;
         // a row without an m has nothing to scale yet (or NaN, which stays)
         const float alpha =
             up && raise_at[q] > kLowest ? __builtin_amdgcn_exp2f(-by * c) : 1.f;
-        raise_at[q] = up ? room : raise_at[q];
+        raise_at[q] = up ? pass.room : raise_at[q];
         l[q] *= alpha;
 #pragma unroll
         for (int i = 0; i < 16; ++i) below[q][i] -= by;
@@ -548,7 +620,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
             p[u][q][h][e] = pack16x2<F16>(s[u][q][8 * h + 2 * e], s[u][q][8 * h + 2 * e + 1]);
       }
     }
-    if (masked && clear_nonfinite<F16, DP, kTileKeys>(vt)) *cleared = 1;
+    if (masked && clear_nonfinite<F16, DP, kTileKeys>(vt)) flags[0] = 1;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -564,7 +636,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
   if (CAUSAL || w.full % kTileKeys) {
     wait_lgkm0();
     lds_barrier();
-    if (__builtin_expect(*cleared, 0)) {
+    if (__builtin_expect(flags[0], 0)) {
       const int to = min(w.end, w.tiles * kTileKeys);
 #pragma unroll 1
       for (int key = max(w.full / kTileKeys, w.t0) * kTileKeys; key < to; ++key)
@@ -573,9 +645,30 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(At
           add_nonfinite<T::kDTiles, F16>(a, w.w.k0 + key, w.hk, key < seen[q], o[q]);
     }
   }
+  bool lost = false;
 #pragma unroll
   for (int q = 0; q < QT; ++q)
-    finish<T::kRows, T::kDTiles, F16>(a, w, row[q], l[q], -below[q][0], c, o[q]);
+    lost |= finish<T::kRows, T::kDTiles, F16>(a, w, row[q], l[q], -below[q][0], c, o[q],
+                                              pass.first());
+  return lost;
+}
+
+template <int DP, int QT, int NW, bool F16, bool CAUSAL>
+__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(AttentionArgs a,
+                                                                              uint32_t slots,
+                                                                              uint32_t xcds,
+                                                                              uint32_t share) {
+  using T = Kernel<DP, QT, NW, F16>;
+  extern __shared__ __align__(1024) uint8_t lds[];
+  lds_ints flags = (lds_ints)(lds + 2 * T::kStages * T::kTileBytes);
+  if (threadIdx.x == 0) flags[0] = flags[1] = 0;  // a barrier follows in every tile
+  Tile w;
+  if (!locate<T::kRows, CAUSAL>(a, slots, xcds, share, &w)) return;
+  const float c = a.scale * kLog2e;
+  Pass<F16> pass(c);
+  const bool lost = walk<DP, QT, NW, F16, CAUSAL>(a, w, pass, lds, flags, threadIdx.x);
+  if (pass_again<F16>(&pass, lost, flags + 1, c))
+    walk<DP, QT, NW, F16, CAUSAL>(a, w, pass, lds, flags, thread_anew());
 }
 
 // MFMAs of the pipeline below, whose accumulators stay where they are put: the output in
@@ -673,8 +766,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
   constexpr int kFrags = 2 * T::kSteps, kSlots = kFrags * QT, kAhead = 3, kRing = 4;
   constexpr int kElems = 16 * QT;  // of a lane and unit
   extern __shared__ __align__(1024) uint8_t lds[];
-  volatile int* cleared = reinterpret_cast<int*>(lds + 2 * T::kStages * T::kTileBytes);
-  if (threadIdx.x == 0) *cleared = 0;
+  lds_ints flags = (lds_ints)(lds + 2 * T::kStages * T::kTileBytes);
+  if (threadIdx.x == 0) flags[0] = flags[1] = 0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
@@ -702,6 +795,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
   auto copy_v = [&](int t, int stage) __attribute__((always_inline)) {
     if (t < w.tiles) copy(vbase, vstride, true, t, T::kV + stage * T::kTileBytes);
   };
+  const float c = a.scale * kLog2e;
+  Pass<F16> pass(c);
   copy_k(w.t0, 0);
   copy_v(w.t0, 0);
   copy_k(w.t0 + 1, 1);
@@ -724,8 +819,6 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
 #pragma unroll
     for (int d = 0; d < T::kDTiles; ++d) o[q][d] = (v16f){0};
   }
-  const float c = a.scale * kLog2e;
-  const float room = kRoom<F16> / c;
 
   // lane's addresses of a unit's operands
   const uint8_t* kat[T::kSteps];
@@ -854,7 +947,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
         // a row without an m has nothing to scale yet (or NaN, which stays)
         const float alpha =
             up && raise_at[q] > kLowest ? __builtin_amdgcn_exp2f(-by * c) : 1.f;
-        raise_at[q] = up ? room : raise_at[q];
+        raise_at[q] = up ? pass.room : raise_at[q];
         l[q] *= alpha;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -920,7 +1013,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
       const int key0 = t * kTileKeys;
       if (key0 + kTileKeys > w.full &&
           clear_nonfinite<F16, DP, kTileKeys>(lds + T::kV + st * T::kTileBytes))
-        *cleared = 1;
+        flags[0] = 1;
       step(pv, sa, sb, pb, pa, st * T::kTileBytes + T::kUnitBytes,
            before * T::kTileBytes + T::kUnitBytes, after * T::kTileBytes);
       settle(sb, sa, pa, key0 + 32);
@@ -969,7 +1062,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
   if (CAUSAL || w.full % kTileKeys) {
     wait_lgkm0();
     lds_barrier();
-    if (__builtin_expect(*cleared, 0)) {
+    if (__builtin_expect(flags[0], 0)) {
       const int to = min(w.end, w.tiles * kTileKeys);
 #pragma unroll 1
       for (int key = max(w.full / kTileKeys, w.t0) * kTileKeys; key < to; ++key)
@@ -978,9 +1071,14 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
           add_nonfinite<T::kDTiles, F16>(a, w.w.k0 + key, w.hk, key < seen[q], o[q]);
     }
   }
+  bool lost = false;
 #pragma unroll
   for (int q = 0; q < QT; ++q)
-    finish<T::kRows, T::kDTiles, F16>(a, w, row[q], l[q], -below[q][0], c, o[q]);
+    lost |= finish<T::kRows, T::kDTiles, F16>(a, w, row[q], l[q], -below[q][0], c, o[q],
+                                              pass.first());
+  // without the pipeline
+  if (pass_again<F16>(&pass, lost, flags + 1, c))
+    walk<DP, QT, NW, F16, CAUSAL>(a, w, pass, lds, flags, thread_anew());
 }
 
 // ---- few rows: single tokens against a long cache ----------------------------
@@ -1006,7 +1104,8 @@ struct Few {
   static constexpr int kCopies = kUnitBytes / 1024;
   static constexpr int kJoinRow = DP + 4;  // floats of a row of partial sums
   static constexpr int kLds = kWaves * kWaveBytes;
-  static_assert(kWaves * (32 * kJoinRow + 64) * 4 <= kLds, "sums fit the ring");
+  static constexpr int kFlag = kWaves * (32 * kJoinRow + 64) * 4;  // behind the sums
+  static_assert(kFlag + 4 <= kLds, "sums fit the ring");
 };
 
 // What a block does: a tile of a sequence's rows with one of the `splits` parts of its
@@ -1086,18 +1185,16 @@ __device__ __forceinline__ bool locate_few(const AttentionArgs& a, uint32_t at, 
   return false;
 }
 
+// One pass over a block's keys; the sums of its waves joined, and written.
 template <int DP, bool F16>
-__global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(AttentionArgs a) {
+__device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& work, int hk,
+                                         const Pass<F16>& pass, uint8_t* lds, int tid) {
   using T = Few<DP>;
   constexpr int kSteps = DP / 16, kDTiles = DP / 32;
-  extern __shared__ __align__(1024) uint8_t lds[];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
   const int group = a.group;
-  const int hk = (int)(blockIdx.x % (uint32_t)a.k_heads);
-  FewWork work;
-  if (!locate_few(a, blockIdx.x / (uint32_t)a.k_heads, &work)) return;
   const Where& w = work.w;
 
   const int rows = w.lq * group, row0 = w.tile * 32;
@@ -1142,11 +1239,11 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
     }
   };
 
+  const float c = a.scale * kLog2e;
   v16f o[kDTiles], below = (v16f){0};
 #pragma unroll
   for (int d = 0; d < kDTiles; ++d) o[d] = (v16f){0};
   float l = 0.f, raise_at = -__builtin_inff();
-  const float c = a.scale * kLog2e, room = kRoom<F16> / c;
 
   int u = first + wave, stage = 0;
   if (u < last) issue(u, 0);
@@ -1178,9 +1275,9 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
     top = fmaxf(top, other_half(top));
     if (__any(top > raise_at)) {
       const bool up = top > raise_at;
-      const float by = up ? top : 0.f;
+      const float by = up ? top + pass.over : 0.f;
       const float alpha = up && raise_at > kLowest ? __builtin_amdgcn_exp2f(-by * c) : 1.f;
-      raise_at = up ? room : raise_at;
+      raise_at = up ? pass.room : raise_at;
       l *= alpha;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -1236,6 +1333,7 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
   constexpr int kPart = 32 * T::kJoinRow;
   float* part = reinterpret_cast<float*>(lds);
   float* stat = part + T::kWaves * kPart;  // [wave][m, l][32]
+  if (tid == 0) *(lds_ints)(lds + T::kFlag) = 0;
 #pragma unroll
   for (int d = 0; d < kDTiles; ++d)
 #pragma unroll
@@ -1253,7 +1351,8 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
   lds_barrier();
   const int here = min(32, rows - row0);
   constexpr int kQuads = DP / 4;
-  for (int i = threadIdx.x; i < here * kQuads; i += 64 * T::kWaves) {
+  bool lost = false;
+  for (int i = tid; i < here * kQuads; i += 64 * T::kWaves) {
     const int jr = i / kQuads, e = i % kQuads * 4;
     if (e >= a.d) continue;
     float m = kLowest;
@@ -1271,6 +1370,10 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[q] = __builtin_fmaf(f, x[q], acc[q]);
     }
+    if (Pass<F16>::kAgain && total < __builtin_inff()) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) lost |= !(__builtin_fabsf(acc[q]) < __builtin_inff());
+    }
     const bool some = total > 0.f || total != total;
     const float inv = some ? 1.0f / total : 0.f;
     const float lse2 = some ? log2f(total) - kLift<F16> + m * c : -__builtin_inff();
@@ -1286,21 +1389,42 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
     }
     if (work.splits > 1) {
       const int64_t at = (int64_t)blockIdx.x * a.part_step + jr;
-      if (e == 0) a.part_lse[at] = lse2;
-      if (some) *reinterpret_cast<v4f*>(a.part + at * a.d + e) = acc;
+      if (e == 0 && pass.first()) a.part_lse[at] = lse2;
+      v4f* to = reinterpret_cast<v4f*>(a.part + at * a.d + e);
+      if (some) *to = pass.first() ? acc : finite_of(*to, acc);
       continue;
     }
-    if (a.lse && e == 0) a.lse[(int64_t)jhead * a.q_tokens + w.q0 + jtoken] = lse2 * kLn2;
+    if (a.lse && e == 0 && pass.first())
+      a.lse[(int64_t)jhead * a.q_tokens + w.q0 + jtoken] = lse2 * kLn2;
     const u2 f = {pack16x2<F16>(acc[0], acc[1]), pack16x2<F16>(acc[2], acc[3])};
-    *reinterpret_cast<u2*>(a.out + (int64_t)(w.q0 + jtoken) * a.out_stride +
-                           (int64_t)jhead * a.out_head_stride + e) = f;
+    u2* to = reinterpret_cast<u2*>(a.out + (int64_t)(w.q0 + jtoken) * a.out_stride +
+                                   (int64_t)jhead * a.out_head_stride + e);
+    *to = pass.first() ? f : finite_of16<F16>(*to, f);
   }
+  return lost;
 }
 
-// Joins the splits of a row: out = sum_s 2^(lse_s - lse) out_s. A block takes a row: a
-// thread a split's factor, then groups of lanes, four elements each, the splits in turn,
-// all of whose loads are under way together.
+template <int DP, bool F16>
+__global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(AttentionArgs a) {
+  extern __shared__ __align__(1024) uint8_t lds[];
+  const int hk = (int)(blockIdx.x % (uint32_t)a.k_heads);
+  FewWork work;
+  if (!locate_few(a, blockIdx.x / (uint32_t)a.k_heads, &work)) return;
+  const float c = a.scale * kLog2e;
+  Pass<F16> pass(c);
+  const bool lost = few_pass<DP, F16>(a, work, hk, pass, lds, threadIdx.x);
+  if (!pass_again<F16>(&pass, lost, (lds_ints)(lds + Few<DP>::kFlag), c)) return;
+  lds_barrier();  // all have read the flag: the ring takes its place
+  few_pass<DP, F16>(a, work, hk, pass, lds, thread_anew());
+}
+
+// Joins the splits of a row: out = sum_s 2^(lse_s - lse) out_s, with a power of two out of
+// the factors, so that their sum is below 1 and that of the parts in fp32's range. A block
+// takes a row: a thread a split's factor, then groups of lanes, four elements each, the
+// splits in turn, all of whose loads are under way together.
 constexpr int kJoinThreads = 256;
+constexpr float kJoinScale = 1024.f;
+static_assert(kMaxSplits < kJoinScale, "the factors' sum");
 
 template <bool F16>
 __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionArgs a, int lanes) {
@@ -1349,7 +1473,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
 #pragma unroll
   for (int i = 0; i < kMaxSplits / kJoinThreads; ++i) {
     const float f = __builtin_amdgcn_exp2f(x[i] - top);  // 0 for a split that saw nothing
-    if (tid + i * kJoinThreads < splits) factor[tid + i * kJoinThreads] = f;
+    if (tid + i * kJoinThreads < splits) factor[tid + i * kJoinThreads] = f * (1 / kJoinScale);
     sum += f;
   }
 #pragma unroll
@@ -1383,7 +1507,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] += p[q];
     }
-    const float inv = none ? 0.f : 1.0f / sum;
+    const float inv = none ? 0.f : 1.0f / sum * kJoinScale;
     const u2 f = {pack16x2<F16>(v[0] * inv, v[1] * inv), pack16x2<F16>(v[2] * inv, v[3] * inv)};
     *reinterpret_cast<u2*>(a.out + token * a.out_stride + (int64_t)head * a.out_head_stride + e) =
         f;
@@ -1421,7 +1545,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_rows_kernel(Atten
     sum += f;
 #pragma unroll
     for (int q = 0; q < 4; ++q)  // what a split that saw nothing holds is not its result
-      v[q] = f != 0.f ? __builtin_fmaf(f, p[q], v[q]) : v[q];
+      v[q] = f != 0.f ? __builtin_fmaf(f * (1 / kJoinScale), p[q], v[q]) : v[q];
   }
   const bool none = sum == 0.f;
   const int64_t token = r / a.q_heads;
@@ -1429,7 +1553,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_rows_kernel(Atten
   if (a.lse && e == 0)
     a.lse[head * a.q_tokens + token] = none ? -__builtin_inff() : (top + log2f(sum)) * kLn2;
   if (e < a.d) {
-    const float inv = none ? 0.f : 1.0f / sum;
+    const float inv = none ? 0.f : 1.0f / sum * kJoinScale;
     const u2 f = {pack16x2<F16>(v[0] * inv, v[1] * inv), pack16x2<F16>(v[2] * inv, v[3] * inv)};
     *reinterpret_cast<u2*>(a.out + token * a.out_stride + (int64_t)head * a.out_head_stride + e) =
         f;

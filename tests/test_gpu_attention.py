@@ -145,6 +145,52 @@ def test_scores_that_climb_and_fall(tile, hq, hk, d, dtype):
             close(qs, ks, v, out, lse, d ** -0.5, causal)
 
 
+# every kernel: the two of many rows, that of few, heads of each padded size
+EACH = [(256, 4, 2, 128), (128, 4, 2, 128), (32, 4, 2, 128), (128, 3, 1, 64), (32, 3, 1, 64),
+        (128, 1, 1, 256), (32, 2, 1, 256), (256, 2, 2, 96)]
+
+
+@pytest.mark.parametrize("tile,hq,hk,d", EACH)
+@pytest.mark.parametrize("power", [90, 97, 120])
+def test_large_values_under_scores_that_climb_and_fall(tile, hq, hk, d, power):
+    """Scores that climb by 31 octaves behind a row's first keys, and values of which fp32
+    does not hold 2^31 times as much; a column of small ones beside them, and one of an
+    infinity."""
+    rng = np.random.default_rng(d + tile)
+    n, length = 300, 700
+    q, k, v = make(rng, [n], [length], hq, hk, d, torch.bfloat16, 0.3)
+    level = np.interp(np.arange(length), [0, 100, 350, 500, length], [0, 0, 31, 31, 0])
+    q[:, :, 0] = 1
+    k[:, :, 0] = dev(level * math.log(2) * d ** 0.5, torch.bfloat16)[:, None]
+    v *= 2.0 ** power
+    v[:, :, 1] *= 2.0 ** (-60 - power)
+    for causal in (False, True):
+        out, lse = cr.convrot_attention(q, k, v, causal=causal, return_lse=True, tile=tile)
+        close(q, k, v, out, lse, d ** -0.5, causal)
+        one = v.clone()
+        one[600, :, 5] = math.inf
+        got, got_lse = cr.convrot_attention(q, k, one, causal=causal, return_lse=True, tile=tile)
+        sees = torch.arange(n, device=DEV) + length - n >= (600 if causal else 0)
+        assert (got[sees][:, :, 5] == math.inf).all()
+        got[sees, :, 5] = out[sees, :, 5]
+        assert torch.equal(got, out) and torch.equal(got_lse, lse)
+
+
+@pytest.mark.parametrize("tile,hq,hk,d", EACH)
+@pytest.mark.parametrize("n,length", [(300, 700), (2, 9000), (40, 5000)])
+def test_values_whose_sum_leaves_fp32(n, length, tile, hq, hk, d):
+    """Equal scores and values of nearly the largest bf16: their mean is one, their sum is
+    not; one block's keys and parts that are joined."""
+    rng = np.random.default_rng(n)
+    q, k, v = make(rng, [n], [length], hq, hk, d, torch.bfloat16)
+    k[:] = k[:1]
+    v = dev((1.25 + 0.5 * rng.random((length, hk, d))) * 2.0 ** 127, torch.bfloat16)
+    v[:, :, ::3] *= -1
+    for causal in (False, True):
+        out, lse = cr.convrot_attention(q, k, v, causal=causal, return_lse=True, tile=tile)
+        close(q, k, v, out, lse, d ** -0.5, causal)
+
+
 @DTYPES
 @pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
 @pytest.mark.parametrize("hq,hk,d", [(1, 1, 8), (3, 3, 16), (4, 2, 40), (5, 1, 64), (2, 1, 72),
