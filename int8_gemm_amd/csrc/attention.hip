@@ -46,12 +46,17 @@ constexpr float kRoom = F16 ? 10.f : 32.f;
 template <bool F16>
 constexpr float kLift = F16 ? 4.f : 0.f;
 constexpr float kLowest = -3.402823466e38f;
+// Scores start from -m, so those formed below a reference far under zero have only its
+// bits. A first pass takes no reference below kDeepest / c, which leaves a weight right to
+// 2^-14: scores there have none beside any others, and a block with a row that has seen no
+// others goes over its keys again.
+constexpr float kDeepest = -256.f;
 // bf16 values may be so large (above 2^96 / keys) that such weights take their sum out of
 // fp32 (half ones, below 2^16, are not). A block in whose result something is not finite,
 // although the sum of the weights is, goes over its keys again with the reference raised at
 // every larger score and 2^32 above it, so that no row's weights sum to more than 1: the
 // elements that are finite then replace those that were not, the others stay. Looking costs
-// an instruction an element of the result and a barrier.
+// an instruction for two elements of the result and a barrier.
 constexpr float kOver = 32.f;
 constexpr float kMostOver = 1e36f;  // finite where the scale is next to nothing
 template <bool F16>
@@ -64,6 +69,29 @@ struct Pass {
     room = -over;
   }
   __device__ bool first() const { return !kAgain || over == 0.f; }
+};
+
+// EXACT: any reference, and the scores that make a row leave one far under zero are formed
+// again from zero: whether m is that far under it, the largest of them being `top` above m.
+__device__ __forceinline__ bool leaves_far(float below, float top) {
+  return below > 2.f * __builtin_fabsf(top - below);
+}
+
+// What a row's scores have to pass before it has a reference, and whether it has one by the
+// bound that it keeps.
+template <bool EXACT>
+__device__ __forceinline__ float no_reference(float c) {
+  return EXACT ? -__builtin_inff() : kDeepest / c;
+}
+template <bool EXACT>
+__device__ __forceinline__ bool referred(float raise_at) {
+  return EXACT ? raise_at > kLowest : raise_at > 0.f;
+}
+
+// What a wave finds in its rows' results: elements that are not finite though the sum of
+// their weights is, and rows without a reference that see keys.
+struct Found {
+  bool lost, unmet;
 };
 
 template <bool F16>
@@ -96,6 +124,18 @@ __device__ __forceinline__ void static_for_each(F& f, std::integer_sequence<int,
 template <int N, typename F>
 __device__ __forceinline__ void static_for(F f) {
   static_for_each(f, std::make_integer_sequence<int, N>{});
+}
+
+__device__ __forceinline__ int wave_number(int tid) {
+  return __builtin_amdgcn_readfirstlane(tid >> 6);
+}
+
+// The thread's number once more, of which the compiler does not know that it is the same:
+// nothing worked out from it is kept in registers from one part of a kernel to the next.
+__device__ __forceinline__ int thread_anew() {
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  return tid;
 }
 
 __device__ __forceinline__ float other_half(float v) {
@@ -194,9 +234,9 @@ __device__ __forceinline__ u4 values(const uint8_t* vt, int key, int dtile) {
   return (u4){w0.x, w0.y, w1.x, w1.y};
 }
 
-template <int DP, int QT, int NW, bool F16>
+template <int DP, int NW>
 struct Kernel {
-  static constexpr int kRows = 32 * QT * NW;         // rows of a block
+  static constexpr int kRows = 32 * NW;              // rows of a block
   static constexpr int kRowBytes = DP * 2;
   static constexpr int kChunks = DP / 8;
   static constexpr int kTileBytes = kTileKeys * kRowBytes;
@@ -266,6 +306,13 @@ __device__ __forceinline__ void add_nonfinite(const AttentionArgs& a, int64_t ke
   }
 }
 
+// What the kernels for many rows are called with: slots per key head, XCDs, and how many of
+// those share a key head.
+struct TileCall {
+  AttentionArgs a;
+  uint32_t slots, xcds, share;
+};
+
 // A block's tile of rows and its keys.
 struct Tile {
   Where w;
@@ -283,10 +330,11 @@ struct Tile {
 // heads take a head's tiles in turn. The first a.whole tiles are a block's each, the
 // last ones are split. False for a block without a tile.
 template <int ROWS, bool CAUSAL>
-__device__ __forceinline__ bool locate(const AttentionArgs& a, uint32_t slots, uint32_t xcds,
-                                       uint32_t share, Tile* t) {
-  t->tail = a.splits > 1 && blockIdx.x >= a.whole;
-  uint32_t id = t->tail ? blockIdx.x - a.whole : blockIdx.x;
+__device__ __forceinline__ bool locate(const TileCall& call, uint32_t block, Tile* t) {
+  const AttentionArgs& a = call.a;
+  const uint32_t slots = call.slots, xcds = call.xcds, share = call.share;
+  t->tail = a.splits > 1 && block >= a.whole;
+  uint32_t id = t->tail ? block - a.whole : block;
   if (CAUSAL && !t->tail) {
     const uint32_t x = id % xcds, heads = (uint32_t)a.k_heads * share / xcds;
     const uint32_t at = id / xcds * share + x % share;
@@ -365,20 +413,21 @@ __device__ __forceinline__ U finite_of16(U before, U now) {
 template <int ROWS, int DTILES, bool F16>
 __device__ __forceinline__ bool finish(const AttentionArgs& a, const Tile& t, int row, float l,
                                        float m, float c, const v16f (&o)[DTILES], bool first) {
-  const int half = (threadIdx.x >> 5) & 1;
+  const int half = (thread_anew() >> 5) & 1;
   const float sum = l + other_half(l);
   const bool some = sum > 0.f || sum != sum;
   const float inv = some ? 1.0f / sum : 0.f;
   const float lse2 = some ? log2f(sum) - kLift<F16> + m * c : -__builtin_inff();
   if (row >= t.rows) return false;
-  float probe = 0.f;  // NaN once something is not finite
+  float most = 0.f;  // infinite or NaN once something is
   if (Pass<F16>::kAgain) {
 #pragma unroll
     for (int d = 0; d < DTILES; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) probe = __builtin_fmaf(o[d][i], 0.f, probe);
+      for (int i = 0; i < 16; ++i)
+        most = __builtin_elementwise_maximum(most, __builtin_fabsf(o[d][i]));
   }
-  const bool lost = probe != probe && sum < __builtin_inff();
+  const bool lost = !(most < __builtin_inff()) && sum < __builtin_inff();
   if (t.tail) {
     const int64_t at = (int64_t)t.piece * ROWS + row - t.row0;
     if (half == 0 && first) a.part_lse[at] = lse2;
@@ -425,26 +474,32 @@ __device__ __forceinline__ bool finish(const AttentionArgs& a, const Tile& t, in
   return lost;
 }
 
-// Whether the block goes over its keys again: some wave of it lost an element in its first
-// pass. Every wave comes here with what it found. The second pass is code of its own: as
-// the same code in a loop it kept so much from one to the other that the first one of 32760
-// x 512 keys x 40 heads took 444 us for 427.
-template <bool F16>
-__device__ __forceinline__ bool pass_again(Pass<F16>* pass, bool lost, lds_ints flag, float c) {
-  if (!Pass<F16>::kAgain) return false;
-  if (__builtin_expect(__any(lost), 0)) *flag = 1;
+// What some wave of a block finds, noted in a flag for all of them, which come here with
+// what they found. What a block then does again is code of its own: as the same code in a
+// loop it kept so much from one pass to the next that the first one of 32760 x 512 keys x 40
+// heads took 444 us for 427.
+__device__ __forceinline__ void note(bool what, lds_ints flag) {
+  if (__builtin_expect(__any(what), 0)) *flag = 1;
+}
+__device__ __forceinline__ void all_noted() {
   wait_lgkm0();
   lds_barrier();
-  if (__builtin_expect(*flag == 0, 1)) return false;
-  pass->again(c);
-  return true;
 }
-// The thread's number, of which the compiler does not know that it is the same: nothing
-// worked out from it for the first pass is kept for the second.
-__device__ __forceinline__ int thread_anew() {
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));
-  return tid;
+
+// The kernel's arguments (its only parameter) and the block's number once more, as
+// thread_anew's.
+template <typename C>
+__device__ __forceinline__ C call_anew() {
+  auto from = (const __attribute__((address_space(4))) C*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(from));
+  C call;
+  __builtin_memcpy(&call, from, sizeof(C));
+  return call;
+}
+__device__ __forceinline__ uint32_t block_anew() {
+  uint32_t block = blockIdx.x;
+  asm volatile("" : "+s"(block));
+  return block;
 }
 
 // The first key and value of a tile's head, as bytes.
@@ -457,7 +512,7 @@ __device__ __forceinline__ const int8_t* head_bytes(const uint16_t* p, const Whe
 template <int STEPS, bool CAUSAL>
 __device__ __forceinline__ void load_query(const AttentionArgs& a, const Where& w, int hk, int row,
                                            u4 (&qf)[STEPS], int* seen) {
-  const int half = (threadIdx.x >> 5) & 1;
+  const int half = (thread_anew() >> 5) & 1;
   const int r = min(row, w.lq * a.group - 1);
   const int token = r / a.group, head = hk * a.group + r % a.group;
   *seen = CAUSAL ? min(w.lk, token + w.lk - w.lq + 1) : w.lk;
@@ -491,21 +546,19 @@ __device__ __forceinline__ void mask(v16f* s, int key0, int seen) {
 // busy 0.37 of the cycles at 2.0 GHz (power: fetching the next tile early gains nothing).
 // Heads of up to 256: 8192 x 8 heads of 256 in 685 us (0.80 PFLOP/s), one block a compute
 // unit, its output a whole 128 registers a lane.
-template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__device__ __forceinline__ bool walk(const AttentionArgs& a, const Tile& w,
-                                     const Pass<F16>& pass, uint8_t* lds, lds_ints flags,
-                                     int tid) {
-  using T = Kernel<DP, QT, NW, F16>;
+// One pass of a wave's 32 rows, from row0 of the block's ROWS on, over the block's keys, U
+// units of 32 at a time.
+template <int DP, int NW, bool F16, bool CAUSAL, int ROWS, int U, bool EXACT>
+__device__ __forceinline__ Found walk(const AttentionArgs& a, const Tile& w,
+                                      const Pass<F16>& pass, uint8_t* lds, lds_ints flags,
+                                      int tid, int row0) {
+  using T = Kernel<DP, NW>;
   const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = wave_number(tid);
   const int half = lane >> 5, col = lane & 31;
-  int row[QT], seen[QT];
-  u4 qf[QT][T::kSteps];
-#pragma unroll
-  for (int q = 0; q < QT; ++q) {
-    row[q] = w.row0 + (wave * QT + q) * 32 + col;
-    load_query<T::kSteps, CAUSAL>(a, w.w, w.hk, row[q], qf[q], &seen[q]);
-  }
+  int seen;
+  u4 qf[T::kSteps];
+  load_query<T::kSteps, CAUSAL>(a, w.w, w.hk, w.row0 + row0 + col, qf, &seen);
 
   // copies: lane i of a copy fills the 16 bytes behind 16 i
   const int8_t* kbase = head_bytes(a.k, w.w, a.k_stride, a.k_head_stride, w.hk);
@@ -527,17 +580,11 @@ __device__ __forceinline__ bool walk(const AttentionArgs& a, const Tile& w,
   };
 
   const float c = a.scale * kLog2e;
-  v16f o[QT][T::kDTiles];
-  v16f below[QT];  // -m in every place: the first product starts from it
-  float l[QT], raise_at[QT];
+  v16f o[T::kDTiles];
+  v16f below = (v16f){0};  // -m in every place: the first product starts from it
+  float l = 0.f, raise_at = no_reference<EXACT>(c);
 #pragma unroll
-  for (int q = 0; q < QT; ++q) {
-    below[q] = (v16f){0};
-    raise_at[q] = -__builtin_inff();  // no m yet
-    l[q] = 0.f;
-#pragma unroll
-    for (int d = 0; d < T::kDTiles; ++d) o[q][d] = (v16f){0};
-  }
+  for (int d = 0; d < T::kDTiles; ++d) o[d] = (v16f){0};
 
   if (w.t0 < w.tiles) issue(w.t0, 0);
   for (int t = w.t0; t < w.tiles; ++t) {
@@ -548,89 +595,82 @@ __device__ __forceinline__ bool walk(const AttentionArgs& a, const Tile& w,
     if (t + 1 < w.tiles) issue(t + 1, stage ^ 1);
     const uint8_t* kt = lds + stage * T::kTileBytes;
     uint8_t* vt = lds + (T::kStages + stage) * T::kTileBytes;
-    v16f s[2][QT];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int st = 0; st < T::kSteps; ++st) {
-        const int r = u * 32 + col;
-        const u4 kf = *reinterpret_cast<const u4*>(kt + r * T::kRowBytes +
-                                                   k_slot<DP>(r, 2 * st + half) * 16);
-#pragma unroll
-        for (int q = 0; q < QT; ++q)
-          s[u][q] = mfma<F16>(kf, qf[q][st], st == 0 ? below[q] : s[u][q]);
-      }
-    }
     const bool masked = (t + 1) * kTileKeys > w.full;
-    if (masked) {
+#pragma unroll 1
+    for (int u0 = 0; u0 < 2; u0 += U) {
+      v16f s[U];
+      float top;
+      // the units' scores from `from`, and the row's largest
+      auto score = [&](const v16f& from) __attribute__((always_inline)) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < U; ++u) {
+          s[u] = from;
 #pragma unroll
-        for (int q = 0; q < QT; ++q) mask(&s[u][q], t * kTileKeys + u * 32, seen[q]);
-    }
-    float top[QT];
-    bool raise = false;
+          for (int st = 0; st < T::kSteps; ++st) {
+            const int r = (u0 + u) * 32 + col;
+            const u4 kf = *reinterpret_cast<const u4*>(kt + r * T::kRowBytes +
+                                                       k_slot<DP>(r, 2 * st + half) * 16);
+            s[u] = mfma<F16>(kf, qf[st], s[u]);
+          }
+          if (masked) mask(&s[u], t * kTileKeys + (u0 + u) * 32, seen);
+        }
+        top = s[0][0];
 #pragma unroll
-    for (int q = 0; q < QT; ++q) {
-      top[q] = s[0][q][0];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+          for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+        top = fmaxf(top, other_half(top));
+      };
+      score(below);
+      if (__any(top > raise_at)) {
+        const bool up = top > raise_at;
+        const float left = EXACT && up && leaves_far(below[0], top) ? below[0] : 0.f;
+        if (EXACT && __any(left != 0.f)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top[q] = fmaxf(top[q], s[u][q][i]);
-      top[q] = fmaxf(top[q], other_half(top[q]));
-      raise |= top[q] > raise_at[q];
-    }
-    if (__any(raise)) {
-#pragma unroll
-      for (int q = 0; q < QT; ++q) {
-        const bool up = top[q] > raise_at[q];
-        const float by = up ? top[q] + pass.over : 0.f;
+          for (int i = 0; i < 16; ++i) below[i] = left != 0.f ? 0.f : below[i];
+          score(below);
+        }
+        const float by = up ? top + pass.over : 0.f;
         // a row without an m has nothing to scale yet (or NaN, which stays)
         const float alpha =
-            up && raise_at[q] > kLowest ? __builtin_amdgcn_exp2f(-by * c) : 1.f;
-        raise_at[q] = up ? pass.room : raise_at[q];
-        l[q] *= alpha;
+            up && referred<EXACT>(raise_at) ? __builtin_amdgcn_exp2f(-(by + left) * c) : 1.f;
+        raise_at = up ? pass.room : raise_at;
+        l *= alpha;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) below[q][i] -= by;
+        for (int i = 0; i < 16; ++i) below[i] -= by;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[u][q][i] -= by;
+          for (int i = 0; i < 16; ++i) s[u][i] -= by;
 #pragma unroll
         for (int d = 0; d < T::kDTiles; ++d)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[q][d][i] *= alpha;
+          for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
       }
-    }
-    u4 p[2][QT][2];
+      u4 p[U][2];
 #pragma unroll
-    for (int q = 0; q < QT; ++q) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[u][q][i] = __builtin_amdgcn_exp2f(
-              F16 ? __builtin_fmaf(s[u][q][i], c, kLift<F16>) : s[u][q][i] * c);
-          l[q] += s[u][q][i];
+          s[u][i] =
+              __builtin_amdgcn_exp2f(F16 ? __builtin_fmaf(s[u][i], c, kLift<F16>) : s[u][i] * c);
+          l += s[u][i];
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            p[u][q][h][e] = pack16x2<F16>(s[u][q][8 * h + 2 * e], s[u][q][8 * h + 2 * e + 1]);
+            p[u][h][e] = pack16x2<F16>(s[u][8 * h + 2 * e], s[u][8 * h + 2 * e + 1]);
       }
+      if (u0 == 0 && masked && clear_nonfinite<F16, DP, kTileKeys>(vt)) flags[0] = 1;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int d = 0; d < T::kDTiles; ++d)
+            o[d] = mfma<F16>(values<DP>(vt, (u0 + u) * 32 + h * 16, d), p[u][h], o[d]);
     }
-    if (masked && clear_nonfinite<F16, DP, kTileKeys>(vt)) flags[0] = 1;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int d = 0; d < T::kDTiles; ++d) {
-          const u4 vf = values<DP>(vt, u * 32 + h * 16, d);
-#pragma unroll
-          for (int q = 0; q < QT; ++q) o[q][d] = mfma<F16>(vf, p[u][q][h], o[q][d]);
-        }
   }
 
   if (CAUSAL || w.full % kTileKeys) {
@@ -640,35 +680,67 @@ __device__ __forceinline__ bool walk(const AttentionArgs& a, const Tile& w,
       const int to = min(w.end, w.tiles * kTileKeys);
 #pragma unroll 1
       for (int key = max(w.full / kTileKeys, w.t0) * kTileKeys; key < to; ++key)
-#pragma unroll
-        for (int q = 0; q < QT; ++q)
-          add_nonfinite<T::kDTiles, F16>(a, w.w.k0 + key, w.hk, key < seen[q], o[q]);
+        add_nonfinite<T::kDTiles, F16>(a, w.w.k0 + key, w.hk, key < seen, o);
     }
   }
-  bool lost = false;
-#pragma unroll
-  for (int q = 0; q < QT; ++q)
-    lost |= finish<T::kRows, T::kDTiles, F16>(a, w, row[q], l[q], -below[q][0], c, o[q],
-                                              pass.first());
-  return lost;
+  const int row = w.row0 + row0 + (thread_anew() & 31);
+  const bool unmet = !EXACT && raise_at < 0.f && l == 0.f && row < w.rows &&
+                     seen > w.t0 * kTileKeys;
+  return {finish<ROWS, T::kDTiles, F16>(a, w, row, l, -below[0], c, o, pass.first()), unmet};
+}
+
+// What a block goes over again, QT times 32 rows a wave: everything from the start on
+// (`whole`), or what was lost.
+template <int DP, int QT, int NW, bool F16, bool CAUSAL>
+__device__ __forceinline__ void walk_anew(bool whole, uint8_t* lds, lds_ints flags) {
+  constexpr int kRows = 32 * QT * NW;
+  const TileCall call = call_anew<TileCall>();
+  const AttentionArgs& a = call.a;
+  const int tid = thread_anew();
+  Tile w;
+  if (!locate<kRows, CAUSAL>(call, block_anew(), &w)) return;
+  const float c = a.scale * kLog2e;
+  Pass<F16> pass(c);
+  bool lost;
+  do {
+    if (!whole) pass.again(c);
+    lost = false;
+#pragma unroll 1
+    for (int q = 0; q < QT; ++q) {
+      if (q > 0) lds_barrier();  // the last tile's reads are done
+      lost |= walk<DP, NW, F16, CAUSAL, kRows, 1, true>(a, w, pass, lds, flags, tid,
+                                                        (wave_number(tid) * QT + q) * 32)
+                  .lost;
+    }
+    if (!Pass<F16>::kAgain || !whole) return;
+    whole = false;
+    note(lost, flags + 1);
+    all_noted();
+  } while (flags[1]);
 }
 
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(AttentionArgs a,
-                                                                              uint32_t slots,
-                                                                              uint32_t xcds,
-                                                                              uint32_t share) {
-  using T = Kernel<DP, QT, NW, F16>;
+__device__ __forceinline__ void finish_block(Found found, uint8_t* lds, lds_ints flags) {
+  note(found.lost, flags + 1);
+  note(found.unmet, flags + 2);
+  all_noted();
+  const int whole = flags[2];
+  if (__builtin_expect((whole | flags[1]) != 0, 0))
+    walk_anew<DP, QT, NW, F16, CAUSAL>(whole != 0, lds, flags);
+}
+
+template <int DP, int NW, bool F16, bool CAUSAL>
+__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(TileCall call) {
+  const AttentionArgs& a = call.a;
+  using T = Kernel<DP, NW>;
   extern __shared__ __align__(1024) uint8_t lds[];
   lds_ints flags = (lds_ints)(lds + 2 * T::kStages * T::kTileBytes);
-  if (threadIdx.x == 0) flags[0] = flags[1] = 0;  // a barrier follows in every tile
+  if (threadIdx.x == 0) flags[0] = flags[1] = flags[2] = 0;  // a barrier follows in every tile
   Tile w;
-  if (!locate<T::kRows, CAUSAL>(a, slots, xcds, share, &w)) return;
-  const float c = a.scale * kLog2e;
-  Pass<F16> pass(c);
-  const bool lost = walk<DP, QT, NW, F16, CAUSAL>(a, w, pass, lds, flags, threadIdx.x);
-  if (pass_again<F16>(&pass, lost, flags + 1, c))
-    walk<DP, QT, NW, F16, CAUSAL>(a, w, pass, lds, flags, thread_anew());
+  if (!locate<T::kRows, CAUSAL>(call, blockIdx.x, &w)) return;
+  const Found found = walk<DP, NW, F16, CAUSAL, T::kRows, 2, false>(
+      a, w, Pass<F16>(a.scale * kLog2e), lds, flags, threadIdx.x, wave_number(threadIdx.x) * 32);
+  finish_block<DP, 1, NW, F16, CAUSAL>(found, lds, flags);
 }
 
 // MFMAs of the pipeline below, whose accumulators stay where they are put: the output in
@@ -760,19 +832,19 @@ struct Wide {
 };
 
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kernel(
-    AttentionArgs a, uint32_t slots, uint32_t xcds, uint32_t share) {
+__global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kernel(TileCall call) {
+  const AttentionArgs& a = call.a;
   using T = Wide<DP, QT, NW>;
   constexpr int kFrags = 2 * T::kSteps, kSlots = kFrags * QT, kAhead = 3, kRing = 4;
   constexpr int kElems = 16 * QT;  // of a lane and unit
   extern __shared__ __align__(1024) uint8_t lds[];
   lds_ints flags = (lds_ints)(lds + 2 * T::kStages * T::kTileBytes);
-  if (threadIdx.x == 0) flags[0] = flags[1] = 0;
+  if (threadIdx.x == 0) flags[0] = flags[1] = flags[2] = 0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
   Tile w;
-  if (!locate<T::kRows, CAUSAL>(a, slots, xcds, share, &w)) return;
+  if (!locate<T::kRows, CAUSAL>(call, blockIdx.x, &w)) return;
 
   const int8_t* kbase = head_bytes(a.k, w.w, a.k_stride, a.k_head_stride, w.hk);
   const int8_t* vbase = head_bytes(a.v, w.w, a.v_stride, a.v_head_stride, w.hk);
@@ -796,25 +868,24 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
     if (t < w.tiles) copy(vbase, vstride, true, t, T::kV + stage * T::kTileBytes);
   };
   const float c = a.scale * kLog2e;
-  Pass<F16> pass(c);
+  const float room = kRoom<F16> / c;
   copy_k(w.t0, 0);
   copy_v(w.t0, 0);
   copy_k(w.t0 + 1, 1);
 
-  int row[QT], seen[QT];
+  int seen[QT];
   u4 qf[QT][T::kSteps];
+  const int row0 = w.row0 + wave * QT * 32;
 #pragma unroll
-  for (int q = 0; q < QT; ++q) {
-    row[q] = w.row0 + (wave * QT + q) * 32 + col;
-    load_query<T::kSteps, CAUSAL>(a, w.w, w.hk, row[q], qf[q], &seen[q]);
-  }
+  for (int q = 0; q < QT; ++q)
+    load_query<T::kSteps, CAUSAL>(a, w.w, w.hk, row0 + q * 32 + col, qf[q], &seen[q]);
   v16f o[QT][T::kDTiles], below[QT], sa[QT], sb[QT];
   u4 pa[QT][2], pb[QT][2];
   float l[QT], raise_at[QT], top[QT];
 #pragma unroll
   for (int q = 0; q < QT; ++q) {
     below[q] = (v16f){0};
-    raise_at[q] = -__builtin_inff();
+    raise_at[q] = no_reference<false>(c);
     l[q] = 0.f;
 #pragma unroll
     for (int d = 0; d < T::kDTiles; ++d) o[q][d] = (v16f){0};
@@ -946,8 +1017,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
         const float by = up ? to : 0.f;
         // a row without an m has nothing to scale yet (or NaN, which stays)
         const float alpha =
-            up && raise_at[q] > kLowest ? __builtin_amdgcn_exp2f(-by * c) : 1.f;
-        raise_at[q] = up ? pass.room : raise_at[q];
+            up && referred<false>(raise_at[q]) ? __builtin_amdgcn_exp2f(-by * c) : 1.f;
+        raise_at[q] = up ? room : raise_at[q];
         l[q] *= alpha;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -1071,14 +1142,15 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
           add_nonfinite<T::kDTiles, F16>(a, w.w.k0 + key, w.hk, key < seen[q], o[q]);
     }
   }
-  bool lost = false;
+  Found found = {false, false};
 #pragma unroll
-  for (int q = 0; q < QT; ++q)
-    lost |= finish<T::kRows, T::kDTiles, F16>(a, w, row[q], l[q], -below[q][0], c, o[q],
-                                              pass.first());
-  // without the pipeline
-  if (pass_again<F16>(&pass, lost, flags + 1, c))
-    walk<DP, QT, NW, F16, CAUSAL>(a, w, pass, lds, flags, thread_anew());
+  for (int q = 0; q < QT; ++q) {
+    const int row = row0 + q * 32 + (thread_anew() & 31);
+    found.unmet |=
+        raise_at[q] < 0.f && l[q] == 0.f && row < w.rows && seen[q] > w.t0 * kTileKeys;
+    found.lost |= finish<T::kRows, T::kDTiles, F16>(a, w, row, l[q], -below[q][0], c, o[q], true);
+  }
+  finish_block<DP, QT, NW, F16, CAUSAL>(found, lds, flags);
 }
 
 // ---- few rows: single tokens against a long cache ----------------------------
@@ -1105,7 +1177,7 @@ struct Few {
   static constexpr int kJoinRow = DP + 4;  // floats of a row of partial sums
   static constexpr int kLds = kWaves * kWaveBytes;
   static constexpr int kFlag = kWaves * (32 * kJoinRow + 64) * 4;  // behind the sums
-  static_assert(kFlag + 4 <= kLds, "sums fit the ring");
+  static_assert(kFlag + 8 <= kLds, "sums fit the ring");
 };
 
 // What a block does: a tile of a sequence's rows with one of the `splits` parts of its
@@ -1186,15 +1258,16 @@ __device__ __forceinline__ bool locate_few(const AttentionArgs& a, uint32_t at, 
 }
 
 // One pass over a block's keys; the sums of its waves joined, and written.
-template <int DP, bool F16>
-__device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& work, int hk,
-                                         const Pass<F16>& pass, uint8_t* lds, int tid) {
+template <int DP, bool F16, bool EXACT>
+__device__ __forceinline__ Found few_pass(const AttentionArgs& a, const FewWork& work,
+                                          uint32_t block, const Pass<F16>& pass, uint8_t* lds,
+                                          int tid) {
   using T = Few<DP>;
   constexpr int kSteps = DP / 16, kDTiles = DP / 32;
   const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = wave_number(tid);
   const int half = lane >> 5, col = lane & 31;
-  const int group = a.group;
+  const int group = a.group, hk = (int)(block % (uint32_t)a.k_heads);
   const Where& w = work.w;
 
   const int rows = w.lq * group, row0 = w.tile * 32;
@@ -1243,7 +1316,7 @@ __device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& 
   v16f o[kDTiles], below = (v16f){0};
 #pragma unroll
   for (int d = 0; d < kDTiles; ++d) o[d] = (v16f){0};
-  float l = 0.f, raise_at = -__builtin_inff();
+  float l = 0.f, raise_at = no_reference<EXACT>(c);
 
   int u = first + wave, stage = 0;
   if (u < last) issue(u, 0);
@@ -1260,23 +1333,35 @@ __device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& 
     asm volatile("" ::: "memory");
     const uint8_t* kt = lds + ring + stage * 2 * T::kUnitBytes;
     uint8_t* vt = lds + ring + stage * 2 * T::kUnitBytes + T::kUnitBytes;
-    v16f s = below;
-#pragma unroll
-    for (int st = 0; st < kSteps; ++st) {
-      const u4 kf = *reinterpret_cast<const u4*>(kt + col * T::kRowBytes +
-                                                 k_slot<DP>(col, 2 * st + half) * 16);
-      s = mfma<F16>(kf, qf[st], s);
-    }
+    v16f s;
     const int key0 = u * T::kUnit;
-    if (key0 + T::kUnit > full) mask(&s, key0, seen);
-    float top = s[0];
+    float top;
+    auto score = [&](const v16f& from) __attribute__((always_inline)) {
+      s = from;
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-    top = fmaxf(top, other_half(top));
+      for (int st = 0; st < kSteps; ++st) {
+        const u4 kf = *reinterpret_cast<const u4*>(kt + col * T::kRowBytes +
+                                                   k_slot<DP>(col, 2 * st + half) * 16);
+        s = mfma<F16>(kf, qf[st], s);
+      }
+      if (key0 + T::kUnit > full) mask(&s, key0, seen);
+      top = s[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+      top = fmaxf(top, other_half(top));
+    };
+    score(below);
     if (__any(top > raise_at)) {
       const bool up = top > raise_at;
+      const float left = EXACT && up && leaves_far(below[0], top) ? below[0] : 0.f;
+      if (EXACT && __any(left != 0.f)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) below[i] = left != 0.f ? 0.f : below[i];
+        score(below);
+      }
       const float by = up ? top + pass.over : 0.f;
-      const float alpha = up && raise_at > kLowest ? __builtin_amdgcn_exp2f(-by * c) : 1.f;
+      const float alpha =
+          up && referred<EXACT>(raise_at) ? __builtin_amdgcn_exp2f(-(by + left) * c) : 1.f;
       raise_at = up ? pass.room : raise_at;
       l *= alpha;
 #pragma unroll
@@ -1333,7 +1418,8 @@ __device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& 
   constexpr int kPart = 32 * T::kJoinRow;
   float* part = reinterpret_cast<float*>(lds);
   float* stat = part + T::kWaves * kPart;  // [wave][m, l][32]
-  if (tid == 0) *(lds_ints)(lds + T::kFlag) = 0;
+  lds_ints flags = (lds_ints)(lds + T::kFlag);
+  if (tid == 0) flags[0] = flags[1] = 0;
 #pragma unroll
   for (int d = 0; d < kDTiles; ++d)
 #pragma unroll
@@ -1344,14 +1430,14 @@ __device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& 
     }
   if (half == 0) {
     // a row without an m has seen nothing, or only NaN
-    stat[wave * 64 + col] = raise_at > kLowest ? -below[0] : kLowest;
+    stat[wave * 64 + col] = referred<EXACT>(raise_at) ? -below[0] : kLowest;
     stat[wave * 64 + 32 + col] = sum;
   }
   wait_lgkm0();
   lds_barrier();
   const int here = min(32, rows - row0);
   constexpr int kQuads = DP / 4;
-  bool lost = false;
+  Found found = {false, false};
   for (int i = tid; i < here * kQuads; i += 64 * T::kWaves) {
     const int jr = i / kQuads, e = i % kQuads * 4;
     if (e >= a.d) continue;
@@ -1372,12 +1458,15 @@ __device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& 
     }
     if (Pass<F16>::kAgain && total < __builtin_inff()) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) lost |= !(__builtin_fabsf(acc[q]) < __builtin_inff());
+      for (int q = 0; q < 4; ++q) found.lost |= !(__builtin_fabsf(acc[q]) < __builtin_inff());
     }
     const bool some = total > 0.f || total != total;
     const float inv = some ? 1.0f / total : 0.f;
     const float lse2 = some ? log2f(total) - kLift<F16> + m * c : -__builtin_inff();
     const int jtoken = (row0 + jr) / group, jhead = hk * group + (row0 + jr) % group;
+    if (!EXACT)
+      found.unmet |=
+          total == 0.f && (a.causal ? min(w.lk, jtoken + shift) : w.lk) > first * T::kUnit;
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[q] *= inv;
     if (a.splits > 1 && e == 0 && work.split == 0) {
@@ -1388,7 +1477,7 @@ __device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& 
                     work.splits > 1 ? work.splits : 0);
     }
     if (work.splits > 1) {
-      const int64_t at = (int64_t)blockIdx.x * a.part_step + jr;
+      const int64_t at = (int64_t)block * a.part_step + jr;
       if (e == 0 && pass.first()) a.part_lse[at] = lse2;
       v4f* to = reinterpret_cast<v4f*>(a.part + at * a.d + e);
       if (some) *to = pass.first() ? acc : finite_of(*to, acc);
@@ -1401,21 +1490,42 @@ __device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& 
                                    (int64_t)jhead * a.out_head_stride + e);
     *to = pass.first() ? f : finite_of16<F16>(*to, f);
   }
-  return lost;
+  return found;
+}
+
+// What a block goes over again, as walk_anew.
+template <int DP, bool F16>
+__device__ __forceinline__ void few_anew(bool whole, uint8_t* lds, lds_ints flags) {
+  const AttentionArgs a = call_anew<AttentionArgs>();
+  const uint32_t block = block_anew();
+  FewWork work;
+  if (!locate_few(a, block / (uint32_t)a.k_heads, &work)) return;
+  const float c = a.scale * kLog2e;
+  Pass<F16> pass(c);
+  do {
+    lds_barrier();  // all have read the flags: the ring takes their place
+    if (!whole) pass.again(c);
+    const Found found = few_pass<DP, F16, true>(a, work, block, pass, lds, thread_anew());
+    if (!Pass<F16>::kAgain || !whole) return;
+    whole = false;
+    note(found.lost, flags);
+    all_noted();
+  } while (flags[0]);
 }
 
 template <int DP, bool F16>
 __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(AttentionArgs a) {
   extern __shared__ __align__(1024) uint8_t lds[];
-  const int hk = (int)(blockIdx.x % (uint32_t)a.k_heads);
   FewWork work;
   if (!locate_few(a, blockIdx.x / (uint32_t)a.k_heads, &work)) return;
-  const float c = a.scale * kLog2e;
-  Pass<F16> pass(c);
-  const bool lost = few_pass<DP, F16>(a, work, hk, pass, lds, threadIdx.x);
-  if (!pass_again<F16>(&pass, lost, (lds_ints)(lds + Few<DP>::kFlag), c)) return;
-  lds_barrier();  // all have read the flag: the ring takes its place
-  few_pass<DP, F16>(a, work, hk, pass, lds, thread_anew());
+  const Found found = few_pass<DP, F16, false>(a, work, blockIdx.x,
+                                               Pass<F16>(a.scale * kLog2e), lds, threadIdx.x);
+  lds_ints flags = (lds_ints)(lds + Few<DP>::kFlag);
+  note(found.lost, flags);
+  note(found.unmet, flags + 1);
+  all_noted();
+  const int whole = flags[1];
+  if (__builtin_expect((whole | flags[0]) != 0, 0)) few_anew<DP, F16>(whole != 0, lds, flags);
 }
 
 // Joins the splits of a row: out = sum_s 2^(lse_s - lse) out_s, with a power of two out of
@@ -1582,15 +1692,16 @@ hipError_t launch_tiles(K kern, int threads, int lds, const AttentionArgs& a,
     const int64_t of_group = p.slots * (a.k_heads / (int)common);
     grid = (of_group + share - 1) / share * xcds;
   }
-  kern<<<dim3((uint32_t)grid), dim3(threads), lds, st>>>(a, (uint32_t)p.slots, xcds, share);
+  const TileCall call = {a, (uint32_t)p.slots, xcds, share};
+  kern<<<dim3((uint32_t)grid), dim3(threads), lds, st>>>(call);
   return hipGetLastError();
 }
 
-template <int DP, int QT, int NW, bool F16>
+template <int DP, int NW, bool F16>
 hipError_t launch_tile(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
-  return launch_tiles(a.causal ? attention_kernel<DP, QT, NW, F16, true>
-                               : attention_kernel<DP, QT, NW, F16, false>,
-                      64 * NW, Kernel<DP, QT, NW, F16>::kLds, a, p, st);
+  return launch_tiles(a.causal ? attention_kernel<DP, NW, F16, true>
+                               : attention_kernel<DP, NW, F16, false>,
+                      64 * NW, Kernel<DP, NW>::kLds, a, p, st);
 }
 
 template <int DP, int QT, int NW, bool F16>
@@ -1625,9 +1736,9 @@ hipError_t launch_dtype(const AttentionArgs& a, const AttentionPlan& p, hipStrea
   else if (a.d <= 64)
     e = launch_wide<64, 1, 4, F16>(a, p, st);
   else if (a.d <= 128)
-    e = launch_tile<128, 1, 4, F16>(a, p, st);
+    e = launch_tile<128, 4, F16>(a, p, st);
   else
-    e = launch_tile<256, 1, 4, F16>(a, p, st);
+    e = launch_tile<256, 4, F16>(a, p, st);
   if (e != hipSuccess || a.splits == 1) return e;
   int lanes = 1;
   while (lanes * 4 < a.d) lanes *= 2;

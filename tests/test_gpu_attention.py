@@ -192,6 +192,56 @@ def test_values_whose_sum_leaves_fp32(n, length, tile, hq, hk, d):
 
 
 @DTYPES
+@pytest.mark.parametrize("tile,hq,hk,d", EACH)
+@pytest.mark.parametrize("levels", [(-1e6,), (-1e9, -1e5), (-1e30,)], ids=str)
+def test_keys_far_below_the_others_take_no_bits_from_them(tile, hq, hk, d, levels, dtype):
+    """A row's first keys may score any distance below those that carry its weight: the
+    tolerance is that of the latter alone. Some rows score all keys alike, others by half."""
+    if dtype == torch.float16:
+        levels = [max(x, -6e4) for x in levels]     # of half's range, times q and scale
+    rng = np.random.default_rng(d + tile)
+    n, length, far = 300, 900, 160
+    q, k, v = make(rng, [n], [length], hq, hk, d, dtype, 2.0)
+    scale = d ** -0.5
+    up = 1.0 if dtype == torch.bfloat16 else 64.0
+    q[:, :, 0] = dev(rng.choice([0, 0.5, 1], (n, hq)) * up, dtype)
+    q[:, 0, 0] = up
+    k[:, :, 0] = 0
+    each = far // len(levels)
+    for i, x in enumerate(levels):
+        k[i * each:(i + 1) * each, :, 0] = x if dtype == torch.float16 else x / scale
+    v[:far] = 100
+    for causal in (False, True):
+        out, lse = cr.convrot_attention(q, k, v, causal=causal, return_lse=True, tile=tile)
+        for h in range(hq):
+            low = (q[:, h, 0] > 0).cpu()
+            g = h // (hq // hk)
+            qh, kh, vh = q[:, h:h + 1], k[:, g:g + 1], v[:, g:g + 1]
+            rest, kh = qh.clone(), kh.clone()
+            rest[:, :, 0] = kh[:, :, 0] = 0         # 0 on one side or both where a key counts
+            for rows, keys in ((low, (kh[far:], vh[far:])), (~low, (kh, vh))):
+                if not causal:
+                    close(rest[rows], *keys, out[rows, h:h + 1], lse[h:h + 1, rows], scale, False)
+                elif rows.all():
+                    close(rest, *keys, out[:, h:h + 1], lse[h:h + 1], scale, True)
+
+
+@DTYPES
+@pytest.mark.parametrize("tile,hq,hk,d", EACH)
+@pytest.mark.parametrize("n,length", [(300, 500), (3, 6000), (40, 33)])
+def test_rows_all_of_whose_keys_score_far_below_zero(n, length, tile, hq, hk, d, dtype):
+    """The softmax does not know how far; heads and rows of different distance side by side."""
+    rng = np.random.default_rng(d + tile + n)
+    q, k, v = make(rng, [n], [length], hq, hk, d, dtype, 2.0)
+    scale = d ** -0.5
+    q[:, :, 0] = dev(rng.choice([0, 0.75, 1, 1.25, 2, 30], (n, hq)), dtype)
+    k[:, :, 0] = -177.4 / scale                 # about 2^-256, and further
+    for causal in (False, True):
+        out, lse = cr.convrot_attention(q, k, v, causal=causal, return_lse=True, tile=tile)
+        close(q, k, v, out, lse, scale, causal)
+
+
+@DTYPES
 @pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
 @pytest.mark.parametrize("hq,hk,d", [(1, 1, 8), (3, 3, 16), (4, 2, 40), (5, 1, 64), (2, 1, 72),
                                      (4, 4, 80), (3, 1, 96), (2, 2, 112), (7, 1, 128),
