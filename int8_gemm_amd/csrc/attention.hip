@@ -48,9 +48,10 @@ constexpr float kLift = F16 ? 4.f : 0.f;
 constexpr float kLowest = -3.402823466e38f;
 // Scores start from -m, so those formed below a reference far under zero have only its
 // bits. A first pass takes no reference below kDeepest / c, which leaves a weight right to
-// 2^-14: scores there have none beside any others, and a block with a row that has seen no
-// others goes over its keys again.
+// 2^-14; scores there get none. Beside a reference above kDeep / c they have none, and a
+// row whose reference ends lower, or that has seen nothing above, is gone over again.
 constexpr float kDeepest = -256.f;
+constexpr float kDeep = -192.f;
 // bf16 values may be so large (above 2^96 / keys) that such weights take their sum out of
 // fp32 (half ones, below 2^16, are not). A block in whose result something is not finite,
 // although the sum of the weights is, goes over its keys again with the reference raised at
@@ -89,10 +90,20 @@ __device__ __forceinline__ bool referred(float raise_at) {
 }
 
 // What a wave finds in its rows' results: elements that are not finite though the sum of
-// their weights is, and rows without a reference that see keys.
+// their weights is, and rows that have to be formed exactly. Those are rows with a reference
+// below kDeep or none (m 0) though they see keys.
 struct Found {
-  bool lost, unmet;
+  bool lost;
+  uint64_t inexact;  // rows of the wave
 };
+// The rows, 32 of which two lanes each hold, of which some lane says so.
+__device__ __forceinline__ uint32_t rows_where(bool what) {
+  const uint64_t lanes = __ballot(what);
+  return (uint32_t)lanes | (uint32_t)(lanes >> 32);
+}
+__device__ __forceinline__ bool is_inexact(float mc, float l, bool sees) {
+  return mc < kDeep || (l == 0.f && sees);
+}
 
 template <bool F16>
 __device__ __forceinline__ v16f mfma(const u4& a, const u4& b, const v16f& c) {
@@ -412,13 +423,14 @@ __device__ __forceinline__ U finite_of16(U before, U now) {
 // True if something in it is not finite though its sum is.
 template <int ROWS, int DTILES, bool F16>
 __device__ __forceinline__ bool finish(const AttentionArgs& a, const Tile& t, int row, float l,
-                                       float m, float c, const v16f (&o)[DTILES], bool first) {
+                                       float m, float c, const v16f (&o)[DTILES], bool first,
+                                       bool write) {
   const int half = (thread_anew() >> 5) & 1;
   const float sum = l + other_half(l);
   const bool some = sum > 0.f || sum != sum;
   const float inv = some ? 1.0f / sum : 0.f;
   const float lse2 = some ? log2f(sum) - kLift<F16> + m * c : -__builtin_inff();
-  if (row >= t.rows) return false;
+  if (row >= t.rows || !write) return false;
   float most = 0.f;  // infinite or NaN once something is
   if (Pass<F16>::kAgain) {
 #pragma unroll
@@ -547,11 +559,11 @@ __device__ __forceinline__ void mask(v16f* s, int key0, int seen) {
 // Heads of up to 256: 8192 x 8 heads of 256 in 685 us (0.80 PFLOP/s), one block a compute
 // unit, its output a whole 128 registers a lane.
 // One pass of a wave's 32 rows, from row0 of the block's ROWS on, over the block's keys, U
-// units of 32 at a time.
+// units of 32 at a time. Rows that `only` does not name are not written.
 template <int DP, int NW, bool F16, bool CAUSAL, int ROWS, int U, bool EXACT>
 __device__ __forceinline__ Found walk(const AttentionArgs& a, const Tile& w,
                                       const Pass<F16>& pass, uint8_t* lds, lds_ints flags,
-                                      int tid, int row0) {
+                                      int tid, int row0, uint32_t only) {
   using T = Kernel<DP, NW>;
   const int lane = tid & 63;
   const int wave = wave_number(tid);
@@ -683,16 +695,22 @@ __device__ __forceinline__ Found walk(const AttentionArgs& a, const Tile& w,
         add_nonfinite<T::kDTiles, F16>(a, w.w.k0 + key, w.hk, key < seen, o);
     }
   }
-  const int row = w.row0 + row0 + (thread_anew() & 31);
-  const bool unmet = !EXACT && raise_at < 0.f && l == 0.f && row < w.rows &&
-                     seen > w.t0 * kTileKeys;
-  return {finish<ROWS, T::kDTiles, F16>(a, w, row, l, -below[0], c, o, pass.first()), unmet};
+  const int col_anew = thread_anew() & 31, row = w.row0 + row0 + col_anew;
+  uint32_t inexact = 0;
+  if (!EXACT)
+    inexact = rows_where(row < w.rows && is_inexact(-below[0] * c, l + other_half(l),
+                                                        seen > w.t0 * kTileKeys));
+  return {finish<ROWS, T::kDTiles, F16>(a, w, row, l, -below[0], c, o, pass.first(),
+                                        only >> col_anew & 1),
+          inexact};
 }
 
-// What a block goes over again, QT times 32 rows a wave: everything from the start on
-// (`whole`), or what was lost.
+// What a block goes over again, QT times 32 rows a wave: rows that were inexact, and then,
+// or instead, what was lost. The others stay, so that a row's bits do not depend on those
+// beside it.
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__device__ __forceinline__ void walk_anew(bool whole, uint8_t* lds, lds_ints flags) {
+__device__ __forceinline__ void walk_anew(bool exact, uint64_t rows, uint8_t* lds,
+                                          lds_ints flags) {
   constexpr int kRows = 32 * QT * NW;
   const TileCall call = call_anew<TileCall>();
   const AttentionArgs& a = call.a;
@@ -703,30 +721,31 @@ __device__ __forceinline__ void walk_anew(bool whole, uint8_t* lds, lds_ints fla
   Pass<F16> pass(c);
   bool lost;
   do {
-    if (!whole) pass.again(c);
+    if (!exact) pass.again(c);
     lost = false;
 #pragma unroll 1
     for (int q = 0; q < QT; ++q) {
       if (q > 0) lds_barrier();  // the last tile's reads are done
+      const uint32_t only = exact ? (uint32_t)(rows >> (32 * q)) : ~0u;
       lost |= walk<DP, NW, F16, CAUSAL, kRows, 1, true>(a, w, pass, lds, flags, tid,
-                                                        (wave_number(tid) * QT + q) * 32)
+                                                        (wave_number(tid) * QT + q) * 32, only)
                   .lost;
     }
-    if (!Pass<F16>::kAgain || !whole) return;
-    whole = false;
+    if (!Pass<F16>::kAgain || !exact) return;
+    exact = false;
     note(lost, flags + 1);
     all_noted();
   } while (flags[1]);
 }
 
 template <int DP, int QT, int NW, bool F16, bool CAUSAL>
-__device__ __forceinline__ void finish_block(Found found, uint8_t* lds, lds_ints flags) {
+__device__ __forceinline__ void finish_block(const Found& found, uint8_t* lds, lds_ints flags) {
   note(found.lost, flags + 1);
-  note(found.unmet, flags + 2);
+  note(found.inexact != 0, flags + 2);
   all_noted();
-  const int whole = flags[2];
-  if (__builtin_expect((whole | flags[1]) != 0, 0))
-    walk_anew<DP, QT, NW, F16, CAUSAL>(whole != 0, lds, flags);
+  const int exact = flags[2];
+  if (__builtin_expect((exact | flags[1]) != 0, 0))
+    walk_anew<DP, QT, NW, F16, CAUSAL>(exact != 0, found.inexact, lds, flags);
 }
 
 template <int DP, int NW, bool F16, bool CAUSAL>
@@ -739,7 +758,8 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attention_kernel(Ti
   Tile w;
   if (!locate<T::kRows, CAUSAL>(call, blockIdx.x, &w)) return;
   const Found found = walk<DP, NW, F16, CAUSAL, T::kRows, 2, false>(
-      a, w, Pass<F16>(a.scale * kLog2e), lds, flags, threadIdx.x, wave_number(threadIdx.x) * 32);
+      a, w, Pass<F16>(a.scale * kLog2e), lds, flags, threadIdx.x, wave_number(threadIdx.x) * 32,
+      ~0u);
   finish_block<DP, 1, NW, F16, CAUSAL>(found, lds, flags);
 }
 
@@ -1142,13 +1162,16 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
           add_nonfinite<T::kDTiles, F16>(a, w.w.k0 + key, w.hk, key < seen[q], o[q]);
     }
   }
-  Found found = {false, false};
+  Found found = {false, 0};
 #pragma unroll
   for (int q = 0; q < QT; ++q) {
     const int row = row0 + q * 32 + (thread_anew() & 31);
-    found.unmet |=
-        raise_at[q] < 0.f && l[q] == 0.f && row < w.rows && seen[q] > w.t0 * kTileKeys;
-    found.lost |= finish<T::kRows, T::kDTiles, F16>(a, w, row, l[q], -below[q][0], c, o[q], true);
+    const bool sees = seen[q] > w.t0 * kTileKeys;
+    const bool inexact =
+        row < w.rows && is_inexact(-below[q][0] * c, l[q] + other_half(l[q]), sees);
+    found.inexact |= (uint64_t)rows_where(inexact) << (32 * q);
+    found.lost |=
+        finish<T::kRows, T::kDTiles, F16>(a, w, row, l[q], -below[q][0], c, o[q], true, true);
   }
   finish_block<DP, QT, NW, F16, CAUSAL>(found, lds, flags);
 }
@@ -1257,11 +1280,13 @@ __device__ __forceinline__ bool locate_few(const AttentionArgs& a, uint32_t at, 
   return false;
 }
 
-// One pass over a block's keys; the sums of its waves joined, and written.
+// One pass over a block's keys; the sums of its waves joined, and the rows that `only`
+// names written. True if one of them has an element lost; the second flag takes the rows
+// that were inexact.
 template <int DP, bool F16, bool EXACT>
-__device__ __forceinline__ Found few_pass(const AttentionArgs& a, const FewWork& work,
-                                          uint32_t block, const Pass<F16>& pass, uint8_t* lds,
-                                          int tid) {
+__device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& work,
+                                         uint32_t block, const Pass<F16>& pass, uint8_t* lds,
+                                         int tid, uint32_t only) {
   using T = Few<DP>;
   constexpr int kSteps = DP / 16, kDTiles = DP / 32;
   const int lane = tid & 63;
@@ -1437,10 +1462,10 @@ __device__ __forceinline__ Found few_pass(const AttentionArgs& a, const FewWork&
   lds_barrier();
   const int here = min(32, rows - row0);
   constexpr int kQuads = DP / 4;
-  Found found = {false, false};
+  bool lost = false;
   for (int i = tid; i < here * kQuads; i += 64 * T::kWaves) {
     const int jr = i / kQuads, e = i % kQuads * 4;
-    if (e >= a.d) continue;
+    if (e >= a.d || (EXACT && !(only >> jr & 1))) continue;
     float m = kLowest;
 #pragma unroll
     for (int v = 0; v < T::kWaves; ++v) m = fmaxf(m, stat[v * 64 + jr]);
@@ -1458,15 +1483,17 @@ __device__ __forceinline__ Found few_pass(const AttentionArgs& a, const FewWork&
     }
     if (Pass<F16>::kAgain && total < __builtin_inff()) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) found.lost |= !(__builtin_fabsf(acc[q]) < __builtin_inff());
+      for (int q = 0; q < 4; ++q) lost |= !(__builtin_fabsf(acc[q]) < __builtin_inff());
     }
     const bool some = total > 0.f || total != total;
     const float inv = some ? 1.0f / total : 0.f;
     const float lse2 = some ? log2f(total) - kLift<F16> + m * c : -__builtin_inff();
     const int jtoken = (row0 + jr) / group, jhead = hk * group + (row0 + jr) % group;
-    if (!EXACT)
-      found.unmet |=
-          total == 0.f && (a.causal ? min(w.lk, jtoken + shift) : w.lk) > first * T::kUnit;
+    if (!EXACT) {
+      const bool sees = (a.causal ? min(w.lk, jtoken + shift) : w.lk) > first * T::kUnit;
+      if (__builtin_expect(is_inexact(total == 0.f ? 0.f : m * c, total, sees), 0))
+        atomicOr(reinterpret_cast<int*>(lds + T::kFlag) + 1, 1 << jr);
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[q] *= inv;
     if (a.splits > 1 && e == 0 && work.split == 0) {
@@ -1490,27 +1517,31 @@ __device__ __forceinline__ Found few_pass(const AttentionArgs& a, const FewWork&
                                    (int64_t)jhead * a.out_head_stride + e);
     *to = pass.first() ? f : finite_of16<F16>(*to, f);
   }
-  return found;
+  return lost;
 }
 
 // What a block goes over again, as walk_anew.
 template <int DP, bool F16>
-__device__ __forceinline__ void few_anew(bool whole, uint8_t* lds, lds_ints flags) {
+__device__ __forceinline__ void few_anew(uint32_t rows, uint8_t* lds, lds_ints flags) {
   const AttentionArgs a = call_anew<AttentionArgs>();
   const uint32_t block = block_anew();
   FewWork work;
   if (!locate_few(a, block / (uint32_t)a.k_heads, &work)) return;
   const float c = a.scale * kLog2e;
   Pass<F16> pass(c);
+  bool more = flags[0];
+  bool exact = rows != 0;
   do {
     lds_barrier();  // all have read the flags: the ring takes their place
-    if (!whole) pass.again(c);
-    const Found found = few_pass<DP, F16, true>(a, work, block, pass, lds, thread_anew());
-    if (!Pass<F16>::kAgain || !whole) return;
-    whole = false;
-    note(found.lost, flags);
+    if (!exact) pass.again(c);
+    const bool lost = few_pass<DP, F16, true>(a, work, block, pass, lds, thread_anew(),
+                                              exact ? rows : ~0u);
+    if (!Pass<F16>::kAgain || !exact) return;
+    exact = false;
+    note(lost, flags);
     all_noted();
-  } while (flags[0]);
+    more |= flags[0] != 0;
+  } while (more);
 }
 
 template <int DP, bool F16>
@@ -1518,14 +1549,13 @@ __global__ __launch_bounds__(64 * Few<DP>::kWaves, 1) void attention_few_kernel(
   extern __shared__ __align__(1024) uint8_t lds[];
   FewWork work;
   if (!locate_few(a, blockIdx.x / (uint32_t)a.k_heads, &work)) return;
-  const Found found = few_pass<DP, F16, false>(a, work, blockIdx.x,
-                                               Pass<F16>(a.scale * kLog2e), lds, threadIdx.x);
+  const bool lost = few_pass<DP, F16, false>(
+      a, work, blockIdx.x, Pass<F16>(a.scale * kLog2e), lds, threadIdx.x, ~0u);
   lds_ints flags = (lds_ints)(lds + Few<DP>::kFlag);
-  note(found.lost, flags);
-  note(found.unmet, flags + 1);
+  note(lost, flags);
   all_noted();
-  const int whole = flags[1];
-  if (__builtin_expect((whole | flags[0]) != 0, 0)) few_anew<DP, F16>(whole != 0, lds, flags);
+  const uint32_t inexact = flags[1];
+  if (__builtin_expect((inexact | flags[0]) != 0, 0)) few_anew<DP, F16>(inexact, lds, flags);
 }
 
 // Joins the splits of a row: out = sum_s 2^(lse_s - lse) out_s, with a power of two out of

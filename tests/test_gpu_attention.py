@@ -242,6 +242,41 @@ def test_rows_all_of_whose_keys_score_far_below_zero(n, length, tile, hq, hk, d,
 
 
 @DTYPES
+@pytest.mark.parametrize("tile,hq,hk,d", EACH)
+@pytest.mark.parametrize("level", [-120, -160, -192, -224, -256, -288])
+def test_keys_a_little_below_the_others_far_below_zero(level, tile, hq, hk, d, dtype):
+    """First keys 2 and 6 octaves below the others, all of them `level` octaves below one."""
+    rng = np.random.default_rng(d + tile - level)
+    n, length = 290, 450
+    q, k, v = make(rng, [n], [length], hq, hk, d, dtype, 0.1)
+    q[:, :, 0] = 1
+    octaves = level + np.where(np.arange(length) < 97, -6, np.where(np.arange(length) < 225, -2, 0))
+    k[:, :, 0] = dev(octaves * math.log(2) * d ** 0.5, dtype)[:, None]
+    v[:225] += 4
+    for causal in (False, True):
+        out, lse = cr.convrot_attention(q, k, v, causal=causal, return_lse=True, tile=tile)
+        close(q, k, v, out, lse, d ** -0.5, causal)
+
+
+@DTYPES
+@pytest.mark.parametrize("tile,hq,hk,d", EACH + [(128, 4, 2, 72), (128, 3, 1, 40)])
+@pytest.mark.parametrize("n,length", [(300, 500), (9, 6000)])
+def test_rows_beside_one_that_is_formed_again_keep_their_bits(n, length, tile, hq, hk, d, dtype):
+    rng = np.random.default_rng(d + tile + n)
+    q, k, v = make(rng, [n], [length], hq, hk, d, dtype, 4.0)
+    k[:, :, 0] = -2000
+    q[:, :, 0] = 0
+    for causal in (False, True):
+        want, want_lse = cr.convrot_attention(q, k, v, causal=causal, return_lse=True, tile=tile)
+        other = q.clone()
+        other[7, :, 0] = 16                     # scores of -4000 and less
+        got, lse = cr.convrot_attention(other, k, v, causal=causal, return_lse=True, tile=tile)
+        rest = [i for i in range(n) if i != 7]
+        assert torch.equal(got[rest], want[rest]) and torch.equal(lse[:, rest], want_lse[:, rest])
+        assert (lse[:, 7] < -1000).all()
+
+
+@DTYPES
 @pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
 @pytest.mark.parametrize("hq,hk,d", [(1, 1, 8), (3, 3, 16), (4, 2, 40), (5, 1, 64), (2, 1, 72),
                                      (4, 4, 80), (3, 1, 96), (2, 2, 112), (7, 1, 128),
