@@ -91,7 +91,9 @@ __device__ __forceinline__ bool referred(float raise_at) {
 
 // What a wave finds in its rows' results: elements that are not finite though the sum of
 // their weights is, and rows that have to be formed exactly. Those are rows with a reference
-// below kDeep or none (m 0) though they see keys.
+// below kDeep or none (m 0) though they see keys, and, where the head is padded, rows whose
+// sum is NaN: the chunks behind the head's end repeat its last one in LDS, and an infinity
+// there met the query's zeros. An exact pass takes zeros for them.
 struct Found {
   bool lost;
   uint64_t inexact;  // rows of the wave
@@ -101,8 +103,14 @@ __device__ __forceinline__ uint32_t rows_where(bool what) {
   const uint64_t lanes = __ballot(what);
   return (uint32_t)lanes | (uint32_t)(lanes >> 32);
 }
-__device__ __forceinline__ bool is_inexact(float mc, float l, bool sees) {
-  return mc < kDeep || (l == 0.f && sees);
+template <int DP>
+__device__ __forceinline__ bool is_inexact(float mc, float l, bool sees, int d) {
+  return mc < kDeep || (l == 0.f && sees) || (d < DP && l != l);
+}
+// Elements from 8 chunk on of a head of d.
+__device__ __forceinline__ u4 inside_head(const u4& w, int chunk, int d) {
+  const u4 zero = {0, 0, 0, 0};
+  return chunk * 8 < d ? w : zero;
 }
 
 template <bool F16>
@@ -622,7 +630,7 @@ __device__ __forceinline__ Found walk(const AttentionArgs& a, const Tile& w,
             const int r = (u0 + u) * 32 + col;
             const u4 kf = *reinterpret_cast<const u4*>(kt + r * T::kRowBytes +
                                                        k_slot<DP>(r, 2 * st + half) * 16);
-            s[u] = mfma<F16>(kf, qf[st], s[u]);
+            s[u] = mfma<F16>(EXACT ? inside_head(kf, 2 * st + half, a.d) : kf, qf[st], s[u]);
           }
           if (masked) mask(&s[u], t * kTileKeys + (u0 + u) * 32, seen);
         }
@@ -698,8 +706,8 @@ __device__ __forceinline__ Found walk(const AttentionArgs& a, const Tile& w,
   const int col_anew = thread_anew() & 31, row = w.row0 + row0 + col_anew;
   uint32_t inexact = 0;
   if (!EXACT)
-    inexact = rows_where(row < w.rows && is_inexact(-below[0] * c, l + other_half(l),
-                                                        seen > w.t0 * kTileKeys));
+    inexact = rows_where(row < w.rows && is_inexact<DP>(-below[0] * c, l + other_half(l),
+                                                        seen > w.t0 * kTileKeys, a.d));
   return {finish<ROWS, T::kDTiles, F16>(a, w, row, l, -below[0], c, o, pass.first(),
                                         only >> col_anew & 1),
           inexact};
@@ -1168,7 +1176,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
     const int row = row0 + q * 32 + (thread_anew() & 31);
     const bool sees = seen[q] > w.t0 * kTileKeys;
     const bool inexact =
-        row < w.rows && is_inexact(-below[q][0] * c, l[q] + other_half(l[q]), sees);
+        row < w.rows && is_inexact<DP>(-below[q][0] * c, l[q] + other_half(l[q]), sees, a.d);
     found.inexact |= (uint64_t)rows_where(inexact) << (32 * q);
     found.lost |=
         finish<T::kRows, T::kDTiles, F16>(a, w, row, l[q], -below[q][0], c, o[q], true, true);
@@ -1367,7 +1375,7 @@ __device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& 
       for (int st = 0; st < kSteps; ++st) {
         const u4 kf = *reinterpret_cast<const u4*>(kt + col * T::kRowBytes +
                                                    k_slot<DP>(col, 2 * st + half) * 16);
-        s = mfma<F16>(kf, qf[st], s);
+        s = mfma<F16>(EXACT ? inside_head(kf, 2 * st + half, a.d) : kf, qf[st], s);
       }
       if (key0 + T::kUnit > full) mask(&s, key0, seen);
       top = s[0];
@@ -1491,7 +1499,7 @@ __device__ __forceinline__ bool few_pass(const AttentionArgs& a, const FewWork& 
     const int jtoken = (row0 + jr) / group, jhead = hk * group + (row0 + jr) % group;
     if (!EXACT) {
       const bool sees = (a.causal ? min(w.lk, jtoken + shift) : w.lk) > first * T::kUnit;
-      if (__builtin_expect(is_inexact(total == 0.f ? 0.f : m * c, total, sees), 0))
+      if (__builtin_expect(is_inexact<DP>(total == 0.f ? 0.f : m * c, total, sees, a.d), 0))
         atomicOr(reinterpret_cast<int*>(lds + T::kFlag) + 1, 1 << jr);
     }
 #pragma unroll

@@ -419,6 +419,32 @@ def test_keys_that_the_mask_hides_have_no_part(hq, hk, d, n, length, tile, what,
 
 
 @DTYPES
+@pytest.mark.parametrize("tile,hq,hk,d", [
+    (256, 4, 2, 72), (256, 2, 2, 96), (256, 2, 1, 128), (128, 4, 2, 80), (128, 2, 2, 120),
+    (128, 3, 1, 8), (128, 3, 1, 40), (128, 1, 1, 64), (128, 1, 1, 136), (128, 2, 1, 192),
+    (128, 1, 1, 256), (32, 4, 2, 72), (32, 3, 1, 40), (32, 2, 1, 160), (32, 2, 1, 128)])
+def test_an_infinite_key_that_is_seen(tile, hq, hk, d, dtype):
+    """A score of -infinity has no weight, wherever in the head the infinity stands; one of
+    +infinity leaves no result."""
+    rng = np.random.default_rng(d)
+    n, length, at = 300, 500, 77
+    q, k, v = make(rng, [n], [length], hq, hk, d, dtype)
+    keep = [j for j in range(length) if j != at]
+    for col in (d - 1, d - 8, 0):
+        q[:, :, col] = q[:, :, col].abs() + 0.125
+        x = k.clone()
+        x[at, :, col] = -math.inf
+        out, lse = cr.convrot_attention(q, x, v, return_lse=True, tile=tile)
+        close(q, k[keep], v[keep], out, lse, d ** -0.5, False)
+        # causal rows all see it
+        out, lse = cr.convrot_attention(q, x, v, causal=True, return_lse=True, tile=tile)
+        close(q, k[keep], v[keep], out, lse, d ** -0.5, True)
+        x[at, :, col] = math.inf
+        out, lse = cr.convrot_attention(q, x, v, return_lse=True, tile=tile)
+        assert out.isnan().all() and not lse.isfinite().any()
+
+
+@DTYPES
 @pytest.mark.parametrize("hq,hk,d,n,length,tile", [
     (2, 2, 128, 200, 70, 128), (4, 2, 64, 90, 300, 0), (2, 1, 256, 70, 129, 0),
     (2, 2, 128, 3, 33, 32),
