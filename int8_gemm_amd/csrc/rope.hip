@@ -121,7 +121,7 @@ struct Place {
   }
 };
 
-// The lane's 8 (cos, sin), (1, 0) where it turns nothing.
+// The lane's 8 (cos, sin), anything where it turns nothing.
 template <bool HALVES>
 __device__ __forceinline__ void load_turns(const HeadsArgs& a, const Place<HALVES>& pl,
                                            int64_t token, float (&cs)[8], float (&sn)[8]) {
@@ -144,16 +144,19 @@ __device__ __forceinline__ void load_turns(const HeadsArgs& a, const Place<HALVE
   }
 }
 
+// Elements that are not rotated stay as they are: (1, 0) would make a NaN of the neighbour of
+// an infinity, and lose the sign of a zero.
 template <bool HALVES>
-__device__ __forceinline__ void turn(float (&v)[2][8], const float (&cs)[8],
-                                     const float (&sn)[8]) {
+__device__ __forceinline__ void turn(float (&v)[2][8], const Place<HALVES>& pl,
+                                     const float (&cs)[8], const float (&sn)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    const bool turned = HALVES || e < 4 ? pl.turn0 : pl.turn1;
     float& x = HALVES ? v[0][e] : v[e >> 2][2 * (e & 3)];
     float& y = HALVES ? v[1][e] : v[e >> 2][2 * (e & 3) + 1];
     const float p = x, q = y;
-    x = __builtin_fmaf(p, cs[e], -(q * sn[e]));
-    y = __builtin_fmaf(q, cs[e], p * sn[e]);
+    x = turned ? __builtin_fmaf(p, cs[e], -(q * sn[e])) : p;
+    y = turned ? __builtin_fmaf(q, cs[e], p * sn[e]) : q;
   }
 }
 
@@ -375,7 +378,7 @@ __global__ __launch_bounds__(ROW ? 64 * kMaxRowWaves : kHeadThreads) void heads_
         for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
       }
     }
-    if (a.table) turn<HALVES>(v, cs, sn);
+    if (a.table) turn<HALVES>(v, pl, cs, sn);
     uint16_t* o = x.out + token * x.out_stride + (int64_t)head * x.out_head_stride;
     if (live && in[i][0]) *reinterpret_cast<u4*>(o + pl.c0 * 8) = pack8<F16>(v[0]);
     if (live && in[i][1]) *reinterpret_cast<u4*>(o + pl.c1 * 8) = pack8<F16>(v[1]);

@@ -167,6 +167,34 @@ def test_in_place_in_a_fused_projection(span, halves):
         assert torch.equal(whole[:, 16:], before[:, 16:])      # v
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("halves", [False, True], ids=["neighbours", "halves"])
+@pytest.mark.parametrize("heads,d,pairs", [(3, 64, 8), (3, 64, 16), (1, 128, 24), (5, 72, 32),
+                                           (40, 128, 40), (2, 256, 64), (2, 40, 16)])
+def test_elements_behind_the_pairs_stay(heads, d, pairs, halves, dtype):
+    """Without a norm they are what they were, infinities, NaN and the sign of a zero too,
+    whatever lies beside them."""
+    rng = np.random.default_rng(d + pairs)
+    tokens = 70
+    x = rng.standard_normal((tokens, heads, d))
+    tail = x[..., 2 * pairs:]
+    kind = rng.integers(0, 6, tail.shape)
+    for i, what in enumerate((np.inf, -np.inf, np.nan, -0.0, 0.0)):
+        tail[kind == i] = what
+    q = dev(x, dtype)
+    angle = rng.random((tokens, pairs)) * 6
+    table = dev(np.stack((np.cos(angle), np.sin(angle)), -1), torch.float32)
+    got, _ = cr.convrot_qk_norm_rope(q, table=table, norm=None, halves=halves)
+    want = ref.rotate(f64(q)[..., :2 * pairs], f64(table), halves)
+    head = f64(got)[..., :2 * pairs]
+    assert (np.abs(head - want) <= H16[dtype][0] * np.abs(want) + 8 * U * np.abs(x).max(
+        where=np.isfinite(x), initial=0)).all()
+    a, b = (t[..., 2 * pairs:].contiguous() for t in (got, q))
+    some = ~b.isnan()
+    assert torch.equal(a[some].view(torch.int16), b[some].view(torch.int16))
+    assert a[~some].isnan().all()
+
+
 def test_other_layouts():
     rng = np.random.default_rng(6)
     dt, t, h, d = torch.bfloat16, 20, 6, 64
