@@ -575,9 +575,10 @@ convrot_status convrot_norm_residual(const convrot_norm_args* args, void* stream
  *   the product with v (few rows: to twice its bits), whose finite values may have
  *   any magnitude. Results are the same bits from run to run and on any number of
  *   compute units.
- *   workspace (256-byte aligned, convrot_attention_workspace_size bytes, nullable
- *   where that is 0) holds the parts of calls with few queries, whose keys are
- *   split over the card; with less, a call splits less, and sums in another order.
+ *   workspace (256-byte aligned, convrot_attention_workspace_size bytes) holds the
+ *   parts of calls whose keys are split over the card: those with few queries, and
+ *   the last round of larger ones. With less, down to none (null), a call splits
+ *   less, and sums in another order.
  *   k and v tokens are at most 2^22 elements apart. scale > 0. tile, a test / tuning
  *   hook: 0 = automatic, 32 (the kernel for few rows), 128 or, for 64 < d <= 128, 256
  *   = rows (query, head of a group) of a block. */

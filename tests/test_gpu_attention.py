@@ -548,6 +548,22 @@ def test_a_last_round_that_is_split(dtype):
                   d ** -0.5, False)
 
 
+@pytest.mark.parametrize("n,length,hq,hk,tile", [(2200, 2100, 33, 33, 256), (700, 4000, 2, 2, 128),
+                                                 (1, 9000, 8, 2, 0)])
+def test_no_workspace(n, length, hq, hk, tile):
+    """A call that asks for one does without: no keys are split."""
+    rng = np.random.default_rng(14)
+    q, k, v = make(rng, [n], [length], hq, hk, 128, torch.bfloat16, 3.0)
+    assert cr.convrot_attention_workspace_size(q, k, v, tile=tile) > 0
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    assert none.data_ptr() == 0
+    out, lse = cr.convrot_attention(q, k, v, return_lse=True, tile=tile, workspace=none)
+    for h in (0, hq - 1):
+        g = h // (hq // hk)
+        close(q[:, h:h + 1], k[:, g:g + 1], v[:, g:g + 1], out[:, h:h + 1], lse[h:h + 1],
+              128 ** -0.5, False)
+
+
 @DTYPES
 def test_many_sequences(dtype):
     """More than a wave's worth of sequences, some empty."""
