@@ -13,6 +13,12 @@
 // the layout of the second product's operand as it is: O^T += V^T P^T, whose
 // contraction takes keys in the order in which the first product's result has
 // them. V^T comes from LDS through the transposing reads.
+//
+// That rounding of the weights is half a step of the inputs' type each, as v's own was
+// (their sum is taken before, in fp32): the output is off by 0.0023 of its norm in bf16 for
+// 0.0017 of one that is rounded once. A second 16-bit part of each weight takes half as many
+// products again, which is what bounds these kernels; the one for few rows waits for memory
+// and carries it.
 
 #include <type_traits>
 #include <utility>
@@ -57,7 +63,8 @@ constexpr float kDeep = -192.f;
 // although the sum of the weights is, goes over its keys again with the reference raised at
 // every larger score and 2^32 above it, so that no row's weights sum to more than 1: the
 // elements that are finite then replace those that were not, the others stay. Looking costs
-// an instruction for two elements of the result and a barrier.
+// an instruction for two elements of the result and a barrier; 4608 x 4608 x 30 heads take 310
+// us, with an infinite value that every row sees 850, with every row formed exactly 710.
 constexpr float kOver = 32.f;
 constexpr float kMostOver = 1e36f;  // finite where the scale is next to nothing
 template <bool F16>
@@ -560,12 +567,13 @@ __device__ __forceinline__ void mask(v16f* s, int key0, int seen) {
 // Two 64-key tiles of K and V in LDS, one in use and one on its way. Heads of 65 to 128
 // elements run two blocks a compute unit, so that one block's start, softmax and end lie
 // under the other's products: the better choice for keys of a few tiles and for rows that
-// do not fill the card with 256 (16384 queries x 40 heads of 128 over 256 keys: 142 us, with
-// 256 rows a block 175; over 4608: 1457 and 1331). 32760 x 40 heads over 512 keys take 424 us,
-// 0.81 PFLOP/s: of a round's 21 us 6.5 are a block's start and end, and the MFMAs are
-// busy 0.37 of the cycles at 2.0 GHz (power: fetching the next tile early gains nothing).
-// Heads of up to 256: 8192 x 8 heads of 256 in 685 us (0.80 PFLOP/s), one block a compute
-// unit, its output a whole 128 registers a lane.
+// do not fill the card with 256 (16384 queries x 40 heads of 128 over 256 keys: 143 us, with
+// 256 rows a block 180; over 4608: 1410 and 1333). 32760 x 40 heads over 512 keys take 430 us,
+// 0.80 PFLOP/s: of a round's 21 us 6.5 are a block's start and end, and the MFMAs are
+// busy 0.40 of the cycles at 2.0 GHz (power: fetching the next tile early gains nothing).
+// Heads of up to 256: 8192 x 8 heads of 256 in 708 us (0.78 PFLOP/s), one block a compute
+// unit, its output a whole 128 registers a lane: a SIMD has one wave, whose products, softmax
+// and products follow one another, and the MFMAs are busy 0.32 of the cycles at 2.1 GHz.
 // One pass of a wave's 32 rows, from row0 of the block's ROWS on, over the block's keys, U
 // units of 32 at a time. Rows that `only` does not name are not written.
 template <int DP, int NW, bool F16, bool CAUSAL, int ROWS, int U, bool EXACT>
@@ -832,16 +840,18 @@ __device__ __forceinline__ void settle_vec(v16f (&s)[N]) {
 // read serves both of a wave's 32-row halves.
 //
 // Heads of 65 to 128 elements: 256 rows a block, one wave a SIMD with the output in
-// accumulation registers. 32760 x 32760 x 40 heads of 128 take 17.9 to 18.5 ms, 1.2
-// PFLOP/s, bound by power: the clock falls to 1.83 GHz with the MFMAs busy 0.59 of the
-// cycles, and on zeros the same instructions reach 1.51 PFLOP/s. 4.8 vector instructions
+// accumulation registers. 32760 x 32760 x 40 heads of 128 take 18.1 to 18.9 ms, 1.16 to 1.21
+// PFLOP/s, bound by power: the clock falls to 1.86 GHz with the MFMAs busy 0.58 of the
+// cycles, and on zeros the same instructions reach 1.51 PFLOP/s. 4.9 vector instructions
 // a score; no bank conflicts. Eight waves of 32 rows take twice the LDS reads: 1.53
 // PFLOP/s on zeros, 1.14 on random values (this: 1.21 then). Causal, 16384 x 16384 x 16
-// heads: 0.94 ms (1.17 PFLOP/s of the scores that count).
+// heads: 0.93 to 0.96 ms (1.15 to 1.19 PFLOP/s of the scores that count).
 //
 // Heads of up to 64: 128 rows a block, 32 a wave, the output beside the scores, three waves
 // a SIMD; half the products a score, so bound by vector instructions and their latency.
-// 16384 x 16384 x 16 heads of 64: 1.11 ms (0.99 PFLOP/s), the kernel above 1.18.
+// 16384 x 16384 x 16 heads of 64: 1.12 to 1.17 ms (0.94 to 0.98 PFLOP/s), the kernel above
+// 1.18 where this takes 1.12. At 5060 x 5060 x 32 heads, causal, vector instructions issue in
+// 0.79 of the busy cycles (the MFMAs 0.47) and the compute units are busy 0.78 of the time.
 template <int DP, int QT, int NW>
 struct Wide {
   static constexpr int kWaves = NW;
@@ -1191,8 +1201,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 1) void attention_wide_kern
 // waits for no other wave until the end, where the waves' sums are joined. Weights
 // go into the second product in two 16-bit parts, which costs nothing here.
 //
-// One token of 32 / 4 heads of 128 against 100000 keys streams at 4.7 TB/s, 32 caches of
-// 4096 keys at 4.9 (a large copy: 4.9); 12 caches of 1 to 8192 used keys take 48 us, 4.7 of
+// One token of 32 / 4 heads of 128 against 100000 keys streams at 4.5 TB/s, 32 caches of
+// 4096 keys at 5.0 (a large copy: 4.9); 12 caches of 1 to 8192 used keys take 48 us, 4.8 of
 // them the second launch, which joins the parts; blocks cut by the room of the caches took
 // 64.
 template <int DP>
@@ -1802,7 +1812,7 @@ size_t workspace_bytes(const AttentionPlan& p, int d) {
 // A kernel's blocks on a full card (256 compute units; a constant, as the split decides
 // the order of sums): `room` at a time, a round of which takes `tile` us per key tile and
 // `start` us beside. Fitted to 16384 queries x 40 heads of 128 over 256 to 4608 keys
-// (10 rounds; measured 142 to 1457 us with 128 rows a block, 175 to 1331 us with 256),
+// (10 rounds; measured 143 to 1410 us with 128 rows a block, 180 to 1333 us with 256),
 // 48 heads of 64 and 16 of 256 alike.
 // In a round of at most half its blocks, those of a kernel that runs two a compute unit
 // have one to themselves and take 0.62 of the time.
